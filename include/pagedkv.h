@@ -86,6 +86,7 @@ enum {
 #define PKV_DEV_ERR_QLEN 8    /* kv length shorter than the query length            */
 #define PKV_DEV_ERR_TIMEOUT 16 /* a bounded pipeline wait gave up; output invalid   */
 #define PKV_DEV_ERR_LEN 32    /* a length exceeds the stated maximum; it is clamped  */
+#define PKV_DEV_ERR_SCALE 128 /* a block scale outside [2^-48, 2^48]; it is clamped  */
 #define PKV_DEV_ERR_BOUNDS 64 /* debug build only: a derived offset left its buffer  */
 
 /* Human-readable name of a pkv_status value (static string). */
@@ -187,6 +188,50 @@ int paged_append(const void *append_key, const void *append_value, int64_t nnz,
                  int32_t batch_size, int32_t num_kv_heads, int32_t head_dim,
                  int32_t page_size, int32_t layout, int32_t dtype,
                  int32_t *err_word, void *stream);
+
+/*
+ * paged_append_scaled -- paged_append into an E4M3 cache with one fp32 scale
+ * for each block of scale_block tokens and head, K and V apart: the element
+ * of (page, head, slot, d) stands for its E4M3 value times
+ *   scales[page * scale_page_stride + head * (page_size / scale_block)
+ *          + slot / scale_block].
+ * The new tokens are 16-bit (dtype PKV_F16 or PKV_BF16) and are quantised
+ * here.  Every block that gets new tokens takes the scale
+ *   s' = max(s, 2^e) if it holds earlier tokens (slots before its first new
+ *        token; s is the scale it has), else 2^e,
+ *   e  = the smallest whole number in [-40, 40] with |x| <= 448 * 2^e for
+ *        every finite new value x of the block and head;
+ * new values become e4m3(x / s') and, where s' > s, earlier ones
+ * e4m3(c * (s / s')), both rounded to nearest even; beyond 448 s' (with
+ * infinities) a value becomes the largest of its sign, NaN stays NaN.  With
+ * scales that are powers of two all of this is exact but for the rounding to
+ * E4M3 itself, so the result does not depend on how the work is divided.
+ * Slots after a block's last new token keep their codes; blocks without new
+ * tokens keep their scale; no other byte is written.
+ *  - The entries of one request that fall into one block have consecutive
+ *    positions and follow one another in batch_indices / positions (as
+ *    paged_batch_indices_positions gives them).  An entry that breaks this
+ *    next to its predecessor (same request and block, position not one
+ *    higher) sets PKV_DEV_ERR_POS and its run is skipped; entries of one
+ *    block further apart race, as duplicates do.  Two requests must not
+ *    append to one shared page.
+ *  - page_size a power of two in [8, 256]; scale_block a power of two in
+ *    [8, page_size]; head_dim a multiple of 16; page_stride in E4M3 elements,
+ *    a multiple of 16; scale_page_stride in floats, at least
+ *    num_kv_heads * (page_size / scale_block).
+ * Device errors as paged_append (BATCH, POS, PAGE: the entry is skipped);
+ * an earlier scale outside [2^-48, 2^48] sets PKV_DEV_ERR_SCALE and is
+ * brought into that range.
+ */
+int paged_append_scaled(const void *append_key, const void *append_value, int64_t nnz,
+                        const int32_t *batch_indices, const int32_t *positions,
+                        void *k_cache, void *v_cache, int64_t page_stride,
+                        int64_t max_num_pages, float *k_scales, float *v_scales,
+                        int64_t scale_page_stride, int32_t scale_block,
+                        const int32_t *kv_indices, const int32_t *kv_indptr,
+                        const int32_t *kv_last_page_len, int32_t batch_size,
+                        int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                        int32_t layout, int32_t dtype, int32_t *err_word, void *stream);
 
 /*
  * paged_decode_workspace_size -- bytes of device workspace paged_decode needs
@@ -300,6 +345,57 @@ int paged_decode_ex(const void *query, int64_t num_tokens, const void *k_cache,
                     int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
                     int32_t page_size, int32_t layout, int32_t dtype, int32_t enable_pdl,
                     void *out, float *lse, int32_t *err_word, void *stream);
+
+/*
+ * paged_decode_window_workspace_size -- paged_decode_workspace_size for
+ * paged_decode_window: the longest request's visible keys are then at most
+ * window_left + q_len_per_req + first_tokens (in whole 64-key tiles).
+ */
+size_t paged_decode_window_workspace_size(int32_t batch_size, int32_t q_len_per_req,
+                                          int32_t num_qo_heads, int32_t num_kv_heads,
+                                          int32_t head_dim, int32_t max_seq_len,
+                                          int32_t page_size, int32_t window_left,
+                                          int32_t first_tokens);
+
+/*
+ * paged_decode_window -- paged_decode_ex with two additions: a few first
+ * tokens that stay visible under a window, and an E4M3 cache with one scale
+ * for each block of tokens and head.
+ *  - first_tokens (>= 0): with window_left >= 0 the query at position p sees
+ *    key j iff j <= p and (j >= p - window_left or j < first_tokens).  With
+ *    window_left = -1 every key j <= p is visible and first_tokens has no
+ *    effect.  Keys that no query of a request sees, from first_tokens to
+ *    L - Q - window_left - 1, are not read, nor are the block-table entries
+ *    of pages that hold only such keys: those pages may have been freed.
+ *  - k_scales / v_scales NULL and scale_block 0: no block scales.  Otherwise
+ *    dtype is PKV_F16_E4M3 or PKV_BF16_E4M3 and the element of (page, head,
+ *    slot, d) stands for its E4M3 value times
+ *      scales[page * scale_page_stride + head * (page_size / scale_block)
+ *             + slot / scale_block],
+ *    fp32; scale_block is a power of two in [8, page_size] and
+ *    scale_page_stride (floats) >= num_kv_heads * (page_size / scale_block).
+ *    A scale is a positive number in [2^-48, 2^48]; one outside (0, negative
+ *    or NaN included) sets PKV_DEV_ERR_SCALE and is brought into that range
+ *    (NaN to 2^-48).  bmm1_scale and bmm2_scale apply on top.
+ *  - workspace: >= paged_decode_window_workspace_size(...) bytes, 256-byte
+ *    aligned; calls that may overlap on the GPU take one each.
+ * Everything else, including errors, is as paged_decode_ex (cum_seq_lens_q
+ * NULL: max_q_len tokens for every request).
+ */
+int paged_decode_window(const void *query, int64_t num_tokens, const void *k_cache,
+                        const void *v_cache, int64_t page_stride, int64_t max_num_pages,
+                        const float *k_scales, const float *v_scales,
+                        int64_t scale_page_stride, int32_t scale_block, void *workspace,
+                        size_t workspace_bytes, const int32_t *block_tables,
+                        int32_t block_table_stride, const uint32_t *seq_lens,
+                        int32_t batch_size, int32_t max_seq_len, float bmm1_scale,
+                        float bmm2_scale, const float *bmm1_scale_dev,
+                        const float *bmm2_scale_dev, int32_t window_left,
+                        int32_t first_tokens, const float *sinks, int32_t max_q_len,
+                        const int32_t *cum_seq_lens_q, int32_t num_qo_heads,
+                        int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                        int32_t layout, int32_t dtype, int32_t enable_pdl, void *out,
+                        float *lse, int32_t *err_word, void *stream);
 
 /*
  * paged_decode_noalloc -- paged_decode without a caller workspace.  The API

@@ -12,6 +12,7 @@ from .binding import (  # noqa: F401
     paged_seq_lens,
     paged_batch_indices_positions,
     paged_append,
+    paged_append_scaled,
     paged_decode_workspace_size,
     paged_decode,
     paged_decode_noalloc,

@@ -50,6 +50,12 @@ _SIGNATURES = {
     "paged_decode_noalloc": ([_c_p, _c_p, _c_p, _i64, _i64, _c_p, _i32, _c_p, _i32, _i32,
                               _f32, _f32, _i32, _c_p, _i32, _i32, _i32, _i32, _i32, _i32,
                               _i32, _c_p, _c_p, _c_p, _c_p], ctypes.c_int),
+    "paged_append_scaled": ([_c_p, _c_p, _i64, _c_p, _c_p, _c_p, _c_p, _i64, _i64, _c_p, _c_p, _i64, _i32,
+                             _c_p, _c_p, _c_p, _i32, _i32, _i32, _i32, _i32, _i32, _c_p, _c_p], ctypes.c_int),
+    "paged_decode_window_workspace_size": ([_i32] * 9, _sz),
+    "paged_decode_window": ([_c_p, _i64, _c_p, _c_p, _i64, _i64, _c_p, _c_p, _i64, _i32, _c_p, _sz, _c_p, _i32,
+                             _c_p, _i32, _i32, _f32, _f32, _c_p, _c_p, _i32, _i32, _c_p, _i32, _c_p, _i32, _i32,
+                             _i32, _i32, _i32, _i32, _i32, _c_p, _c_p, _c_p, _c_p], ctypes.c_int),
     "paged_prefill_workspace_size": ([_i32] * 4, _sz),
     "paged_prefill": ([_c_p, _i64, _c_p, _c_p, _i64, _i64, _i64, _f32, _c_p, _sz, _i32,
                        _i32, _c_p, _c_p, _c_p, _i32, _i32, _i32, _i32, _i32, _i32,
@@ -194,6 +200,40 @@ def base_dtype(kv_cache) -> torch.dtype:
     return (kv_cache[0] if isinstance(kv_cache, (tuple, list)) else kv_cache).dtype
 
 
+def split_scales(kv_scales, num_pages: int, num_heads: int, page_size: int, device):
+    """(k_ptr, v_ptr, page stride, block) of the block scales of an E4M3
+    cache: one float32 tensor [pages, 2, heads, page_size // block] or a
+    (k, v) tuple of [pages, heads, page_size // block]."""
+    if isinstance(kv_scales, (tuple, list)):
+        k, v = kv_scales
+        if k.shape != v.shape or k.stride(0) != v.stride(0):
+            raise PagedKVError("K and V scales must have the same shape and page stride")
+    else:
+        if kv_scales.dim() != 4 or kv_scales.shape[1] != 2:
+            raise PagedKVError("a single kv_scales tensor must be [pages, 2, heads, blocks]")
+        k, v = kv_scales[:, 0], kv_scales[:, 1]
+    if k.dim() != 3 or k.shape[0] != num_pages or k.shape[1] != num_heads or k.shape[2] < 1 \
+            or page_size % k.shape[2]:
+        raise PagedKVError(f"scales must be [{num_pages}, {num_heads}, page_size // block] for each of K and V")
+    for t in (k, v):
+        if t.dtype != torch.float32 or t.device != device:
+            raise PagedKVError("scales are float32 on the cache's device")
+        if t.stride(2) != 1 and t.shape[2] > 1 or t.stride(1) != t.shape[2] and t.shape[1] > 1:
+            raise PagedKVError("the scales of a page must be contiguous")
+    n = num_heads * k.shape[2]
+    stride = k.stride(0) if num_pages > 1 else max(n, k.stride(0))
+    return _ptr(k), _ptr(v), stride, page_size // k.shape[2]
+
+
+def _same_device(*tensors):
+    """All given tensors live on the current CUDA device: the library
+    launches there."""
+    here = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != here):
+            raise PagedKVError("tensor arguments must live on the current CUDA device")
+
+
 # ---- index helpers ------------------------------------------------------------------
 
 def paged_seq_lens(kv_indptr, kv_last_page_len, page_size: int, seq_lens=None,
@@ -244,6 +284,48 @@ def paged_append(append_key, append_value, batch_indices, positions, paged_kv_ca
         _dtype_code(append_key), _ptr(err_word), _stream(stream)))
 
 
+def paged_append_scaled(append_key, append_value, batch_indices, positions, paged_kv_cache, kv_scales,
+                        kv_indices, kv_indptr, kv_last_page_len, kv_layout="NHD", err_word=None,
+                        stream=None) -> None:
+    """Append 16-bit tokens to an E4M3 cache with one power-of-two scale for
+    each block of tokens and head.  kv_scales (float32, updated in place):
+    [pages, 2, heads, page_size // block] or a (K, V) tuple of [pages, heads,
+    page_size // block]; an element stands for its E4M3 value times its
+    block's scale.  A block that gets tokens takes the larger of its scale
+    (if it holds earlier tokens) and the smallest power of two under which the
+    new values fit; earlier values of a block whose scale grew are rounded
+    again.  The entries of one request and block have consecutive positions
+    and follow one another, as paged_batch_indices_positions gives them."""
+    layout = _layout_code(kv_layout)
+    kp, vp, stride, P, H, S, D, base = split_cache(paged_kv_cache, layout)
+    nnz = append_key.shape[0]
+    if not (append_key.is_contiguous() and append_value.is_contiguous()):
+        raise PagedKVError("append_key/append_value must be contiguous")
+    if append_value.shape != append_key.shape or tuple(append_key.shape[1:]) != (H, D):
+        raise PagedKVError(f"append_key/append_value must both be [nnz, {H}, {D}]")
+    if base_dtype(paged_kv_cache) != torch.float8_e4m3fn:
+        raise PagedKVError("the cache holds float8_e4m3fn")
+    dtype = _dtype_code(append_key)
+    if dtype not in (F16, BF16) or append_value.dtype != append_key.dtype:
+        raise PagedKVError("append_key/append_value are both fp16 or both bf16")
+    for t in (batch_indices, positions):
+        if t.dtype != torch.int32 or t.numel() < nnz or not t.is_contiguous():
+            raise PagedKVError(f"batch_indices/positions must be contiguous int32 with >= {nnz} entries")
+    B = kv_last_page_len.shape[0]
+    for t in (kv_indices, kv_indptr, kv_last_page_len):
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise PagedKVError("kv_indices/kv_indptr/kv_last_page_len must be contiguous int32")
+    if kv_indptr.numel() != B + 1:
+        raise PagedKVError(f"kv_indptr must have {B + 1} entries")
+    ks, vs, ss, block = split_scales(kv_scales, P, H, S, base.device)
+    _same_device(base, append_key, append_value, batch_indices, positions, kv_indices, kv_indptr,
+                 kv_last_page_len, err_word)
+    _check(load_library().paged_append_scaled(
+        _ptr(append_key), _ptr(append_value), nnz, _ptr(batch_indices), _ptr(positions), kp, vp, stride, P,
+        ks, vs, ss, block, _ptr(kv_indices), _ptr(kv_indptr), _ptr(kv_last_page_len), B, H, D, S, layout, dtype,
+        _ptr(err_word), _stream(stream)))
+
+
 # ---- decode -------------------------------------------------------------------------------
 
 def _scale_arg(scale, device):
@@ -257,7 +339,11 @@ def _scale_arg(scale, device):
 
 
 def paged_decode_workspace_size(batch_size, q_len_per_req, num_qo_heads, num_kv_heads,
-                                head_dim, max_seq_len, page_size, window_left=-1) -> int:
+                                head_dim, max_seq_len, page_size, window_left=-1, first_tokens=0) -> int:
+    if first_tokens:
+        return int(load_library().paged_decode_window_workspace_size(
+            batch_size, q_len_per_req, num_qo_heads, num_kv_heads, head_dim,
+            max_seq_len, page_size, window_left, first_tokens))
     return int(load_library().paged_decode_workspace_size(
         batch_size, q_len_per_req, num_qo_heads, num_kv_heads, head_dim,
         max_seq_len, page_size, window_left))
@@ -289,14 +375,18 @@ def paged_decode(query, kv_cache, workspace, block_tables, seq_lens, max_seq_len
                  bmm1_scale: float = 1.0, bmm2_scale: float = 1.0, window_left: int = -1,
                  sinks=None, kv_layout="HND", q_len_per_req: int = 1, out=None,
                  lse=None, err_word=None, stream=None, max_q_len=None, cum_seq_lens_q=None,
-                 enable_pdl=None):
+                 enable_pdl=None, first_tokens: int = 0, kv_scales=None):
     """seq_lens: int32 (or uint32) tensor holding the unsigned kv lengths.
     With cum_seq_lens_q ([B+1] int32 on the device) and max_q_len, request b
     has the query rows cum[b] .. cum[b+1]-1 (variable-length queries) and
     q_len_per_req is ignored.  bmm1_scale / bmm2_scale may be one-element
     float32 device tensors, read when the kernels run; enable_pdl launches
     the call's first kernel as a programmatic dependent of the stream's
-    previous kernel (None / False: an ordinary launch)."""
+    previous kernel (None / False: an ordinary launch).  first_tokens: keys
+    at the start of each request that stay visible under window_left; the
+    pages between them and the window are not read.  kv_scales: block scales
+    of a float8_e4m3fn cache (see paged_append_scaled); each element stands
+    for its value times its block's scale."""
     layout = _layout_code(kv_layout)
     kp, vp, stride, P, Hkv, S, D, base = split_cache(kv_cache, layout)
     rows, Hqo, Dq = query.shape
@@ -315,6 +405,22 @@ def paged_decode(query, kv_cache, workspace, block_tables, seq_lens, max_seq_len
         _check_decode_args(query, out, lse, block_tables, seq_lens, B * q_len_per_req)
     s1, s1_dev = _scale_arg(bmm1_scale, query.device)
     s2, s2_dev = _scale_arg(bmm2_scale, query.device)
+    if first_tokens or kv_scales is not None:
+        ks = vs = None
+        ss = block = 0
+        if kv_scales is not None:
+            if base.dtype != torch.float8_e4m3fn:
+                raise PagedKVError("kv_scales belong to a float8_e4m3fn cache")
+            ks, vs, ss, block = split_scales(kv_scales, P, Hkv, S, base.device)
+        _same_device(query, base, workspace, block_tables, seq_lens, cum_seq_lens_q, sinks, out, lse, err_word)
+        mq = int(max_q_len) if cum_seq_lens_q is not None else q_len_per_req
+        _check(load_library().paged_decode_window(
+            _ptr(query), rows, kp, vp, stride, P, ks, vs, ss, block, _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _ptr(block_tables), block_tables.stride(0),
+            _ptr(seq_lens), B, max_seq_len, s1, s2, s1_dev, s2_dev, window_left, first_tokens, _ptr(sinks), mq,
+            _ptr(cum_seq_lens_q), Hqo, Hkv, D, S, layout, _decode_dtype(query, base), 1 if enable_pdl else 0,
+            _ptr(out), _ptr(lse), _ptr(err_word), _stream(stream)))
+        return out
     if s1_dev or s2_dev or enable_pdl:
         mq = int(max_q_len) if cum_seq_lens_q is not None else q_len_per_req
         _check(load_library().paged_decode_ex(

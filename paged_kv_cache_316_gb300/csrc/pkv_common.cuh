@@ -203,6 +203,24 @@ __device__ __forceinline__ float fast_log2(float x) {
     return y;
 }
 
+// 1 / x on the special-function unit (PTX rcp.approx).
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Scales outside [2^-48, 2^48] are flagged and brought into that range: with
+// it, the weights of two keys that a softmax must tell apart (2^30) stay
+// apart by less than fp32's exponent range after the V scales are folded in
+// (see the decode split kernel).
+constexpr float kScaleMin = 3.5527136788005009e-15f, kScaleMax = 281474976710656.f;
+__device__ __forceinline__ float checked_scale(float x, int32_t *err) {
+    if (x >= kScaleMin && x <= kScaleMax) return x;
+    set_err(err, PKV_DEV_ERR_SCALE);
+    return x > kScaleMax ? kScaleMax : kScaleMin;  // (NaN: the lower end)
+}
+
 // Byte offset of 16-byte chunk `c` of row `r` in a row-major smem tile whose
 // rows are `row_bytes` long: chunks are XOR-swizzled within each group of 8
 // so that 8 consecutive rows at the same logical chunk hit distinct banks.
