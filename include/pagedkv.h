@@ -569,6 +569,62 @@ int paged_prefill_fp8(const void *q, int64_t total_q, const void *k_cache,
                       int32_t kv_dtype, int32_t out_dtype, void *out, float *lse,
                       int32_t *err_word, void *stream);
 
+/*
+ * paged_prefill_scaled_workspace_size -- bytes of device workspace that
+ * paged_prefill_window needs over E4M3 caches with block scales: the plain
+ * prefill's and room for the dequantised keys and values
+ * (batch_size * max_sequence_kv tokens in 16 bits).
+ */
+size_t paged_prefill_scaled_workspace_size(int32_t batch_size, int32_t num_qo_heads,
+                                           int32_t num_kv_heads,
+                                           int32_t max_token_per_sequence,
+                                           int32_t max_sequence_kv, int32_t d_qk,
+                                           int32_t d_vo);
+
+/*
+ * paged_prefill_window -- paged_prefill_ex under a sliding window that keeps
+ * a few first tokens visible, and over E4M3 caches with one scale for each
+ * block of tokens and head.
+ *  - window_left >= 0: query i of a request, at position p = kv_b - q_b + i,
+ *    sees key j iff (j >= p - window_left or j < first_tokens), j < kv_b and,
+ *    with causal, j <= p.  window_left = -1: no window, first_tokens has no
+ *    effect.  Key tiles that no row of a 128-row query tile sees are not
+ *    read; neither are the block-table entries of page parts that no row of
+ *    it sees, so pages between a request's first tokens and the window of its
+ *    first query may have been freed.
+ *  - dtype PKV_F16 / PKV_BF16 (k_scales, v_scales NULL, scale_block 0): 16-bit
+ *    query, caches (paged, or contiguous with block_tables NULL) and output;
+ *    workspace >= paged_prefill_workspace_size(...).
+ *  - dtype PKV_F16_E4M3 / PKV_BF16_E4M3: 16-bit query and output over paged
+ *    E4M3 caches with block scales as in paged_decode_window (the same scale
+ *    layout for K and V, whatever d_qk and d_vo are); strides in E4M3
+ *    elements, multiples of 16; workspace >=
+ *    paged_prefill_scaled_workspace_size(...).  Keys and values are
+ *    dequantised to the query's 16-bit type first: exact when the scales are
+ *    powers of two and the products lie in that type's range, as those of a
+ *    cache that paged_append_scaled filled from it do; else rounded once.
+ *  - batch_offsets_*: as paged_prefill_ex (each may be NULL; offsets of K and
+ *    V with contiguous K/V only).
+ * Device errors as paged_prefill, and PKV_DEV_ERR_SCALE (see
+ * paged_decode_window).
+ */
+int paged_prefill_window(const void *q, int64_t total_q, const void *k_cache,
+                         const void *v_cache, int64_t k_page_stride,
+                         int64_t v_page_stride, int64_t max_num_pages,
+                         const float *k_scales, const float *v_scales,
+                         int64_t scale_page_stride, int32_t scale_block, float scale,
+                         void *workspace, size_t workspace_bytes,
+                         int32_t max_token_per_sequence, int32_t max_sequence_kv,
+                         const int32_t *actual_seq_lens_q,
+                         const int32_t *actual_seq_lens_kv, const int32_t *block_tables,
+                         int32_t block_table_stride, int32_t batch_size, int32_t causal,
+                         int32_t window_left, int32_t first_tokens, int32_t num_qo_heads,
+                         int32_t num_kv_heads, int32_t d_qk, int32_t d_vo,
+                         int32_t page_size, int32_t layout, int32_t dtype, void *out,
+                         float *lse, const int32_t *batch_offsets_q,
+                         const int32_t *batch_offsets_o, const int32_t *batch_offsets_k,
+                         const int32_t *batch_offsets_v, int32_t *err_word, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,6 +18,7 @@ from .binding import (  # noqa: F401
     paged_decode_noalloc,
     paged_prefill_workspace_size,
     paged_prefill_fp8_workspace_size,
+    paged_prefill_scaled_workspace_size,
     paged_prefill,
     kernel_launches,
     set_wait_limit_ns,

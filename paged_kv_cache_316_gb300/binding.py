@@ -64,6 +64,10 @@ _SIGNATURES = {
                           _i32, _c_p, _c_p, _c_p, _i32, _i32, _i32, _i32, _i32, _i32,
                           _i32, _i32, _i32, _i32, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p,
                           _c_p], ctypes.c_int),
+    "paged_prefill_scaled_workspace_size": ([_i32] * 7, _sz),
+    "paged_prefill_window": ([_c_p, _i64, _c_p, _c_p, _i64, _i64, _i64, _c_p, _c_p, _i64, _i32, _f32, _c_p, _sz,
+                              _i32, _i32, _c_p, _c_p, _c_p, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                              _i32, _i32, _i32, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p], ctypes.c_int),
     "paged_prefill_fp8_workspace_size": ([_i32] * 5 + [_i64] + [_i32] * 4, _sz),
     "paged_prefill_fp8": ([_c_p, _i64, _c_p, _c_p, _i64, _i64, _i64, _f32, _c_p, _c_p, _c_p, _c_p,
                            _sz, _i32, _i32, _c_p, _c_p, _c_p, _i32, _i32, _i32, _i32, _i32, _i32,
@@ -495,6 +499,13 @@ def paged_prefill_fp8_workspace_size(batch_size, num_qo_heads, num_kv_heads,
         E4M3 if kv_dtype == torch.float8_e4m3fn else BF16))
 
 
+def paged_prefill_scaled_workspace_size(batch_size, num_qo_heads, num_kv_heads, max_token_per_sequence,
+                                        max_sequence_kv, d_qk, d_vo) -> int:
+    """Workspace of paged_prefill over E4M3 caches with block scales (kv_scales)."""
+    return int(load_library().paged_prefill_scaled_workspace_size(
+        batch_size, num_qo_heads, num_kv_heads, max_token_per_sequence, max_sequence_kv, d_qk, d_vo))
+
+
 def _scale_ptr(t, device):
     if t is None:
         return None
@@ -509,7 +520,8 @@ def paged_prefill(q, k_cache, v_cache, scale: float, workspace,
                   causal: bool = True, out=None, lse=None, kv_layout="HND",
                   err_word=None, stream=None, batch_offsets_q=None, batch_offsets_o=None,
                   batch_offsets_k=None, batch_offsets_v=None, q_scale=None, k_scale=None,
-                  v_scale=None, o_data_type=None):
+                  v_scale=None, o_data_type=None, window_left: int = -1, first_tokens: int = 0,
+                  kv_scales=None):
     """block_tables=None: k_cache / v_cache are contiguous [rows, Hkv, d]
     tensors (the page's non-paged case; kv_layout is then NHD).  The
     batch_offsets_* tensors ([B] int32 on the device, token rows) place each
@@ -517,7 +529,13 @@ def paged_prefill(q, k_cache, v_cache, scale: float, workspace,
     q and/or the (paged) caches may be float8_e4m3fn: q_scale, k_scale and
     v_scale (one float32 each on the device, or None for 1) dequantise them,
     and the output is o_data_type (bf16 when q is E4M3 and none is given);
-    the workspace then needs paged_prefill_fp8_workspace_size bytes."""
+    the workspace then needs paged_prefill_fp8_workspace_size bytes.
+    window_left, first_tokens: the query at position p sees key j if also
+    j >= p - window_left or j < first_tokens (-1: no window); the pages between
+    a request's first tokens and its first query's window are not read.
+    kv_scales: block scales of float8_e4m3fn caches under a 16-bit query (see
+    paged_append_scaled); the workspace then needs
+    paged_prefill_scaled_workspace_size bytes."""
     if block_tables is None:
         kv_layout = "NHD"
     layout = _layout_code(kv_layout)
@@ -534,6 +552,12 @@ def paged_prefill(q, k_cache, v_cache, scale: float, workspace,
     if dk != d_qk:
         raise PagedKVError("q head_dim differs from the key cache's")
     e4 = torch.float8_e4m3fn
+    if kv_scales is not None or window_left != -1 or first_tokens:
+        return _prefill_window(q, k_cache, v_cache, scale, workspace, max_token_per_sequence, max_sequence_kv,
+                               actual_seq_lens_q, actual_seq_lens_kv, block_tables, causal, out, lse, layout,
+                               (P, Hkv, S, dv), err_word, stream,
+                               (batch_offsets_q, batch_offsets_o, batch_offsets_k, batch_offsets_v),
+                               (q_scale, k_scale, v_scale), o_data_type, window_left, first_tokens, kv_scales)
     fp8 = q.dtype == e4 or k_cache.dtype == e4 or any(x is not None for x in (q_scale, k_scale, v_scale))
     odt = o_data_type or (torch.bfloat16 if q.dtype == e4 else q.dtype)
     if out is None:
@@ -578,4 +602,57 @@ def paged_prefill(q, k_cache, v_cache, scale: float, workspace,
             _ptr(actual_seq_lens_kv), _ptr(block_tables), bt_stride, B,
             int(causal), Hqo, Hkv, d_qk, dv, S, layout, _dtype_code(q), _ptr(out),
             _ptr(lse), *(_ptr(o) for o in offsets), _ptr(err_word), _stream(stream)))
+    return out, lse
+
+
+def _prefill_window(q, k_cache, v_cache, scale, workspace, max_q, max_kv, lens_q, lens_kv, block_tables, causal, out,
+                    lse, layout, dims, err_word, stream, offsets, scalar_scales, o_data_type, window_left, first_tokens,
+                    kv_scales):
+    """paged_prefill under a window and / or over caches with block scales."""
+    P, Hkv, S, dv = dims
+    total_q, Hqo, d_qk = q.shape
+    dtype = _dtype_code(q)
+    if dtype not in (F16, BF16) or any(x is not None for x in scalar_scales) or o_data_type not in (None, q.dtype):
+        raise PagedKVError("window_left, first_tokens and kv_scales take a 16-bit query and output and no "
+                           "q_scale / k_scale / v_scale")
+    if not q.is_contiguous():
+        raise PagedKVError("q must be contiguous [total_q, num_qo_heads, d_qk]")
+    ks = vs = None
+    ss = block = 0
+    if kv_scales is not None:
+        if k_cache.dtype != torch.float8_e4m3fn or v_cache.dtype != torch.float8_e4m3fn or block_tables is None:
+            raise PagedKVError("kv_scales belong to paged float8_e4m3fn caches")
+        ks, vs, ss, block = split_scales(kv_scales, P, Hkv, S, k_cache.device)
+        dtype = F16_E4M3 if dtype == F16 else BF16_E4M3
+    elif k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
+        raise PagedKVError("the caches hold the query's type, or float8_e4m3fn with kv_scales")
+    if v_cache.shape[:-1] != k_cache.shape[:-1]:
+        raise PagedKVError("K and V caches must have the same pages, heads and page size")
+    for t in (k_cache, v_cache):
+        if P > 0 and not t[0].is_contiguous():
+            raise PagedKVError("each page must be contiguous")
+    if out is None:
+        out = torch.empty((total_q, Hqo, dv), dtype=q.dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty((total_q, Hqo), dtype=torch.float32, device=q.device)
+    if tuple(out.shape) != (total_q, Hqo, dv) or out.dtype != q.dtype or not out.is_contiguous():
+        raise PagedKVError(f"out must be a contiguous {q.dtype} [{total_q}, {Hqo}, {dv}] tensor")
+    if tuple(lse.shape) != (total_q, Hqo) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise PagedKVError(f"lse must be a contiguous float32 [{total_q}, {Hqo}] tensor")
+    B = lens_q.shape[0]
+    for t in (lens_q, lens_kv) + tuple(o for o in offsets if o is not None):
+        if t.dtype != torch.int32 or tuple(t.shape) != (B,) or not t.is_contiguous():
+            raise PagedKVError(f"lengths and batch offsets must be contiguous int32 [{B}]")
+    bt_stride = 0
+    if block_tables is not None:
+        if block_tables.dim() != 2 or block_tables.shape[0] < B or block_tables.dtype != torch.int32 \
+                or block_tables.stride(1) != 1:
+            raise PagedKVError("block_tables must be int32 [>= batch_size, pages] with unit column stride")
+        bt_stride = block_tables.stride(0)
+    _same_device(q, k_cache, v_cache, workspace, lens_q, lens_kv, block_tables, out, lse, err_word, *offsets)
+    _check(load_library().paged_prefill_window(
+        _ptr(q), total_q, _ptr(k_cache), _ptr(v_cache), k_cache.stride(0), v_cache.stride(0), P, ks, vs, ss, block,
+        scale, _ptr(workspace), workspace.numel() * workspace.element_size(), max_q, max_kv, _ptr(lens_q),
+        _ptr(lens_kv), _ptr(block_tables), bt_stride, B, int(causal), window_left, first_tokens, Hqo, Hkv, d_qk, dv, S,
+        layout, dtype, _ptr(out), _ptr(lse), *(_ptr(o) for o in offsets), _ptr(err_word), _stream(stream)))
     return out, lse

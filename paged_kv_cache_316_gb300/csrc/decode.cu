@@ -216,7 +216,9 @@ extern "C" int paged_decode_window(const void *query, int64_t num_tokens, const 
                                    int32_t head_dim, int32_t page_size, int32_t layout, int32_t dtype,
                                    int32_t enable_pdl, void *out, float *lse, int32_t *err_word, void *stream) {
     const CallRange nvtx_range("paged_decode_window");
-    if (num_tokens < 0 || max_q_len < 1 || first_tokens < 0) return PKV_ERR_INVALID_ARG;
+    if (num_tokens < 0 || max_q_len < 1 || first_tokens < 0 || window_left < -1) return PKV_ERR_INVALID_ARG;
+    if (max_seq_len > (1 << 30)) return PKV_ERR_UNSUPPORTED;
+    if (window_left > max_seq_len && max_seq_len >= 0) window_left = max_seq_len;  // every key either way
     if (!cum_seq_lens_q && num_tokens < static_cast<int64_t>(batch_size) * max_q_len) return PKV_ERR_INVALID_ARG;
     if (num_tokens == 0) return PKV_OK;
     DecodeExt ext;

@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8>::CTAS) decode_spl
     }
     const int R = p.group * Q;  // query rows of this (request, kv head)
     int lo, first, n_split;
-    DecodeRun run;
+    DecodeRun run = {};
     if constexpr (FIRST) {
         run = decode_run(L, Q, p.window_left, p.first_tokens, p.chunk);
         lo = run.lo;

@@ -118,6 +118,9 @@ struct PrefillParams {
     // rows][128 B]) with the coordinate page * k5_ratio + kv head, or (0)
     // through the 4-D map, one copy per atom ([atom][row][128 B] stages)
     int k5, k5_ratio;
+    // WIN: the query at position p sees key j iff j >= p - window_left or
+    // j < first_tokens (and, causal, j <= p)
+    int window_left, first_tokens;
 };
 
 // cu_q / cu_kv = exclusive prefix sums of the query / kv lengths and
@@ -217,8 +220,12 @@ __device__ __forceinline__ void tmem_wait_ld_regs(uint32_t (&r)[32]) {
 struct PfItem {
     int b, hA, hB, i0, row_base, orow_base, kvh, shift, qb, kvb, n_tiles;
     int kv_k, kv_v;  // first K / V row of the request (contiguous K/V)
+    // WIN: no row of the tile sees the keys [first_tokens, lo); the item reads
+    // the key tiles [0, n_first) and those from n_first + skip on
+    int lo, n_first, skip;
 };
 
+template <bool WIN>
 __device__ __forceinline__ void pf_item(const PrefillParams &p, const int4 itm, int bn, PfItem &it) {
     it.b = itm.x;
     it.hA = itm.y;
@@ -238,13 +245,30 @@ __device__ __forceinline__ void pf_item(const PrefillParams &p, const int4 itm, 
     int k_hi = p.causal ? min(it.kvb, it.shift + it.i0 + kPfRows) : it.kvb;
     if (k_hi < 0) k_hi = 0;
     it.n_tiles = (k_hi + bn - 1) / bn;
+    it.lo = it.n_first = it.skip = 0;
+    if constexpr (WIN) {
+        const int lo = max(0, it.shift + it.i0 - p.window_left);  // of the tile's first row
+        if (lo > p.first_tokens && k_hi > 0) {
+            it.lo = lo;
+            it.n_first = (p.first_tokens + bn - 1) / bn;
+            it.skip = max(0, lo / bn - it.n_first);  // (lo < k_hi: the row sees its own position)
+            it.n_tiles -= it.skip;
+        }
+    }
+}
+// first key of the item's tile j
+template <bool WIN>
+__device__ __forceinline__ int pf_key(const PfItem &it, int j, int bn) {
+    return (WIN && j >= it.n_first ? j + it.skip : j) * bn;
 }
 
 // F8: the query and the caches hold E4M3 (one byte per element; d_qk 128):
 // QK runs as kind::f8f6f4 MMAs straight from the E4M3 tiles, and the E4M3 V
 // tiles are widened (exactly) to fp16 in shared memory by warp 11 for the
 // 16-bit PV, whose P is then fp16.  T is the output type.
-template <typename T, int DQK, int LAYOUT, bool F8 = false>
+// WIN: a sliding window that keeps the first tokens visible; key tiles that
+// no row of the item's query tile sees are skipped.
+template <typename T, int DQK, int LAYOUT, bool F8 = false, bool WIN = false>
 __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const PrefillParams p) {
@@ -468,7 +492,7 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
                 }
                 if (!ok || itm.x < 0) break;
                 PfItem it;
-                pf_item(p, itm, BN, it);
+                pf_item<WIN>(p, itm, BN, it);
                 const int32_t *bt = p.block_tables + static_cast<int64_t>(it.b) * p.bt_stride;
                 // Q blocks of this item, once the previous item's last QK is done;
                 // loaded after the item's first K tile so that the two overlap
@@ -493,10 +517,11 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
                 ok = __shfl_sync(0xffffffffu, ok, leader_lane);
                 if (!ok) break;
                 auto lookup = [&](int j) {  // lane i < nbox: page of box i of tile j
-                    const int key = j * BN + lane * RB;
+                    const int key = pf_key<WIN>(it, j, BN) + lane * RB;
                     int page = oob;
                     if (p.contiguous) return 0;  // one page: the whole tensor
-                    if (lane < nbox && key < it.kvb &&
+                    // (WIN: a page part that no row sees may be gone: zeros)
+                    if (lane < nbox && key < it.kvb && !(WIN && key >= p.first_tokens && key + RB <= it.lo) &&
                         dbg_in(key >> p.page_shift, 1, (p.max_kv + S - 1) >> p.page_shift, p.err)) {
                         page = bt[key >> p.page_shift];
                         if (page < 0 || page >= p.max_num_pages) {
@@ -522,7 +547,7 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
                         } else {
                             const uint32_t full = is_k ? b_kfull(st) : v_full(st);
                             mbar_expect_tx(full, is_k ? KB : (F8 ? V8B : VB));
-                            const int j0 = j * BN;
+                            const int j0 = pf_key<WIN>(it, j, BN);
     #pragma unroll
                             for (int i = 0; i < 16; ++i) {
                                 if (i >= nbox) break;
@@ -646,7 +671,7 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
                     ok = __shfl_sync(0xffffffffu, ok, 0);
                     if (!ok || itm.x < 0) break;
                     PfItem it;
-                    pf_item(p, itm, BN, it);
+                    pf_item<WIN>(p, itm, BN, it);
                     const bool hasB = it.hB >= 0;
                     const int n = it.n_tiles;
                     if (!mwait(b_qfull, k & 1)) { ok = false; break; }
@@ -723,7 +748,7 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok || itm.x < 0) break;
                 PfItem it;
-                pf_item(p, itm, BN, it);
+                pf_item<WIN>(p, itm, BN, it);
                 for (int j = 0; j < it.n_tiles; ++j) {
                     const int t = t_base + j, st = t % SV, us = t / SV;
                     bool w = mbar_wait(b_v8full(st), us & 1, abort_flag, wlim);
@@ -797,7 +822,7 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
         };
         // scores of chunk i of the tile at key offset j0: scaled if the scale
         // is not positive, masked past the row's last key
-        auto scale_mask = [&](int i, int j0, bool warp_full, int lim, uint32_t(&ra)[32]) {
+        auto scale_mask = [&](int i, int j0, bool warp_full, int lim, int row_lo, uint32_t(&ra)[32]) {
             if (!pos_scale) {
 #pragma unroll
                 for (int c = 0; c < 32; ++c) ra[c] = __float_as_uint(__uint_as_float(ra[c]) * sc);
@@ -807,6 +832,15 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 32; ++c)
                     if (c > lr) ra[c] = __float_as_uint(-INFINITY);
+                if constexpr (WIN) {
+                    // columns of the keys [first_tokens, row_lo)
+                    const int ca = max(p.first_tokens - (j0 + 32 * i), 0), cb = row_lo - (j0 + 32 * i);
+                    if (cb > ca) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (c >= ca && c < cb) ra[c] = __float_as_uint(-INFINITY);
+                    }
+                }
             }
         };
         auto chunk_max = [&](const uint32_t(&ra)[32]) {
@@ -846,7 +880,7 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok || itm.x < 0) break;
             PfItem it;
-            pf_item(p, itm, BN, it);
+            pf_item<WIN>(p, itm, BN, it);
             const int n = it.n_tiles;
             const int h = X == 0 ? it.hA : it.hB;
             if (h < 0) {  // block B absent in this item
@@ -855,14 +889,17 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
             }
             const int pos = it.shift + it.i0 + r;
             const int lim = p.causal ? min(pos, it.kvb - 1) : it.kvb - 1;  // last visible key
+            // (WIN) the row does not see the keys [first_tokens, row_lo)
+            const int row_lo = WIN ? max(0, pos - p.window_left) : 0;
             float m_used = -INFINITY, l = 0.f;
             for (int j = 0; j < n; ++j) {
                 const int t = t_base + j, tx = tx_base + j;
-                const int j0 = j * BN;
+                const int j0 = pf_key<WIN>(it, j, BN);
                 // S_X(t) complete, and with it PV_X(t-1)
                 if (!wait_warp(b_sfull(X), tx & 1)) { ok = false; break; }
                 tc_fence_after();
-                const bool warp_full = __all_sync(0xffffffffu, j0 + BN - 1 <= lim);
+                const bool warp_full = __all_sync(0xffffffffu, j0 + BN - 1 <= lim &&
+                                                                      (!WIN || j0 >= row_lo || j0 + BN <= p.first_tokens));
                 uint32_t rs[NCH][32];
 #pragma unroll
                 for (int i = 0; i < NCH; ++i) tmem_ld32(s_addr + 32 * i, rs[i]);
@@ -871,7 +908,7 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
                 float mh = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < NCH; ++i) {
-                    scale_mask(i, j0, warp_full, lim, rs[i]);
+                    scale_mask(i, j0, warp_full, lim, row_lo, rs[i]);
                     mh = fmaxf(mh, chunk_max(rs[i]));
                 }
                 const float mt = pos_scale ? mh * sc : mh;
@@ -893,7 +930,9 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
                 // rows of V past the sequence end may hold anything (even NaN):
                 // block A zeroes them before its PV (block B's PV comes later in
                 // issue order), so that P = 0 there cannot produce 0 * NaN
-                if (X == 0 && j0 + BN > it.kvb) {
+                // (WIN: and rows of keys between the first tokens and the window)
+                const int wa = WIN ? max(p.first_tokens - j0, 0) : 0, wb = WIN ? min(it.lo - j0, BN) : 0;
+                if (X == 0 && (j0 + BN > it.kvb || (WIN && wb > wa))) {
                     const int sv = t % SV, uv = t / SV;
                     if (!wait_warp(b_vfull(sv), uv & 1)) { ok = false; break; }
                     const int zs = max(it.kvb - j0, 0);
@@ -902,6 +941,13 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
                         const int row = zs + (q >> 4), chunk = q & 15;
                         *reinterpret_cast<uint4 *>(vbase + (chunk >> 3) * (BN * 128) + row * 128 + (chunk & 7) * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    if constexpr (WIN) {
+                        for (int q = r; q < (wb - wa) * 16; q += 128) {
+                            const int row = wa + (q >> 4), chunk = q & 15;
+                            *reinterpret_cast<uint4 *>(vbase + (chunk >> 3) * (BN * 128) + row * 128 +
+                                                       (chunk & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
                     }
                     fence_proxy_async_smem();
                 }
@@ -983,11 +1029,11 @@ static size_t prefill_smem_bytes() {
            8 * (13 + 2 * SK + 2 * SV + (F8 ? 2 * SV : 0));
 }
 
-template <typename T, int DQK, int LAYOUT, bool F8 = false>
+template <typename T, int DQK, int LAYOUT, bool F8 = false, bool WIN = false>
 static int launch_prefill(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                           const PrefillParams &p, dim3 grid, cudaStream_t st) {
     const size_t smem = prefill_smem_bytes<DQK, F8>();
-    auto kern = prefill_tc_kernel<T, DQK, LAYOUT, F8>;
+    auto kern = prefill_tc_kernel<T, DQK, LAYOUT, F8, WIN>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem)) != cudaSuccess)
         return PKV_ERR_CUDA;
@@ -1028,6 +1074,13 @@ struct WidenKvParams {
     const int32_t *cu_kv;   // from the plan kernel
     int max_kv, Hkv, page_shift;
     int32_t *err;
+    // SCL: block scales [page][kv head][page_size / block] of K and V,
+    // multiplied in; keys that no query sees through the window (none if
+    // window_left < 0) may be left out
+    const float *scales[2];
+    int64_t scale_stride;
+    int block_shift, window_left, first_tokens, bn, max_q;
+    const int32_t *seq_lens_q;
 };
 constexpr int kWidenTok = 32;  // keys per CTA of the cache widening
 
@@ -1035,7 +1088,9 @@ constexpr int kWidenTok = 32;  // keys per CTA of the cache widening
 // becomes 32 bytes of the packed 16-bit tensor.  A page id outside the pool
 // flags PKV_DEV_ERR_PAGE and its rows widen to zeros, as the 16-bit path's
 // zero-filled rows.
-template <typename T, int LAYOUT>
+// SCL: the values are multiplied by their block's scale (one rounding to T,
+// none when the scale is a power of two and the product is in T's range).
+template <typename T, int LAYOUT, bool SCL = false>
 __global__ void __launch_bounds__(256) prefill_widen_kv_kernel(const WidenKvParams w) {
     pdl_wait();  // cu_kv
     pdl_launch_dependents();
@@ -1043,29 +1098,62 @@ __global__ void __launch_bounds__(256) prefill_widen_kv_kernel(const WidenKvPara
     const int kvb = min(max(w.seq_lens_kv[b], 0), w.max_kv);
     const int j0 = blockIdx.x * kWidenTok;
     if (j0 >= kvb) return;
+    if constexpr (SCL) {
+        // the attention kernel reads whole key tiles of bn keys (a multiple of
+        // kWidenTok): skip those between the first tokens and the window of
+        // the request's first query
+        if (w.window_left >= 0) {
+            const int qb = min(max(w.seq_lens_q[b], 0), w.max_q);
+            const int lo = kvb - qb - w.window_left;
+            if (lo > w.first_tokens && j0 >= (w.first_tokens + w.bn - 1) / w.bn * w.bn && j0 < lo / w.bn * w.bn) return;
+        }
+    }
     const int d = w.d[z], CH = d / 16;
     const int S = 1 << w.page_shift;
     const int64_t row0 = w.cu_kv[b];
     const int n = min(kWidenTok, kvb - j0) * w.Hkv * CH;
     const int32_t *bt = w.block_tables + b * w.bt_stride;
     T *dst = static_cast<T *>(w.dst[z]);
+    // (SCL) keys of the kept tiles that no query sees become zeros, their
+    // pages unread
+    auto seen_key = [&](int j) {
+        if constexpr (SCL) {
+            if (w.window_left < 0) return true;
+            const int qb = min(max(w.seq_lens_q[b], 0), w.max_q);
+            return j < w.first_tokens || j >= kvb - qb - w.window_left;
+        }
+        return true;
+    };
     for (int idx = threadIdx.x; idx < n; idx += blockDim.x) {
         const int c = idx % CH, rest = idx / CH;
         const int h = rest % w.Hkv, j = j0 + rest / w.Hkv;
-        const int page = bt[j >> w.page_shift];
+        const int page = seen_key(j) ? bt[j >> w.page_shift] : -2;
         uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+        float sc = 1.f;
         if (page < 0 || page >= w.max_num_pages) {
-            if (z == 0 && h == 0 && c == 0) set_err(w.err, PKV_DEV_ERR_PAGE);
+            if (z == 0 && h == 0 && c == 0 && (!SCL || page != -2 || seen_key(j))) set_err(w.err, PKV_DEV_ERR_PAGE);
         } else {
             raw = *reinterpret_cast<const uint4 *>(
                 w.src[z] + kv_row_offset<LAYOUT>(page, w.page_stride[z], h, j & (S - 1), w.Hkv, S, d) + c * 16);
+            if constexpr (SCL)
+                sc = checked_scale(__ldg(w.scales[z] + page * w.scale_stride +
+                                         (static_cast<int64_t>(h) << (w.page_shift - w.block_shift)) +
+                                         ((j & (S - 1)) >> w.block_shift)),
+                                   w.err);
         }
         const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
         uint32_t o[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            o[2 * i] = widen_e4m3x2<T>(x[i] & 0xffffu);
-            o[2 * i + 1] = widen_e4m3x2<T>(x[i] >> 16);
+            if constexpr (SCL) {
+                const float2 lo = unpack2<__half>(widen_e4m3x2<__half>(x[i] & 0xffffu));
+                const float2 hi = unpack2<__half>(widen_e4m3x2<__half>(x[i] >> 16));
+                o[2 * i] = pack2<T>(lo.x * sc, lo.y * sc);
+                o[2 * i + 1] = pack2<T>(hi.x * sc, hi.y * sc);
+            } else {
+                o[2 * i] = widen_e4m3x2<T>(x[i] & 0xffffu);
+                o[2 * i + 1] = widen_e4m3x2<T>(x[i] >> 16);
+            }
         }
         uint4 *out = reinterpret_cast<uint4 *>(dst + ((row0 + j) * w.Hkv + h) * d + c * 16);
         out[0] = make_uint4(o[0], o[1], o[2], o[3]);
@@ -1100,13 +1188,21 @@ struct PrefillFp8 {
     const uint8_t *q_src = nullptr;  // E4M3 query rows, widened into the call's `q` first
     bool kv8 = false;                // widen the paged caches after the plan kernel
     WidenKvParams widen{};           // (cu_kv and err filled in by prefill_impl)
+    bool scaled = false;             // the caches have block scales (widen.scales)
     int layout = PKV_HND;            // of the E4M3 caches
 };
 
 template <typename T>
 static int dispatch_prefill(int d_qk, int layout, const CUtensorMap &tq, const CUtensorMap &tk,
                             const CUtensorMap &tv, const PrefillParams &p, dim3 grid, cudaStream_t st,
-                            bool f8_direct) {
+                            bool f8_direct, bool win) {
+    if (win) {
+        if (d_qk == 128)
+            return layout == PKV_HND ? launch_prefill<T, 128, PKV_HND, false, true>(tq, tk, tv, p, grid, st)
+                                     : launch_prefill<T, 128, PKV_NHD, false, true>(tq, tk, tv, p, grid, st);
+        return layout == PKV_HND ? launch_prefill<T, 192, PKV_HND, false, true>(tq, tk, tv, p, grid, st)
+                                 : launch_prefill<T, 192, PKV_NHD, false, true>(tq, tk, tv, p, grid, st);
+    }
     if (f8_direct)  // (d_qk 128)
         return layout == PKV_HND ? launch_prefill<T, 128, PKV_HND, true>(tq, tk, tv, p, grid, st)
                                  : launch_prefill<T, 128, PKV_NHD, true>(tq, tk, tv, p, grid, st);
@@ -1228,7 +1324,8 @@ static int prefill_impl(const void *q, int64_t total_q, const void *k_cache,
                              int32_t d_vo, int32_t page_size, int32_t layout, int32_t dtype,
                              void *out, float *lse, int32_t *err_word, void *stream,
                              const int32_t *off_q, const int32_t *off_o, const int32_t *off_k,
-                             const int32_t *off_v, PrefillFp8 *f8 = nullptr) {
+                             const int32_t *off_v, PrefillFp8 *f8 = nullptr, int32_t window_left = -1,
+                             int32_t first_tokens = 0) {
     // no block table: contiguous K/V of max_num_pages rows, page strides are row strides
     const bool contiguous = block_tables == nullptr;
     if (contiguous) {
@@ -1340,7 +1437,13 @@ static int prefill_impl(const void *q, int64_t total_q, const void *k_cache,
         const dim3 wgrid(static_cast<unsigned>((max_sequence_kv + kWidenTok - 1) / kWidenTok),
                          static_cast<unsigned>(batch_size), 2);
         if (max_sequence_kv > 0) {
-            auto wk = dtype == PKV_BF16
+            auto wk = f8->scaled
+                          ? (dtype == PKV_BF16
+                                 ? (f8->layout == PKV_HND ? prefill_widen_kv_kernel<__nv_bfloat16, PKV_HND, true>
+                                                          : prefill_widen_kv_kernel<__nv_bfloat16, PKV_NHD, true>)
+                                 : (f8->layout == PKV_HND ? prefill_widen_kv_kernel<__half, PKV_HND, true>
+                                                          : prefill_widen_kv_kernel<__half, PKV_NHD, true>))
+                      : dtype == PKV_BF16
                           ? (f8->layout == PKV_HND ? prefill_widen_kv_kernel<__nv_bfloat16, PKV_HND>
                                                    : prefill_widen_kv_kernel<__nv_bfloat16, PKV_NHD>)
                           : (f8->layout == PKV_HND ? prefill_widen_kv_kernel<__half, PKV_HND>
@@ -1384,14 +1487,16 @@ static int prefill_impl(const void *q, int64_t total_q, const void *k_cache,
     p.wait_ns = wait_limit_ns();
     p.k5 = k5;
     p.k5_ratio = k5_ratio;
+    p.window_left = window_left;
+    p.first_tokens = first_tokens;
     const int n_qt = (max_token_per_sequence + kPfRows - 1) / kPfRows;
     const int64_t items = static_cast<int64_t>(n_qt) * num_kv_heads * pairs * batch_size;
     if (n_qt > 0) {
         // persistent: one CTA per SM (the shared-memory footprint allows one)
         const int64_t ctas = items < num_sms() ? items : num_sms();
         dim3 grid(static_cast<unsigned>(ctas));
-        int rc = dtype == PKV_BF16 ? dispatch_prefill<__nv_bfloat16>(d_qk, layout, tq, tk, tv, p, grid, st, f8d)
-                                   : dispatch_prefill<__half>(d_qk, layout, tq, tk, tv, p, grid, st, f8d);
+        int rc = dtype == PKV_BF16 ? dispatch_prefill<__nv_bfloat16>(d_qk, layout, tq, tk, tv, p, grid, st, f8d, window_left >= 0)
+                                   : dispatch_prefill<__half>(d_qk, layout, tq, tk, tv, p, grid, st, f8d, window_left >= 0);
         if (rc != PKV_OK) return rc;
         ++launches;
     }
@@ -1565,4 +1670,116 @@ extern "C" int paged_prefill_fp8(const void *q, int64_t total_q, const void *k_c
                         max_token_per_sequence, max_sequence_kv, actual_seq_lens_q, actual_seq_lens_kv, nullptr, 0,
                         batch_size, causal, num_qo_heads, num_kv_heads, d_qk, d_vo, 1, PKV_NHD, out_dtype, out, lse,
                         err_word, stream, nullptr, nullptr, nullptr, nullptr, &f8);
+}
+
+// ---- a window with first tokens; E4M3 caches with block scales -------------------
+
+extern "C" size_t paged_prefill_scaled_workspace_size(int32_t batch_size, int32_t num_qo_heads, int32_t num_kv_heads,
+                                                      int32_t max_token_per_sequence, int32_t max_sequence_kv,
+                                                      int32_t d_qk, int32_t d_vo) {
+    if (batch_size < 0 || num_qo_heads < 1 || num_kv_heads < 1 || max_token_per_sequence < 0 || max_sequence_kv < 0 ||
+        d_qk < 1 || d_vo < 1)
+        return 0;
+    size_t a, b, c;
+    return prefill_fp8_ws_bytes(batch_size, num_qo_heads, num_kv_heads, max_sequence_kv, 0, d_qk, d_vo, false, true, &a,
+                                &b, &c);
+}
+
+extern "C" int paged_prefill_window(const void *q, int64_t total_q, const void *k_cache, const void *v_cache,
+                                    int64_t k_page_stride, int64_t v_page_stride, int64_t max_num_pages,
+                                    const float *k_scales, const float *v_scales, int64_t scale_page_stride,
+                                    int32_t scale_block, float scale, void *workspace, size_t workspace_bytes,
+                                    int32_t max_token_per_sequence, int32_t max_sequence_kv,
+                                    const int32_t *actual_seq_lens_q, const int32_t *actual_seq_lens_kv,
+                                    const int32_t *block_tables, int32_t block_table_stride, int32_t batch_size,
+                                    int32_t causal, int32_t window_left, int32_t first_tokens, int32_t num_qo_heads,
+                                    int32_t num_kv_heads, int32_t d_qk, int32_t d_vo, int32_t page_size,
+                                    int32_t layout, int32_t dtype, void *out, float *lse,
+                                    const int32_t *batch_offsets_q, const int32_t *batch_offsets_o,
+                                    const int32_t *batch_offsets_k, const int32_t *batch_offsets_v, int32_t *err_word,
+                                    void *stream) {
+    const CallRange nvtx_range("paged_prefill_window");
+    if (window_left < -1 || first_tokens < 0 || max_sequence_kv < 0) return PKV_ERR_INVALID_ARG;
+    if (max_sequence_kv > (1 << 30)) return PKV_ERR_UNSUPPORTED;
+    // a window that reaches every key is none
+    if (window_left >= max_sequence_kv) window_left = -1;
+    if (first_tokens > max_sequence_kv) first_tokens = max_sequence_kv;
+    if (block_tables && (batch_offsets_k || batch_offsets_v)) return PKV_ERR_INVALID_ARG;  // pages place K/V
+    if (dtype != PKV_F16_E4M3 && dtype != PKV_BF16_E4M3) {
+        if (k_scales || v_scales || scale_block) return PKV_ERR_INVALID_ARG;  // scales belong to an 8-bit cache
+        return prefill_impl(q, total_q, k_cache, v_cache, k_page_stride, v_page_stride, max_num_pages, scale,
+                            workspace, workspace_bytes, max_token_per_sequence, max_sequence_kv, actual_seq_lens_q,
+                            actual_seq_lens_kv, block_tables, block_table_stride, batch_size, causal, num_qo_heads,
+                            num_kv_heads, d_qk, d_vo, page_size, layout, dtype, out, lse, err_word, stream,
+                            batch_offsets_q, batch_offsets_o, batch_offsets_k, batch_offsets_v, nullptr, window_left,
+                            first_tokens);
+    }
+    // E4M3 caches with block scales: dequantised into the workspace, packed
+    // request by request, and read from there as contiguous 16-bit K/V
+    const int32_t out_dtype = dtype == PKV_BF16_E4M3 ? PKV_BF16 : PKV_F16;
+    if (!block_tables || batch_offsets_k || batch_offsets_v) return PKV_ERR_INVALID_ARG;
+    if (batch_size < 0 || num_qo_heads < 1 || num_kv_heads < 1 || max_token_per_sequence < 0 || max_num_pages < 0 ||
+        block_table_stride < 0 || total_q < 0)
+        return PKV_ERR_INVALID_ARG;
+    if (layout != PKV_NHD && layout != PKV_HND) return PKV_ERR_INVALID_ARG;
+    if (num_qo_heads % num_kv_heads) return PKV_ERR_INVALID_ARG;
+    if ((d_qk != 128 && d_qk != 192) || d_vo != 128) return PKV_ERR_UNSUPPORTED;
+    const int ps = ilog2_exact(page_size), bs = ilog2_exact(scale_block);
+    if (ps < 3 || ps > 8) return PKV_ERR_UNSUPPORTED;
+    if (bs < 3 || bs > ps || scale_page_stride < (static_cast<int64_t>(num_kv_heads) << (ps - bs)))
+        return PKV_ERR_INVALID_ARG;
+    if (batch_size > 65535 || static_cast<int64_t>(batch_size) * max_sequence_kv > 0x7fffffff)
+        return PKV_ERR_UNSUPPORTED;
+    if (k_page_stride < static_cast<int64_t>(num_kv_heads) * page_size * d_qk ||
+        v_page_stride < static_cast<int64_t>(num_kv_heads) * page_size * d_vo || k_page_stride % 16 ||
+        v_page_stride % 16 || static_cast<int64_t>(block_table_stride) * page_size < max_sequence_kv)
+        return PKV_ERR_INVALID_ARG;
+    if (batch_size == 0 || total_q == 0) return PKV_OK;
+    if (!q || !k_cache || !v_cache || !k_scales || !v_scales || !actual_seq_lens_q || !actual_seq_lens_kv || !out || !lse)
+        return PKV_ERR_NULL;
+    if (!aligned16(k_cache) || !aligned16(v_cache) ||
+        ((reinterpret_cast<uintptr_t>(k_scales) | reinterpret_cast<uintptr_t>(v_scales)) & 3))
+        return PKV_ERR_INVALID_ARG;
+    size_t q_off, k_off, v_off;
+    const size_t need = prefill_fp8_ws_bytes(batch_size, num_qo_heads, num_kv_heads, max_sequence_kv, total_q, d_qk,
+                                             d_vo, false, true, &q_off, &k_off, &v_off);
+    if (!workspace) return PKV_ERR_NULL;
+    if (workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)) return PKV_ERR_WORKSPACE;
+    char *ws = static_cast<char *>(workspace);
+    PrefillFp8 f8;
+    f8.kv8 = true;
+    f8.scaled = true;
+    f8.layout = layout;
+    WidenKvParams &w = f8.widen;
+    w.src[0] = static_cast<const uint8_t *>(k_cache);
+    w.src[1] = static_cast<const uint8_t *>(v_cache);
+    w.page_stride[0] = k_page_stride;
+    w.page_stride[1] = v_page_stride;
+    w.d[0] = d_qk;
+    w.d[1] = d_vo;
+    w.dst[0] = ws + k_off;
+    w.dst[1] = ws + v_off;
+    w.max_num_pages = max_num_pages;
+    w.block_tables = block_tables;
+    w.bt_stride = block_table_stride;
+    w.seq_lens_kv = actual_seq_lens_kv;
+    w.seq_lens_q = actual_seq_lens_q;
+    w.max_kv = max_sequence_kv;
+    w.max_q = max_token_per_sequence;
+    w.Hkv = num_kv_heads;
+    w.page_shift = ps;
+    w.scales[0] = k_scales;
+    w.scales[1] = v_scales;
+    w.scale_stride = scale_page_stride;
+    w.block_shift = bs;
+    w.window_left = window_left;
+    w.first_tokens = first_tokens;
+    w.bn = pf_bn(d_qk);
+    const int64_t rows = static_cast<int64_t>(batch_size) * max_sequence_kv;
+    return prefill_impl(q, total_q, ws + k_off, ws + v_off, static_cast<int64_t>(num_kv_heads) * d_qk,
+                        static_cast<int64_t>(num_kv_heads) * d_vo, rows, scale, workspace, workspace_bytes,
+                        max_token_per_sequence, max_sequence_kv, actual_seq_lens_q, actual_seq_lens_kv, nullptr, 0,
+                        batch_size, causal, num_qo_heads, num_kv_heads, d_qk, d_vo, 1, PKV_NHD, out_dtype, out, lse,
+                        err_word, stream, batch_offsets_q, batch_offsets_o, nullptr, nullptr, &f8, window_left,
+                        first_tokens);
 }

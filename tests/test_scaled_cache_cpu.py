@@ -88,3 +88,24 @@ def test_binding_refuses_before_the_library():
                 (torch.zeros(4, 8, 1), torch.zeros(4, 8, 2))):
         with pytest.raises(pk.PagedKVError):
             split_scales(bad, 4, 8, 16, dev)
+
+
+def _prefill(lib, **over):  # noqa: F811
+    a = dict(q=GOOD, rows=150, k=GOOD, v=GOOD, kst=8 * 32 * 128, vst=8 * 32 * 128, pages=100, ks=GOOD, vs=GOOD, ss=8,
+             block=32, scale=0.08, ws=GOOD, wsb=1 << 40, mq=100, mkv=200, lq=GOOD, lkv=GOOD, bt=GOOD, bts=8, B=2,
+             causal=1, win=10, first=4, hq=32, hkv=8, dqk=128, dv=128, S=32, layout=1, dtype=4, out=GOOD, lse=GOOD,
+             oq=None, oo=None, ok=None, ov=None, err=None, stream=None)
+    a.update(over)
+    return lib.paged_prefill_window(*a.values())
+
+
+@pytest.mark.parametrize("over, status", [
+    (dict(win=-2), 2), (dict(first=-1), 2), (dict(dtype=1), 2), (dict(dtype=2), 2), (dict(layout=7), 2),
+    (dict(bt=None), 2), (dict(ok=GOOD), 2), (dict(block=4), 2), (dict(block=64), 2), (dict(ss=7), 2),
+    (dict(kst=8 * 32 * 128 + 8), 2), (dict(kst=100), 2), (dict(bts=3), 2), (dict(hkv=5), 2), (dict(dqk=64), 3),
+    (dict(dv=64), 3), (dict(S=4), 3), (dict(ks=None), 1), (dict(vs=None), 1), (dict(lse=None), 1), (dict(k=0x1004), 2),
+    (dict(wsb=4096), 4), (dict(ws=None), 1), (dict(mkv=-1), 2), (dict(rows=0), 0), (dict(B=0), 0),
+    (dict(dtype=1, ks=None, vs=None, block=0, lse=None), 1), (dict(dtype=1, ks=None, vs=None, block=0, wsb=8), 4),
+])
+def test_prefill_window_refuses(lib, over, status):  # noqa: F811
+    assert _prefill(lib, **over) == status
