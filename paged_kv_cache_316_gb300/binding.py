@@ -133,8 +133,13 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # (no Stream object per call)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -170,6 +175,17 @@ def _layout_code(kv_layout) -> int:
     raise PagedKVError(f"kv_layout must be NHD or HND, got {kv_layout!r}")
 
 
+def _rows_contiguous(t) -> bool:
+    """t[0].is_contiguous(), from the shape and strides."""
+    n = 1
+    shape, stride = t.shape, t.stride()
+    for i in range(len(shape) - 1, 0, -1):
+        if shape[i] != 1 and stride[i] != n:
+            return t.numel() == 0
+        n *= shape[i]
+    return True
+
+
 def split_cache(kv_cache, layout: int):
     """(k_ptr, v_ptr, page_stride, num_pages, num_heads, page_size, head_dim)
     for a 5-D [P, 2, ...] tensor or a (k, v) tuple of 4-D tensors."""
@@ -180,17 +196,17 @@ def split_cache(kv_cache, layout: int):
         base = k
         kp, vp = k.data_ptr(), v.data_ptr()
         for t in (k, v):
-            if not t[0].is_contiguous():
+            if not _rows_contiguous(t):
                 raise PagedKVError("each page must be contiguous")
         shape = k.shape[1:]
     else:
         if kv_cache.dim() != 5 or kv_cache.shape[1] != 2:
             raise PagedKVError("a single kv_cache tensor must be [pages, 2, ...]")
-        if not kv_cache[0].is_contiguous():
+        if not _rows_contiguous(kv_cache):
             raise PagedKVError("each page must be contiguous")
         base = kv_cache
         kp = kv_cache.data_ptr()
-        vp = kv_cache[:, 1].data_ptr()
+        vp = kp + kv_cache.stride(1) * kv_cache.element_size()
         shape = kv_cache.shape[2:]
     _ptr(base)
     if layout == HND:
@@ -210,32 +226,39 @@ def split_scales(kv_scales, num_pages: int, num_heads: int, page_size: int, devi
     (k, v) tuple of [pages, heads, page_size // block]."""
     if isinstance(kv_scales, (tuple, list)):
         k, v = kv_scales
-        if k.shape != v.shape or k.stride(0) != v.stride(0):
-            raise PagedKVError("K and V scales must have the same shape and page stride")
+        shape, stride = k.shape, k.stride()
+        if k.dim() != 3 or v.shape != shape or v.stride() != stride:
+            raise PagedKVError("K and V scales must be [pages, heads, blocks] of the same shape and strides")
+        same = v.dtype == torch.float32 and v.get_device() == k.get_device()
+        vp = _ptr(v)
     else:
-        if kv_scales.dim() != 4 or kv_scales.shape[1] != 2:
+        k = kv_scales
+        shape, stride = k.shape, k.stride()
+        if k.dim() != 4 or shape[1] != 2:
             raise PagedKVError("a single kv_scales tensor must be [pages, 2, heads, blocks]")
-        k, v = kv_scales[:, 0], kv_scales[:, 1]
-    if k.dim() != 3 or k.shape[0] != num_pages or k.shape[1] != num_heads or k.shape[2] < 1 \
-            or page_size % k.shape[2]:
+        vp = k.data_ptr() + 4 * stride[1]
+        shape, stride, same = (shape[0],) + tuple(shape[2:]), (stride[0],) + tuple(stride[2:]), True
+    P, H, blocks = shape
+    if P != num_pages or H != num_heads or blocks < 1 or page_size % blocks:
         raise PagedKVError(f"scales must be [{num_pages}, {num_heads}, page_size // block] for each of K and V")
-    for t in (k, v):
-        if t.dtype != torch.float32 or t.device != device:
-            raise PagedKVError("scales are float32 on the cache's device")
-        if t.stride(2) != 1 and t.shape[2] > 1 or t.stride(1) != t.shape[2] and t.shape[1] > 1:
-            raise PagedKVError("the scales of a page must be contiguous")
-    n = num_heads * k.shape[2]
-    stride = k.stride(0) if num_pages > 1 else max(n, k.stride(0))
-    return _ptr(k), _ptr(v), stride, page_size // k.shape[2]
+    if not same or k.dtype != torch.float32 or k.device != device:
+        raise PagedKVError("scales are float32 on the cache's device")
+    if (blocks > 1 and stride[2] != 1) or (H > 1 and stride[1] != blocks):
+        raise PagedKVError("the scales of a page must be contiguous")
+    return _ptr(k), vp, stride[0] if P > 1 else max(H * blocks, stride[0]), page_size // blocks
 
 
 def _same_device(*tensors):
     """All given tensors live on the current CUDA device: the library
     launches there."""
-    here = torch.cuda.current_device() if torch.cuda.is_available() else None
+    here = None
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != here):
-            raise PagedKVError("tensor arguments must live on the current CUDA device")
+        if t is not None:
+            dev = t.get_device()
+            if dev >= 0 and here is None:
+                here = torch.cuda.current_device()
+            if dev < 0 or dev != here:
+                raise PagedKVError("tensor arguments must live on the current CUDA device")
 
 
 # ---- index helpers ------------------------------------------------------------------
@@ -391,6 +414,10 @@ def paged_decode(query, kv_cache, workspace, block_tables, seq_lens, max_seq_len
     pages between them and the window are not read.  kv_scales: block scales
     of a float8_e4m3fn cache (see paged_append_scaled); each element stands
     for its value times its block's scale."""
+    if first_tokens or kv_scales is not None:
+        return _decode_window(query, kv_cache, workspace, block_tables, seq_lens, max_seq_len, bmm1_scale, bmm2_scale,
+                              window_left, sinks, kv_layout, q_len_per_req, out, lse, err_word, stream, max_q_len,
+                              cum_seq_lens_q, enable_pdl, first_tokens, kv_scales)
     layout = _layout_code(kv_layout)
     kp, vp, stride, P, Hkv, S, D, base = split_cache(kv_cache, layout)
     rows, Hqo, Dq = query.shape
@@ -409,22 +436,6 @@ def paged_decode(query, kv_cache, workspace, block_tables, seq_lens, max_seq_len
         _check_decode_args(query, out, lse, block_tables, seq_lens, B * q_len_per_req)
     s1, s1_dev = _scale_arg(bmm1_scale, query.device)
     s2, s2_dev = _scale_arg(bmm2_scale, query.device)
-    if first_tokens or kv_scales is not None:
-        ks = vs = None
-        ss = block = 0
-        if kv_scales is not None:
-            if base.dtype != torch.float8_e4m3fn:
-                raise PagedKVError("kv_scales belong to a float8_e4m3fn cache")
-            ks, vs, ss, block = split_scales(kv_scales, P, Hkv, S, base.device)
-        _same_device(query, base, workspace, block_tables, seq_lens, cum_seq_lens_q, sinks, out, lse, err_word)
-        mq = int(max_q_len) if cum_seq_lens_q is not None else q_len_per_req
-        _check(load_library().paged_decode_window(
-            _ptr(query), rows, kp, vp, stride, P, ks, vs, ss, block, _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _ptr(block_tables), block_tables.stride(0),
-            _ptr(seq_lens), B, max_seq_len, s1, s2, s1_dev, s2_dev, window_left, first_tokens, _ptr(sinks), mq,
-            _ptr(cum_seq_lens_q), Hqo, Hkv, D, S, layout, _decode_dtype(query, base), 1 if enable_pdl else 0,
-            _ptr(out), _ptr(lse), _ptr(err_word), _stream(stream)))
-        return out
     if s1_dev or s2_dev or enable_pdl:
         mq = int(max_q_len) if cum_seq_lens_q is not None else q_len_per_req
         _check(load_library().paged_decode_ex(
@@ -451,6 +462,56 @@ def paged_decode(query, kv_cache, workspace, block_tables, seq_lens, max_seq_len
         bmm2_scale, window_left, _ptr(sinks), q_len_per_req, Hqo, Hkv, D, S,
         layout, _decode_dtype(query, base), _ptr(out), _ptr(lse), _ptr(err_word),
         _stream(stream)))
+    return out
+
+
+def _decode_window(query, kv_cache, workspace, block_tables, seq_lens, max_seq_len, bmm1_scale, bmm2_scale, window_left,
+                   sinks, kv_layout, q_len_per_req, out, lse, err_word, stream, max_q_len, cum_seq_lens_q, enable_pdl,
+                   first_tokens, kv_scales):
+    """paged_decode under a window with first tokens and / or over a cache with
+    block scales."""
+    layout = _layout_code(kv_layout)
+    kp, vp, stride, P, Hkv, S, D, base = split_cache(kv_cache, layout)
+    rows, Hqo, Dq = query.shape
+    if Dq != D:
+        raise PagedKVError("query head_dim differs from the cache's")
+    B = seq_lens.shape[0]
+    dtype = _decode_dtype(query, base)
+    if isinstance(kv_cache, (tuple, list)) and (kv_cache[1].dtype != base.dtype or
+                                                kv_cache[1].get_device() != base.get_device()):
+        raise PagedKVError("K and V caches hold the same type on the same device")
+    ks = vs = None
+    ss = block = 0
+    if kv_scales is not None:
+        if dtype not in (F16_E4M3, BF16_E4M3):
+            raise PagedKVError("kv_scales belong to a float8_e4m3fn cache")
+        ks, vs, ss, block = split_scales(kv_scales, P, Hkv, S, base.device)
+    if out is None:
+        out = torch.empty_like(query)
+    if (cum_seq_lens_q is None) != (max_q_len is None):
+        raise PagedKVError("cum_seq_lens_q and max_q_len go together")
+    if cum_seq_lens_q is None:
+        max_q = q_len_per_req
+        _check_decode_args(query, out, lse, block_tables, seq_lens, B * max_q)
+    else:
+        max_q = int(max_q_len)
+        if cum_seq_lens_q.dtype != torch.int32 or tuple(cum_seq_lens_q.shape) != (B + 1,) \
+                or not cum_seq_lens_q.is_contiguous():
+            raise PagedKVError(f"cum_seq_lens_q must be contiguous int32 [{B + 1}]")
+        _check_decode_args(query, out, lse, block_tables, seq_lens, 0)
+    if not seq_lens.is_contiguous():
+        raise PagedKVError("seq_lens must be contiguous")
+    if sinks is not None and (sinks.dtype != torch.float32 or sinks.numel() != Hqo or not sinks.is_contiguous()):
+        raise PagedKVError(f"sinks must be contiguous float32 [{Hqo}]")
+    s1, s1_dev = _scale_arg(bmm1_scale, query.device)
+    s2, s2_dev = _scale_arg(bmm2_scale, query.device)
+    _same_device(query, base, workspace, block_tables, seq_lens, cum_seq_lens_q, sinks, out, lse, err_word)
+    _check(load_library().paged_decode_window(
+        query.data_ptr(), rows, kp, vp, stride, P, ks, vs, ss, block, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), block_tables.data_ptr(), block_tables.stride(0),
+        seq_lens.data_ptr(), B, max_seq_len, s1, s2, s1_dev, s2_dev, window_left, first_tokens, _ptr(sinks), max_q,
+        _ptr(cum_seq_lens_q), Hqo, Hkv, D, S, layout, dtype, 1 if enable_pdl else 0, out.data_ptr(), _ptr(lse),
+        _ptr(err_word), _stream(stream)))
     return out
 
 
@@ -628,9 +689,8 @@ def _prefill_window(q, k_cache, v_cache, scale, workspace, max_q, max_kv, lens_q
         raise PagedKVError("the caches hold the query's type, or float8_e4m3fn with kv_scales")
     if v_cache.shape[:-1] != k_cache.shape[:-1]:
         raise PagedKVError("K and V caches must have the same pages, heads and page size")
-    for t in (k_cache, v_cache):
-        if P > 0 and not t[0].is_contiguous():
-            raise PagedKVError("each page must be contiguous")
+    if not (_rows_contiguous(k_cache) and _rows_contiguous(v_cache)):
+        raise PagedKVError("each page must be contiguous")
     if out is None:
         out = torch.empty((total_q, Hqo, dv), dtype=q.dtype, device=q.device)
     if lse is None:

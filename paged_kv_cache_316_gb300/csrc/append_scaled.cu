@@ -37,10 +37,15 @@ constexpr int kAsWarps = 8;
 constexpr int kAsEntries = 16;
 constexpr int kAsMinExp = -40, kAsMaxExp = 40;
 
+// The pattern of infinity without sign: magnitudes from it on are not finite.
+template <typename T>
+__device__ __forceinline__ uint32_t inf_bits() {
+    return std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+}
 // Two finite-or-zero magnitudes (16-bit patterns without sign) of a pair.
 template <typename T>
 __device__ __forceinline__ uint32_t finite_mags(uint32_t w) {
-    constexpr uint32_t kInf = sizeof(T) && std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+    const uint32_t kInf = inf_bits<T>();
     uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
     lo = lo < kInf ? lo : 0u;
     hi = hi < kInf ? hi : 0u;
@@ -167,31 +172,43 @@ __global__ void __launch_bounds__(kAsWarps * 32) append_scaled_kernel(const Appe
             float *scale = p.scales[z] + rpage * p.scale_stride +
                            (static_cast<int64_t>(h) << (p.page_shift - p.block_shift)) + (slot0 >> p.block_shift);
             float was = in_block > 0 ? *scale : 0.f;  // (its latency overlaps the rows')
-            constexpr int kHeld = 8;
+            constexpr int kHeld = 8, kC = C_ ? C_ : 16;
+            constexpr uint32_t kMag = 0x7fff7fffu;
             const bool held = C_ != 0 && n * C <= kHeld * 32;
             uint4 v[kHeld];
             uint32_t mag = 0;
             if (held) {
+                // chunk q = lane + 32 k of the run: (C 16) row lane / 16 + 2 k
+                const uint16_t *at = src + (lane / kC) * src_row + (lane % kC) * 8;
 #pragma unroll
                 for (int k = 0; k < kHeld; ++k) {
-                    const int q = lane + 32 * k;
                     v[k] = make_uint4(0u, 0u, 0u, 0u);
-                    if (q < n * C) v[k] = __ldcs(reinterpret_cast<const uint4 *>(src + (q / C) * src_row + (q % C) * 8));
+                    if (lane + 32 * k < n * kC)
+                        v[k] = __ldcs(reinterpret_cast<const uint4 *>(at + static_cast<int64_t>(k * (32 / kC)) * src_row));
                 }
 #pragma unroll
-                for (int k = 0; k < kHeld; ++k) {
-                    mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(finite_mags<T>(v[k].x), finite_mags<T>(v[k].y)),
-                                                 __vmaxu2(finite_mags<T>(v[k].z), finite_mags<T>(v[k].w))));
-                }
+                for (int k = 0; k < kHeld; ++k)
+                    mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(v[k].x & kMag, v[k].y & kMag),
+                                                 __vmaxu2(v[k].z & kMag, v[k].w & kMag)));
             } else {
+                for (int q = lane; q < n * C; q += 32) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(src + (q / C) * src_row + (q % C) * 8);
+                    mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(x.x & kMag, x.y & kMag), __vmaxu2(x.z & kMag, x.w & kMag)));
+                }
+            }
+            mag = __vmaxu2(mag, mag >> 16) & 0xffffu;
+            mag = __reduce_max_sync(0xffffffffu, mag);
+            if (mag >= inf_bits<T>()) {  // an infinity or NaN among them: again, over the finite ones
+                mag = 0;
                 for (int q = lane; q < n * C; q += 32) {
                     const uint4 x = *reinterpret_cast<const uint4 *>(src + (q / C) * src_row + (q % C) * 8);
                     mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(finite_mags<T>(x.x), finite_mags<T>(x.y)),
                                                  __vmaxu2(finite_mags<T>(x.z), finite_mags<T>(x.w))));
                 }
+                mag = __vmaxu2(mag, mag >> 16) & 0xffffu;
+                mag = __reduce_max_sync(0xffffffffu, mag);
             }
-            mag = __vmaxu2(mag, mag >> 16) & 0xffffu;
-            const float amax = widen2<T>(__reduce_max_sync(0xffffffffu, mag)).x;
+            const float amax = widen2<T>(mag).x;
             // 2^e by its bits: e is in [-40, 40]
             float s = __uint_as_float(static_cast<uint32_t>(scale_exponent(amax) + 127) << 23);
             if (in_block > 0) {
@@ -226,9 +243,9 @@ __global__ void __launch_bounds__(kAsWarps * 32) append_scaled_kernel(const Appe
             if (held && pow2) {
 #pragma unroll
                 for (int k = 0; k < kHeld; ++k) {
-                    const int q = lane + 32 * k;
-                    if (q < n * C)
-                        *reinterpret_cast<uint2 *>(dst + (q / C) * dst_row + (q % C) * 8) = quantise8<T, true>(v[k], s);
+                    if (lane + 32 * k < n * kC)
+                        *reinterpret_cast<uint2 *>(dst + (lane / kC + k * (32 / kC)) * dst_row + (lane % kC) * 8) =
+                            quantise8<T, true>(v[k], s);
                 }
             } else {
                 for (int q = lane; q < n * C; q += 32) {
