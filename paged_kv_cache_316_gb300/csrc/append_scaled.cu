@@ -9,13 +9,13 @@
 //
 // The entries of one block form a run (consecutive positions); the first
 // entry of a run leads it.  A CTA takes kAsEntries entries (fewer when there
-// are few): in every warp lane j resolves entry j, so that the chain of index
-// reads runs once for all of a CTA's heads, then the warps share the heads of
-// K and V and take the runs that start in the CTA's entries one after another.
-// A run of up to 16 rows of 128 elements stays in registers between its
-// largest magnitude and its quantisation (eight 16-byte loads a lane, all in
-// flight), so every new value is read once; longer runs and other widths are
-// read twice, the second time from L2.
+// are few): its first warp resolves them, lane j entry j, so that the chain of
+// index reads runs once, and lists the runs that start there; then the warps
+// share out the heads of K and V and take run after run.  A run of up to 16
+// rows of 128 elements is staged through shared memory by the lanes that use
+// it (cp.async, the next run in flight while one is quantised; a lane reads
+// only what it copied, so no barrier is needed), so every new value is read
+// once.  Longer runs and other widths are read twice, the second time from L2.
 #include <type_traits>
 
 #include "pkv_common.cuh"
@@ -93,16 +93,20 @@ __device__ __forceinline__ uint2 quantise8(const uint4 &v, float s) {
     return make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
 }
 
-// C: 16-byte chunks of a source row (0: any, p.D / 8)
-template <typename T, int LAYOUT, int C_>
-__global__ void __launch_bounds__(kAsWarps * 32) append_scaled_kernel(const AppendScaledParams p) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// One run of entries: rows ri .. ri + n - 1 of the new tokens go to the slots
+// slot .. slot + n - 1 of a page, inside one block.
+struct AppendRun {
+    int64_t entry, page;
+    int n, slot;
+};
+
+// Lane j of the CTA's first warp resolves entry i0 + j; the runs that start in
+// the first p.entries of them are listed in `runs`, their number returned.
+__device__ __forceinline__ int list_runs(const AppendScaledParams &p, int64_t i0, bool report, AppendRun *runs) {
+    const int lane = threadIdx.x & 31;
     const int S = 1 << p.page_shift, G = 1 << p.block_shift;
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * p.entries;
-    // lane j: entry i0 + j (the CTA leads the runs that start in its first
-    // p.entries entries; the others tell where those runs end)
     const int64_t i = i0 + lane;
-    const bool report = warp == 0 && blockIdx.y == 0 && lane < p.entries && i < p.nnz;
+    report = report && lane < p.entries;
     int b = -1, pos = -1, most = 0;
     int64_t page = -1;
     bool leads = false;
@@ -140,122 +144,174 @@ __global__ void __launch_bounds__(kAsWarps * 32) append_scaled_kernel(const Appe
             }
         }
     }
-    // entry j + 1 goes on where entry j is
+    // bit j: entry j + 1 goes on where entry j is
     const int b_after = __shfl_down_sync(0xffffffffu, b, 1), pos_after = __shfl_down_sync(0xffffffffu, pos, 1);
     const unsigned joined = __ballot_sync(0xffffffffu, lane < 31 && b_after == b && pos_after == pos + 1);
-    const int C = C_ ? C_ : p.D / 8;
-    const int64_t src_row = static_cast<int64_t>(p.H) * p.D;
-    for (unsigned todo = __ballot_sync(0xffffffffu, leads); todo; todo &= todo - 1) {
-        const int j = __ffs(todo) - 1;
+    int n = min(most, __ffs(~(joined >> lane)));
+    unsigned open = __ballot_sync(0xffffffffu, leads && n < most && lane + n == 32);  // goes on past the lanes
+    for (; open; open &= open - 1) {
+        const int j = __ffs(open) - 1;
         const int rb = __shfl_sync(0xffffffffu, b, j), rpos = __shfl_sync(0xffffffffu, pos, j);
         const int rmost = __shfl_sync(0xffffffffu, most, j);
-        const int64_t rpage = __shfl_sync(0xffffffffu, page, j), ri = i0 + j;
-        // rows of the run: entries ri .. ri + n - 1
-        int n = min(rmost, __ffs(~(joined >> j)));
-        if (n < rmost && j + n == 32) {  // it goes on past the lanes' entries
-            while (n < rmost) {
-                const int k = n + lane;
-                const bool same = k < rmost && p.batch_indices[ri + k] == rb && p.positions[ri + k] == rpos + k;
-                const unsigned m = __ballot_sync(0xffffffffu, same);
-                if (m != 0xffffffffu) {
-                    n += __ffs(~m) - 1;
-                    break;
-                }
-                n += 32;
+        int m = __shfl_sync(0xffffffffu, n, j);
+        while (m < rmost) {
+            const int k = m + lane;
+            const bool same = k < rmost && p.batch_indices[i0 + j + k] == rb && p.positions[i0 + j + k] == rpos + k;
+            const unsigned all = __ballot_sync(0xffffffffu, same);
+            if (all != 0xffffffffu) {
+                m += __ffs(~all) - 1;
+                break;
+            }
+            m += 32;
+        }
+        if (lane == j) n = m;
+    }
+    const unsigned leaders = __ballot_sync(0xffffffffu, leads);
+    if (leads) {
+        AppendRun &r = runs[__popc(leaders & ((1u << lane) - 1))];
+        r.entry = i;
+        r.page = page;
+        r.n = n;
+        r.slot = pos & (S - 1);
+    }
+    return __popc(leaders);
+}
+
+constexpr int kAsHeld = 8;                        // staged 16-byte chunks of a lane
+constexpr int kAsStage = kAsHeld * 32 * 16;       // bytes of one warp's stage
+constexpr int kAsStages = 2;
+constexpr int kAsSmem = kAsWarps * kAsStages * kAsStage;
+
+// D128: rows of 128 elements (16 chunks of 16 bytes), short runs staged;
+// else any width, p.D / 8 chunks.
+template <typename T, int LAYOUT, bool D128>
+__global__ void __launch_bounds__(kAsWarps * 32) append_scaled_kernel(const AppendScaledParams p) {
+    extern __shared__ __align__(16) uint8_t stage_mem[];
+    __shared__ AppendRun runs[kAsEntries];
+    __shared__ int n_runs;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = 1 << p.page_shift, G = 1 << p.block_shift;
+    if (warp == 0) {
+        const int k = list_runs(p, static_cast<int64_t>(blockIdx.x) * p.entries, blockIdx.y == 0, runs);
+        if (lane == 0) n_runs = k;
+    }
+    __syncthreads();
+    const int C = D128 ? 16 : p.D / 8;
+    const int64_t src_row = static_cast<int64_t>(p.H) * p.D;
+    constexpr uint32_t kMag = 0x7fff7fffu;
+    uint8_t *stages = stage_mem + warp * (kAsStages * kAsStage) + lane * 16;  // chunk k at 512 k
+
+    // the warp's items: run by run, heads hk0, hk0 + step, .. of K then V
+    const int hk0 = blockIdx.y * kAsWarps + warp, step = gridDim.y * kAsWarps;
+    const int total_runs = hk0 < 2 * p.H ? n_runs : 0;
+    auto chunk_row = [&](int k) { return (lane >> 4) + 2 * k; };  // (D128) row of the lane's chunk k
+    auto source = [&](const AppendRun &r, int hk) {
+        return p.src[hk >= p.H] + (r.entry * p.H + (hk >= p.H ? hk - p.H : hk)) * static_cast<int64_t>(p.D);
+    };
+    auto issue = [&](int run, int hk, int st) {
+        if constexpr (D128) {
+            if (run < total_runs && runs[run].n <= 2 * kAsHeld) {
+                const int n = runs[run].n;
+                const uint16_t *at = source(runs[run], hk) + (lane >> 4) * src_row + (lane & 15) * 8;
+                const uint32_t to = smem_u32(stages + st * kAsStage);
+#pragma unroll
+                for (int k = 0; k < kAsHeld; ++k)
+                    if (chunk_row(k) < n) cp_async_16(to + 512 * k, at + 2 * k * src_row, true);
+            }
+            cp_async_commit();
+        }
+    };
+    issue(0, hk0, 0);
+    int st = 0;
+    for (int run = 0, hk = hk0; run < total_runs;) {
+        int run2 = run, hk2 = hk + step;  // the next item
+        if (hk2 >= 2 * p.H) {
+            ++run2;
+            hk2 = hk0;
+        }
+        const AppendRun r = runs[run];
+        const int n = r.n, in_block = r.slot & (G - 1);
+        const int z = hk >= p.H ? 1 : 0, h = hk - z * p.H;
+        float *scale = p.scales[z] + r.page * p.scale_stride + (static_cast<int64_t>(h) << (p.page_shift - p.block_shift)) +
+                       (r.slot >> p.block_shift);
+        float was = in_block > 0 ? *scale : 0.f;
+        issue(run2, hk2, st ^ 1);
+        const uint16_t *src = source(r, hk);
+        const bool held = D128 && n <= 2 * kAsHeld;
+        uint4 v[kAsHeld];
+        uint32_t mag = 0;
+        if (held) {
+            cp_async_wait<1>();
+#pragma unroll
+            for (int k = 0; k < kAsHeld; ++k) {
+                v[k] = make_uint4(0u, 0u, 0u, 0u);
+                if (chunk_row(k) < n) v[k] = *reinterpret_cast<const uint4 *>(stages + st * kAsStage + 512 * k);
+                mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(v[k].x & kMag, v[k].y & kMag), __vmaxu2(v[k].z & kMag, v[k].w & kMag)));
+            }
+        } else {
+            for (int q = lane; q < n * C; q += 32) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(src + (q / C) * src_row + (q % C) * 8);
+                mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(x.x & kMag, x.y & kMag), __vmaxu2(x.z & kMag, x.w & kMag)));
             }
         }
-        const int slot0 = rpos & (S - 1), in_block = rpos & (G - 1);
-        for (int hk = blockIdx.y * kAsWarps + warp; hk < 2 * p.H; hk += gridDim.y * kAsWarps) {
-            const int z = hk >= p.H ? 1 : 0, h = hk - z * p.H;
-            const uint16_t *src = p.src[z] + (ri * p.H + h) * static_cast<int64_t>(p.D);
-            uint8_t *cache = p.cache[z];
-            float *scale = p.scales[z] + rpage * p.scale_stride +
-                           (static_cast<int64_t>(h) << (p.page_shift - p.block_shift)) + (slot0 >> p.block_shift);
-            float was = in_block > 0 ? *scale : 0.f;  // (its latency overlaps the rows')
-            constexpr int kHeld = 8, kC = C_ ? C_ : 16;
-            constexpr uint32_t kMag = 0x7fff7fffu;
-            const bool held = C_ != 0 && n * C <= kHeld * 32;
-            uint4 v[kHeld];
-            uint32_t mag = 0;
-            if (held) {
-                // chunk q = lane + 32 k of the run: (C 16) row lane / 16 + 2 k
-                const uint16_t *at = src + (lane / kC) * src_row + (lane % kC) * 8;
-#pragma unroll
-                for (int k = 0; k < kHeld; ++k) {
-                    v[k] = make_uint4(0u, 0u, 0u, 0u);
-                    if (lane + 32 * k < n * kC)
-                        v[k] = __ldcs(reinterpret_cast<const uint4 *>(at + static_cast<int64_t>(k * (32 / kC)) * src_row));
-                }
-#pragma unroll
-                for (int k = 0; k < kHeld; ++k)
-                    mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(v[k].x & kMag, v[k].y & kMag),
-                                                 __vmaxu2(v[k].z & kMag, v[k].w & kMag)));
-            } else {
-                for (int q = lane; q < n * C; q += 32) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(src + (q / C) * src_row + (q % C) * 8);
-                    mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(x.x & kMag, x.y & kMag), __vmaxu2(x.z & kMag, x.w & kMag)));
-                }
+        mag = __vmaxu2(mag, mag >> 16) & 0xffffu;
+        mag = __reduce_max_sync(0xffffffffu, mag);
+        if (mag >= inf_bits<T>()) {  // an infinity or NaN among them: again, over the finite ones
+            mag = 0;
+            for (int q = lane; q < n * C; q += 32) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(src + (q / C) * src_row + (q % C) * 8);
+                mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(finite_mags<T>(x.x), finite_mags<T>(x.y)),
+                                             __vmaxu2(finite_mags<T>(x.z), finite_mags<T>(x.w))));
             }
             mag = __vmaxu2(mag, mag >> 16) & 0xffffu;
             mag = __reduce_max_sync(0xffffffffu, mag);
-            if (mag >= inf_bits<T>()) {  // an infinity or NaN among them: again, over the finite ones
-                mag = 0;
-                for (int q = lane; q < n * C; q += 32) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(src + (q / C) * src_row + (q % C) * 8);
-                    mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(finite_mags<T>(x.x), finite_mags<T>(x.y)),
-                                                 __vmaxu2(finite_mags<T>(x.z), finite_mags<T>(x.w))));
-                }
-                mag = __vmaxu2(mag, mag >> 16) & 0xffffu;
-                mag = __reduce_max_sync(0xffffffffu, mag);
-            }
-            const float amax = widen2<T>(mag).x;
-            // 2^e by its bits: e is in [-40, 40]
-            float s = __uint_as_float(static_cast<uint32_t>(scale_exponent(amax) + 127) << 23);
-            if (in_block > 0) {
-                was = checked_scale(was, p.err);
-                s = fmaxf(s, was);
-            } else {
-                was = s;
-            }
-            __syncwarp();
-            if (lane == 0) *scale = s;
-            if (s > was) {  // earlier tokens of the block, rounded again under the larger scale
-                const float r = was / s;
-                for (int q = lane; q < in_block * C; q += 32) {
-                    uint8_t *at = cache +
-                                  kv_row_offset<LAYOUT>(rpage, p.page_stride, h, slot0 - in_block + q / C, p.H, S, p.D) +
-                                  (q % C) * 8;
-                    const uint2 x = *reinterpret_cast<const uint2 *>(at);
-                    const uint32_t w[2] = {x.x, x.y};
-                    uint32_t o[2];
+        }
+        // 2^e by its bits: e is in [-40, 40]
+        float s = __uint_as_float(static_cast<uint32_t>(scale_exponent(widen2<T>(mag).x) + 127) << 23);
+        if (in_block > 0) {
+            was = checked_scale(was, p.err);
+            s = fmaxf(s, was);
+        } else {
+            was = s;
+        }
+        __syncwarp();
+        if (lane == 0) *scale = s;
+        uint8_t *dst = p.cache[z] + kv_row_offset<LAYOUT>(r.page, p.page_stride, h, r.slot, p.H, S, p.D);
+        const int64_t dst_row = LAYOUT == PKV_HND ? p.D : src_row;
+        if (s > was) {  // earlier tokens of the block, rounded again under the larger scale
+            const float ratio = was / s;
+            for (int q = lane; q < in_block * C; q += 32) {
+                uint8_t *at = dst + (q / C - in_block) * dst_row + (q % C) * 8;
+                const uint2 x = *reinterpret_cast<const uint2 *>(at);
+                const uint32_t w[2] = {x.x, x.y};
+                uint32_t o[2];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float2 lo = widen2<__half>(widen_e4m3x2<__half>(w[k] & 0xffffu));
-                        const float2 hi = widen2<__half>(widen_e4m3x2<__half>(w[k] >> 16));
-                        o[k] = to_e4m3x2(lo.x * r, lo.y * r) | to_e4m3x2(hi.x * r, hi.y * r) << 16;
-                    }
-                    *reinterpret_cast<uint2 *>(at) = make_uint2(o[0], o[1]);
+                for (int k = 0; k < 2; ++k) {
+                    const float2 lo = widen2<__half>(widen_e4m3x2<__half>(w[k] & 0xffffu));
+                    const float2 hi = widen2<__half>(widen_e4m3x2<__half>(w[k] >> 16));
+                    o[k] = to_e4m3x2(lo.x * ratio, lo.y * ratio) | to_e4m3x2(hi.x * ratio, hi.y * ratio) << 16;
                 }
-            }
-            const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0;
-            uint8_t *dst = cache + kv_row_offset<LAYOUT>(rpage, p.page_stride, h, slot0, p.H, S, p.D);
-            const int64_t dst_row = LAYOUT == PKV_HND ? p.D : src_row;
-            if (held && pow2) {
-#pragma unroll
-                for (int k = 0; k < kHeld; ++k) {
-                    if (lane + 32 * k < n * kC)
-                        *reinterpret_cast<uint2 *>(dst + (lane / kC + k * (32 / kC)) * dst_row + (lane % kC) * 8) =
-                            quantise8<T, true>(v[k], s);
-                }
-            } else {
-                for (int q = lane; q < n * C; q += 32) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(src + (q / C) * src_row + (q % C) * 8);
-                    *reinterpret_cast<uint2 *>(dst + (q / C) * dst_row + (q % C) * 8) =
-                        pow2 ? quantise8<T, true>(x, s) : quantise8<T, false>(x, s);
-                }
+                *reinterpret_cast<uint2 *>(at) = make_uint2(o[0], o[1]);
             }
         }
+        const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0;
+        if (held && pow2) {
+            uint8_t *at = dst + (lane >> 4) * dst_row + (lane & 15) * 8;
+#pragma unroll
+            for (int k = 0; k < kAsHeld; ++k)
+                if (chunk_row(k) < n) *reinterpret_cast<uint2 *>(at + 2 * k * dst_row) = quantise8<T, true>(v[k], s);
+        } else {
+            for (int q = lane; q < n * C; q += 32) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(src + (q / C) * src_row + (q % C) * 8);
+                *reinterpret_cast<uint2 *>(dst + (q / C) * dst_row + (q % C) * 8) =
+                    pow2 ? quantise8<T, true>(x, s) : quantise8<T, false>(x, s);
+            }
+        }
+        run = run2;
+        hk = hk2;
+        st ^= 1;
     }
+    if constexpr (D128) cp_async_wait<0>();
 }
 
 }  // namespace pkv
@@ -322,16 +378,20 @@ extern "C" int paged_append_scaled(const void *append_key, const void *append_va
     const int most_y = (2 * num_kv_heads + kAsWarps - 1) / kAsWarps;
     const int64_t gy = (want + gx - 1) / gx;
     const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy < most_y ? gy : most_y));
-    auto pick = [&](auto kd, auto ka) { return head_dim == 128 ? kd : ka; };
+    const bool d128 = head_dim == 128;
+    auto pick = [&](auto k128, auto any) { return d128 ? k128 : any; };
     auto kern = dtype == PKV_BF16
-                    ? (layout == PKV_HND ? pick(append_scaled_kernel<__nv_bfloat16, PKV_HND, 16>,
-                                                append_scaled_kernel<__nv_bfloat16, PKV_HND, 0>)
-                                         : pick(append_scaled_kernel<__nv_bfloat16, PKV_NHD, 16>,
-                                                append_scaled_kernel<__nv_bfloat16, PKV_NHD, 0>))
+                    ? (layout == PKV_HND ? pick(append_scaled_kernel<__nv_bfloat16, PKV_HND, true>,
+                                                append_scaled_kernel<__nv_bfloat16, PKV_HND, false>)
+                                         : pick(append_scaled_kernel<__nv_bfloat16, PKV_NHD, true>,
+                                                append_scaled_kernel<__nv_bfloat16, PKV_NHD, false>))
                     : (layout == PKV_HND
-                           ? pick(append_scaled_kernel<__half, PKV_HND, 16>, append_scaled_kernel<__half, PKV_HND, 0>)
-                           : pick(append_scaled_kernel<__half, PKV_NHD, 16>, append_scaled_kernel<__half, PKV_NHD, 0>));
-    kern<<<grid, kAsWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(p);
+                           ? pick(append_scaled_kernel<__half, PKV_HND, true>, append_scaled_kernel<__half, PKV_HND, false>)
+                           : pick(append_scaled_kernel<__half, PKV_NHD, true>, append_scaled_kernel<__half, PKV_NHD, false>));
+    const size_t smem = d128 ? kAsSmem : 0;
+    if (d128 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+        return PKV_ERR_CUDA;
+    kern<<<grid, kAsWarps * 32, smem, static_cast<cudaStream_t>(stream)>>>(p);
     note_launches(1);
     return launch_status();
 }
