@@ -33,7 +33,7 @@ struct AppendScaledParams {
     int32_t *err;
 };
 
-constexpr int kAsWarps = 8;
+constexpr int kAsWarps = 8;  // two CTAs of 8 warps per SM: three measured slower
 constexpr int kAsEntries = 16;
 constexpr int kAsMinExp = -40, kAsMaxExp = 40;
 
@@ -78,17 +78,31 @@ __device__ __forceinline__ int scale_exponent(float a) {
     return min(max(e, kAsMinExp), kAsMaxExp);
 }
 
-// Eight 16-bit values over s -> eight codes: as products with 1 / s (EXACT:
-// s is a power of two), else as quotients.
-template <typename T, bool EXACT>
+// Eight 16-bit values over s -> eight codes.  kQuotient: divided out.
+// kProduct (s a power of two, as a scale is unless the caller brought another
+// kind): products with 1 / s in fp32, exact.  kHalf (fp16 values, s in
+// [2^-15, 2^24]): the same products in fp16, two to an instruction and without
+// widening; they are exact down to 2^-14, and a smaller quotient becomes code
+// 0 either way (E4M3's smallest value is 2^-9); one beyond fp16's range
+// becomes infinite and saturates as it does in fp32.
+enum { kQuotient, kProduct, kHalf };
+template <typename T, int HOW>
 __device__ __forceinline__ uint2 quantise8(const uint4 &v, float s) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    const float inv = EXACT ? __uint_as_float((254u << 23) - __float_as_uint(s)) : 0.f;
+    const float inv = HOW == kQuotient ? 0.f : __uint_as_float((254u << 23) - __float_as_uint(s));
     uint32_t o[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const float2 f = widen2<T>(w[k]);
-        o[k] = EXACT ? to_e4m3x2(f.x * inv, f.y * inv) : to_e4m3x2(f.x / s, f.y / s);
+        if constexpr (HOW == kHalf) {
+            const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(&w[k]), __float2half2_rn(inv));
+            uint16_t r;
+            asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;\n" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t *>(&x)));
+            o[k] = r;
+        } else {
+            float2 f = widen2<T>(w[k]);
+            f = HOW == kProduct ? __fmul2_rn(f, make_float2(inv, inv)) : make_float2(f.x / s, f.y / s);
+            o[k] = to_e4m3x2(f.x, f.y);
+        }
     }
     return make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
 }
@@ -179,13 +193,13 @@ __device__ __forceinline__ int list_runs(const AppendScaledParams &p, int64_t i0
 
 constexpr int kAsHeld = 8;                        // staged 16-byte chunks of a lane
 constexpr int kAsStage = kAsHeld * 32 * 16;       // bytes of one warp's stage
-constexpr int kAsStages = 2;
+constexpr int kAsStages = 3;
 constexpr int kAsSmem = kAsWarps * kAsStages * kAsStage;
 
 // D128: rows of 128 elements (16 chunks of 16 bytes), short runs staged;
 // else any width, p.D / 8 chunks.
 template <typename T, int LAYOUT, bool D128>
-__global__ void __launch_bounds__(kAsWarps * 32) append_scaled_kernel(const AppendScaledParams p) {
+__global__ void __launch_bounds__(kAsWarps * 32, 2) append_scaled_kernel(const AppendScaledParams p) {
     extern __shared__ __align__(16) uint8_t stage_mem[];
     __shared__ AppendRun runs[kAsEntries];
     __shared__ int n_runs;
@@ -221,27 +235,34 @@ __global__ void __launch_bounds__(kAsWarps * 32) append_scaled_kernel(const Appe
             cp_async_commit();
         }
     };
-    issue(0, hk0, 0);
+    auto next = [&](int &run, int &hk) {
+        hk += step;
+        if (hk >= 2 * p.H) {
+            ++run;
+            hk = hk0;
+        }
+    };
+    int run3 = 0, hk3 = hk0;  // the item after the ones in flight
+    issue(run3, hk3, 0);
+    next(run3, hk3);
+    issue(run3, hk3, 1);
+    next(run3, hk3);
     int st = 0;
     for (int run = 0, hk = hk0; run < total_runs;) {
-        int run2 = run, hk2 = hk + step;  // the next item
-        if (hk2 >= 2 * p.H) {
-            ++run2;
-            hk2 = hk0;
-        }
         const AppendRun r = runs[run];
         const int n = r.n, in_block = r.slot & (G - 1);
         const int z = hk >= p.H ? 1 : 0, h = hk - z * p.H;
         float *scale = p.scales[z] + r.page * p.scale_stride + (static_cast<int64_t>(h) << (p.page_shift - p.block_shift)) +
                        (r.slot >> p.block_shift);
         float was = in_block > 0 ? *scale : 0.f;
-        issue(run2, hk2, st ^ 1);
+        issue(run3, hk3, st == 0 ? 2 : st - 1);
+        next(run3, hk3);
         const uint16_t *src = source(r, hk);
         const bool held = D128 && n <= 2 * kAsHeld;
         uint4 v[kAsHeld];
         uint32_t mag = 0;
         if (held) {
-            cp_async_wait<1>();
+            cp_async_wait<2>();
 #pragma unroll
             for (int k = 0; k < kAsHeld; ++k) {
                 v[k] = make_uint4(0u, 0u, 0u, 0u);
@@ -295,21 +316,22 @@ __global__ void __launch_bounds__(kAsWarps * 32) append_scaled_kernel(const Appe
             }
         }
         const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0;
-        if (held && pow2) {
+        constexpr bool kFp16 = std::is_same<T, __half>::value;
+        if (held && pow2 && (!kFp16 || (s >= 0x1p-15f && s <= 0x1p24f))) {
             uint8_t *at = dst + (lane >> 4) * dst_row + (lane & 15) * 8;
 #pragma unroll
             for (int k = 0; k < kAsHeld; ++k)
-                if (chunk_row(k) < n) *reinterpret_cast<uint2 *>(at + 2 * k * dst_row) = quantise8<T, true>(v[k], s);
+                if (chunk_row(k) < n)
+                    *reinterpret_cast<uint2 *>(at + 2 * k * dst_row) = quantise8<T, kFp16 ? kHalf : kProduct>(v[k], s);
         } else {
             for (int q = lane; q < n * C; q += 32) {
                 const uint4 x = *reinterpret_cast<const uint4 *>(src + (q / C) * src_row + (q % C) * 8);
                 *reinterpret_cast<uint2 *>(dst + (q / C) * dst_row + (q % C) * 8) =
-                    pow2 ? quantise8<T, true>(x, s) : quantise8<T, false>(x, s);
+                    pow2 ? quantise8<T, kProduct>(x, s) : quantise8<T, kQuotient>(x, s);
             }
         }
-        run = run2;
-        hk = hk2;
-        st ^= 1;
+        next(run, hk);
+        st = st == 2 ? 0 : st + 1;
     }
     if constexpr (D128) cp_async_wait<0>();
 }

@@ -94,6 +94,18 @@ def test_scale_that_is_no_power_of_two_and_grows():
     run(c)
 
 
+@pytest.mark.parametrize("exp", [-15, -16, -30, 8, 24, 25, 40])
+def test_earlier_scale_at_the_ends_of_its_range(exp):
+    # fp16 values of every exponent (subnormal ones too) under one held scale
+    c = case([11], [5], 16, 16, 2, 128, wl.HND, torch.float16, 22)
+    g = wl.generator(23)
+    m = torch.exp2(torch.randint(-24, 15, c["key"].shape, generator=g).float())
+    c["key"] = (m * (1 + torch.rand(m.shape, generator=g))).half()
+    c["value"] = (-m * 1.5 * 2.0 ** -10).half()
+    c["scales"][:] = 2.0 ** exp
+    run(c)
+
+
 def test_earlier_scale_out_of_range_is_flagged_and_clamped():
     c = case([2, 2], [3, 5], 16, 16, 2, 128, wl.NHD, torch.bfloat16, 13)
     for b, x in ((0, float("nan")), (1, 0.0)):
