@@ -30,10 +30,13 @@ constexpr int kDecTile = 64;                      // keys per pipeline stage
 // CTAs per SM with a 2-stage ring; more row tiles need more registers: 2
 // CTAs per SM, 3 stages.  An E4M3 stage is half as large, so its ring is 4
 // stages deep at the same CTA counts.
-template <int MT, bool KV8 = false>
+// With swapped operands (SW 8-row tiles, see the split kernel) and 32 rows the
+// output takes 128 registers a lane: 2 CTAs.
+template <int MT, bool KV8 = false, int SW = 0>
 struct DecCfg {
     static constexpr int STAGES = KV8 ? 4 : (MT == 1 ? 2 : 3);
-    static constexpr int CTAS = MT == 1 ? 3 : 2;
+    static constexpr int CTAS = MT == 1 && SW < 4 ? 3 : 2;
+    static constexpr int ROWS = SW == 4 ? 32 : 16 * MT;  // query rows of a CTA
 };
 constexpr int kDecThreads = 128;
 constexpr int kDecRowBytes = kDecD * 2;           // one K or V row
@@ -160,15 +163,15 @@ __device__ __forceinline__ void store4(T *dst, float a, float b, float c, float 
     *reinterpret_cast<uint2 *>(dst) = v;
 }
 
-// SW (an E4M3 cache and at most 8 query rows): the MMAs take the keys as
-// their 16-row side, S^T = K Q^T and O^T = V^T P^T (see the tile loop).
+// SW > 0 (an E4M3 cache and at most 8 SW query rows): the MMAs take the keys
+// as their 16-row side, S^T = K Q^T and O^T = V^T P^T (see the tile loop).
 // EXT: 0 all keys or a window; 1 a window and first tokens; 2 the same over
 // an E4M3 cache with a scale for each block of keys and head.
-template <typename T, int MT, int LAYOUT, bool KV8, bool SW = false, int EXT = 0>
-__global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8>::CTAS) decode_split_kernel(const DecodeParams p) {
+template <typename T, int MT, int LAYOUT, bool KV8, int SW = 0, int EXT = 0>
+__global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8, SW>::CTAS) decode_split_kernel(const DecodeParams p) {
     constexpr bool FIRST = EXT >= 1, SCL = EXT == 2;
     static_assert(!SCL || KV8, "block scales: E4M3 cache");
-    constexpr int kDecStages = DecCfg<MT, KV8>::STAGES;
+    constexpr int kDecStages = DecCfg<MT, KV8, SW>::STAGES;
     constexpr int STAGE_BYTES = DecSmem<KV8>::STAGE;
     // the MMA element type: over an E4M3 cache always fp16 (E4M3 widens to
     // fp16 in one instruction; a bf16 query is brought to fp16 exactly, see
@@ -178,7 +181,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8>::CTAS) decode_spl
     constexpr int NKG = 4 / MT;          // warps that split the keys of a tile
     constexpr int KPW = kDecTile / NKG;  // keys per warp per tile
     constexpr int NT = KPW / 8;          // 8-key score tiles per warp
-    constexpr int ROWS = 16 * MT;
+    constexpr int ROWS = DecCfg<MT, KV8, SW>::ROWS;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *q_s = smem + kDecStages * STAGE_BYTES;
     uint8_t *kvalid = q_s + ROWS * kDecRowBytes;
@@ -487,19 +490,23 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8>::CTAS) decode_spl
         __syncthreads();
     }
 
-    uint32_t qa[8][4];
-    if constexpr (SW) {
-        // B operand of the swapped QK (Q^T, k = head dim, n = query row):
-        // lane (g, c) holds row g, dims 32c + 4kk + {0, 1} and {2, 3} of
-        // k-step kk (the permuted order of the K rows, below)
+    uint32_t qa[SW ? 1 : 8][4];
+    uint32_t qb[SW ? SW : 1][8][2];  // (SW) Q^T fragments of each 8-row tile
+    if constexpr (SW > 0) {
+        // B operand of the swapped QK (Q^T, k = head dim, n = query row): lane
+        // (g, c) holds row 8u + g, dims 32c + 4kk + {0, 1} and {2, 3} of k-step
+        // kk (the permuted order of the K rows, below)
         const int gq = lane >> 2, cq = lane & 3;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-            const int dim = cq * 32 + kk * 4;
-            const uint2 lo = *reinterpret_cast<const uint2 *>(q_s + swz(gq, dim >> 3, kDecRowBytes) + (dim & 7) * 2);
-            qa[kk][0] = lo.x;
-            qa[kk][1] = lo.y;
-        }
+        for (int u = 0; u < SW; ++u)
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+                const int dim = cq * 32 + kk * 4;
+                const uint2 q2 =
+                    *reinterpret_cast<const uint2 *>(q_s + swz(8 * u + gq, dim >> 3, kDecRowBytes) + (dim & 7) * 2);
+                qb[u][kk][0] = q2.x;
+                qb[u][kk][1] = q2.y;
+            }
     } else if constexpr (KV8) {
         // Over an E4M3 cache the head dimension is taken in a permuted order,
         // the same for Q and K (a dot product does not depend on it): the k
@@ -533,16 +540,31 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8>::CTAS) decode_spl
     const int lo1 = p.window_left >= 0 ? max(0, pos1 - p.window_left) : 0;
     const int lo_max = p.window_left >= 0 ? max(0, L - 1 - p.window_left) : 0;
     const int hi_min = FIRST ? L - Q : min(L - Q, k_end - 1);
-    // (swapped operands: lane (g, c) holds query rows 2c and 2c + 1)
-    const int sr0 = 2 * (lane & 3), sr1 = sr0 + 1;
-    const int spos0 = L - Q + min(sr0 / p.group, Q - 1), spos1 = L - Q + min(sr1 / p.group, Q - 1);
-    const int slo0 = p.window_left >= 0 ? max(0, spos0 - p.window_left) : 0;
-    const int slo1 = p.window_left >= 0 ? max(0, spos1 - p.window_left) : 0;
+    // (swapped operands: lane (g, c) holds query rows 8u + 2c and 8u + 2c + 1
+    // of row tile u; (lowest key of the window, position) of every row)
+    const int sr0 = 2 * (lane & 3);
+    constexpr float kNoKey = -3e38f;
+    __shared__ __align__(16) int2 row_bounds[SW > 0 ? ROWS : 1];
+    if constexpr (SW > 0) {
+        if (tid < ROWS) {
+            const int pos = L - Q + min(tid / p.group, Q - 1);
+            row_bounds[tid] = make_int2(p.window_left >= 0 ? max(0, pos - p.window_left) : 0, pos);
+        }
+        __syncthreads();
+    }
 
-    float o[16][4];
+    // output: n-tiles of 8 dims, or (SW) 8 m-tiles of 16 dims for each row tile
+    constexpr int NO = SW ? 8 * SW : 16;
+    float o[NO][4];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    for (int i = 0; i < NO; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float ms[SW ? SW : 1][2], ls[SW ? SW : 1][2];  // (SW) the same for each row tile
+#pragma unroll
+    for (int u = 0; u < SW; ++u) {
+        ms[u][0] = ms[u][1] = kNoKey;  // (finite: a masked score's distance to it is -inf)
+        ls[u][0] = ls[u][1] = 0.f;
+    }
 
     // a key at or after a row's window start, or one of the first tokens
     auto from = [&](int j, int row_lo) { return j >= row_lo || (FIRST && j < p.first_tokens); };
@@ -570,15 +592,21 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8>::CTAS) decode_spl
         const uint8_t *k8 = smem + stage * STAGE_BYTES;  // E4M3 K rows (KV8)
         const uint8_t *v8 = k8 + kDec8TileBytes;         // E4M3 V rows (KV8)
 
-        if constexpr (SW) {
-            // Swapped operands for at most 8 query rows: S^T (the warp's 16
-            // keys x 8 rows) = K Q^T and O^T (128 dims x 8 rows) += V^T P^T,
-            // so that the keys fill the MMA's 16-row side and half as many
-            // MMAs cover a tile.  Lane (g, c) = (lane / 4, lane % 4) holds
-            // the scores of keys kw0 + g and kw0 + g + 8 for query rows 2c
-            // and 2c + 1; rows at or beyond R are padding, masked out.
+        if constexpr (SW > 0) {
+            // Swapped operands for at most 8 SW query rows: S^T (the warp's 16
+            // keys x 8 rows) = K Q^T and O^T (128 dims x 8 rows) += V^T P^T for
+            // each 8-row tile u, so that the keys fill the MMA's 16-row side
+            // and a K or V value is widened once for all row tiles.  Lane
+            // (g, c) = (lane / 4, lane % 4) holds the scores of keys kw0 + g and
+            // kw0 + g + 8 for query rows 8u + 2c and 8u + 2c + 1; rows at or
+            // beyond R are padding that nothing reads.
             const int g = lane >> 2, c = lane & 3;
-            float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};  // even / odd k-steps
+            constexpr int CH = SW <= 2 ? 2 : 1;  // MMA chains of a row tile's scores (even / odd k-steps)
+            float sc[SW][CH][4];
+#pragma unroll
+            for (int u = 0; u < SW; ++u)
+#pragma unroll
+                for (int i = 0; i < CH; ++i) sc[u][i][0] = sc[u][i][1] = sc[u][i][2] = sc[u][i][3] = 0.f;
             {
                 // A = K rows kw0 + g and kw0 + g + 8: the word at byte
                 // 32c + 4kk of a row holds dims 32c + 4kk .. + 3, both halves
@@ -594,15 +622,11 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8>::CTAS) decode_spl
                 for (int kk = 0; kk < 8; ++kk) {
                     const uint32_t a[4] = {widen_e4m3x2<TM>(wa[kk] & 0xffffu), widen_e4m3x2<TM>(wb[kk] & 0xffffu),
                                            widen_e4m3x2<TM>(wa[kk] >> 16), widen_e4m3x2<TM>(wb[kk] >> 16)};
-                    if (kk & 1)
-                        mma16816<TM>(sb, a, qa[kk][0], qa[kk][1]);
-                    else
-                        mma16816<TM>(sa, a, qa[kk][0], qa[kk][1]);
+#pragma unroll
+                    for (int u = 0; u < SW; ++u) mma16816<TM>(sc[u][kk & (CH - 1)], a, qb[u][kk][0], qb[u][kk][1]);
                 }
             }
-            // element e: key kw0 + g + 8 (e / 2), query row 2c + (e % 2)
-            float sv[4];
-            float kmA = 0.f, kmB = 0.f, lvA = 0.f, lvB = 0.f, ivA = 1.f, ivB = 1.f;
+            float kmA = scale_log2, kmB = scale_log2, lvA = 0.f, lvB = 0.f, ivA = 1.f, ivB = 1.f;
             if constexpr (SCL) {
                 const float2 fA = scales_of(j0, j0 + kw0), fB = scales_of(j0, j0 + kw0 + 8);
                 kmA = fA.x * scale_log2;
@@ -614,53 +638,74 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8>::CTAS) decode_spl
             }
             const bool interior = !any_bad[kg] && (j0 >= lo_max || (FIRST && j0 + kDecTile <= p.first_tokens)) &&
                                   j0 + kDecTile - 1 <= hi_min;
+            // element e of a row tile: key kw0 + g + 8 (e / 2), query row 8u + 2c + (e % 2)
+            float sv[SW][4];
+            bool higher = false;  // a score more than 2^8 above its row's maximum
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float x = SCL ? fmaf(sa[e] + sb[e], e & 2 ? kmB : kmA, e & 2 ? lvB : lvA) : (sa[e] + sb[e]) * scale_log2;
-                const int jj = kw0 + g + 8 * (e >> 1), j = j0 + jj;
-                bool vis = (e & 1 ? sr1 : sr0) < R;
-                if (!interior)
-                    vis = vis && kvalid[stage * kDecTile + jj] &&
-                          (e & 1 ? (from(j, slo1) && j <= spos1) : (from(j, slo0) && j <= spos0));
-                sv[e] = vis ? x : -INFINITY;
-            }
-            // row maxima over the warp's 16 keys (the lanes of one c)
-            float mx0 = fmaxf(sv[0], sv[2]), mx1 = fmaxf(sv[1], sv[3]);
+            for (int u = 0; u < SW; ++u) {
 #pragma unroll
-            for (int o_ = 4; o_ < 32; o_ <<= 1) {
-                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o_));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o_));
-            }
-            const float mn0 = mx0 > m0 + 8.f ? mx0 : m0, mn1 = mx1 > m1 + 8.f ? mx1 : m1;
-            const float base0 = mn0 == -INFINITY ? 0.f : mn0;
-            const float base1 = mn1 == -INFINITY ? 0.f : mn1;
-            const float al0 = fast_exp2(m0 - base0), al1 = fast_exp2(m1 - base1);
-            const float p0 = fast_exp2(sv[0] - base0), p1 = fast_exp2(sv[1] - base1);
-            const float p2 = fast_exp2(sv[2] - base0), p3 = fast_exp2(sv[3] - base1);
-            // (this lane's keys; summed over g at the end)
-            l0 = l0 * al0 + (SCL ? fmaf(p0, ivA, p2 * ivB) : p0 + p2);
-            l1 = l1 * al1 + (SCL ? fmaf(p1, ivA, p3 * ivB) : p1 + p3);
-            m0 = mn0;
-            m1 = mn1;
-            if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    o[i][0] *= al0;
-                    o[i][2] *= al0;
-                    o[i][1] *= al1;
-                    o[i][3] *= al1;
+                for (int e = 0; e < 4; ++e) {
+                    const float x0 = CH == 2 ? sc[u][0][e] + sc[u][CH - 1][e] : sc[u][0][e];
+                    const float x = SCL ? fmaf(x0, e & 2 ? kmB : kmA, e & 2 ? lvB : lvA) : x0 * scale_log2;
+                    sv[u][e] = x;
                 }
             }
-            // B = P^T (k = the warp's 16 keys, n = query row): lane (g, c)
-            // needs row g's P of keys 2c, 2c + 1, 2c + 8, 2c + 9, held by
-            // lanes (2c, g / 2) and (2c + 1, g / 2) as their row-2c' or
-            // row-2c'+1 pair
-            const uint32_t he = pack2<TM>(p0, p2), ho = pack2<TM>(p1, p3);
-            const int srcA = 8 * c + (g >> 1), srcB = srcA + 4;
-            const uint32_t eA = __shfl_sync(0xffffffffu, he, srcA), oA = __shfl_sync(0xffffffffu, ho, srcA);
-            const uint32_t eB = __shfl_sync(0xffffffffu, he, srcB), oB = __shfl_sync(0xffffffffu, ho, srcB);
-            const uint32_t vA = (g & 1) ? oA : eA, vB = (g & 1) ? oB : eB;
-            const uint32_t pb0 = __byte_perm(vA, vB, 0x5410), pb1 = __byte_perm(vA, vB, 0x7632);
+            if (!interior) {
+#pragma unroll
+                for (int hk = 0; hk < 2; ++hk) {
+                    const int jj = kw0 + g + 8 * hk, j = j0 + jj;
+                    const bool here = kvalid[stage * kDecTile + jj] != 0;
+#pragma unroll
+                    for (int u = 0; u < SW; ++u) {
+                        const int4 b = *reinterpret_cast<const int4 *>(&row_bounds[8 * u + sr0]);
+                        if (!(here && from(j, b.x) && j <= b.y)) sv[u][2 * hk] = -INFINITY;
+                        if (!(here && from(j, b.z) && j <= b.w)) sv[u][2 * hk + 1] = -INFINITY;
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < SW; ++u)
+                higher = higher || fmaxf(sv[u][0], sv[u][2]) > ms[u][0] + 8.f || fmaxf(sv[u][1], sv[u][3]) > ms[u][1] + 8.f;
+            // the running maxima rise only where a tile's exceeds them by more
+            // than 8 (a factor 2^8): only then are the row maxima over the
+            // warp's 16 keys (the lanes of one c) needed
+            if (__any_sync(0xffffffffu, higher)) {
+#pragma unroll
+                for (int u = 0; u < SW; ++u) {
+                    float mx0 = fmaxf(sv[u][0], sv[u][2]), mx1 = fmaxf(sv[u][1], sv[u][3]);
+#pragma unroll
+                    for (int o_ = 4; o_ < 32; o_ <<= 1) {
+                        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o_));
+                        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o_));
+                    }
+                    const float mn0 = mx0 > ms[u][0] + 8.f ? mx0 : ms[u][0], mn1 = mx1 > ms[u][1] + 8.f ? mx1 : ms[u][1];
+                    const float al0 = fast_exp2(ms[u][0] - mn0), al1 = fast_exp2(ms[u][1] - mn1);
+                    ls[u][0] *= al0;
+                    ls[u][1] *= al1;
+                    ms[u][0] = mn0;
+                    ms[u][1] = mn1;
+#pragma unroll
+                    for (int i = 8 * u; i < 8 * u + 8; ++i) {
+                        o[i][0] *= al0;
+                        o[i][2] *= al0;
+                        o[i][1] *= al1;
+                        o[i][3] *= al1;
+                    }
+                }
+            }
+            // B = P^T (k = the warp's 16 keys, n = query row): the transposes of
+            // the two 8 x 8 blocks (keys x rows) of P
+            uint32_t pb[SW][2];
+#pragma unroll
+            for (int u = 0; u < SW; ++u) {
+                const float p0 = fast_exp2(sv[u][0] - ms[u][0]), p1 = fast_exp2(sv[u][1] - ms[u][1]);
+                const float p2 = fast_exp2(sv[u][2] - ms[u][0]), p3 = fast_exp2(sv[u][3] - ms[u][1]);
+                // (this lane's keys; summed over g at the end)
+                ls[u][0] += SCL ? fmaf(p0, ivA, p2 * ivB) : p0 + p2;
+                ls[u][1] += SCL ? fmaf(p1, ivA, p3 * ivB) : p1 + p3;
+                pb[u][0] = transpose8x8(pack2<TM>(p0, p1));
+                pb[u][1] = transpose8x8(pack2<TM>(p2, p3));
+            }
             // A = V^T (m = head dim, k = key) of m-tile i: its row m is dim
             // 16 (m % 8) + 2i + m / 8, so that a lane's 16 dims of a V row are
             // one 16-byte chunk (g) and the two keys of an A register are
@@ -679,8 +724,11 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8>::CTAS) decode_spl
                                         widen_e4m3x2<TM>(y01 & 0xffffu), widen_e4m3x2<TM>(y01 >> 16)};
                 const uint32_t a1[4] = {widen_e4m3x2<TM>(x23 & 0xffffu), widen_e4m3x2<TM>(x23 >> 16),
                                         widen_e4m3x2<TM>(y23 & 0xffffu), widen_e4m3x2<TM>(y23 >> 16)};
-                mma16816<TM>(o[2 * i], a0, pb0, pb1);
-                mma16816<TM>(o[2 * i + 1], a1, pb0, pb1);
+#pragma unroll
+                for (int u = 0; u < SW; ++u) {
+                    mma16816<TM>(o[8 * u + 2 * i], a0, pb[u][0], pb[u][1]);
+                    mma16816<TM>(o[8 * u + 2 * i + 1], a1, pb[u][0], pb[u][1]);
+                }
             }
         } else {
             float sc[NT][4];
@@ -830,12 +878,14 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8>::CTAS) decode_spl
     pdl_launch_dependents();  // the merge kernel may get ready; it waits for this grid
 
     // combine the key groups of this CTA through shared memory
-    if constexpr (SW) {  // a row's keys are spread over the lanes of one c
+    if constexpr (SW > 0) {  // a row's keys are spread over the lanes of one c
 #pragma unroll
-        for (int o_ = 4; o_ < 32; o_ <<= 1) {
-            l0 += __shfl_xor_sync(0xffffffffu, l0, o_);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, o_);
-        }
+        for (int u = 0; u < SW; ++u)
+#pragma unroll
+            for (int o_ = 4; o_ < 32; o_ <<= 1) {
+                ls[u][0] += __shfl_xor_sync(0xffffffffu, ls[u][0], o_);
+                ls[u][1] += __shfl_xor_sync(0xffffffffu, ls[u][1], o_);
+            }
     } else {
         l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
         l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
@@ -843,24 +893,26 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8>::CTAS) decode_spl
         l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
     }
     float *comb_o = reinterpret_cast<float *>(smem);  // [NKG][ROWS][128]
-    if constexpr (SW) {
-        // lane (g, c) holds rows 2c and 2c + 1 at dims 16g .. 16g + 15:
-        // o[i][0 / 1] at dim 16g + 2i, o[i][2 / 3] at dim 16g + 2i + 1
+    if constexpr (SW > 0) {
+        // lane (g, c) holds rows 8u + 2c and 8u + 2c + 1 at dims 16g .. 16g + 15:
+        // o[8u + i][0 / 1] at dim 16g + 2i, o[8u + i][2 / 3] at dim 16g + 2i + 1
         const int g = lane >> 2;
-        float *w0 = &comb_o[(kg * ROWS + sr0) * kDecD + 16 * g];
-        float *w1 = &comb_o[(kg * ROWS + sr1) * kDecD + 16 * g];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            *reinterpret_cast<float4 *>(w0 + 4 * q) =
-                make_float4(o[2 * q][0], o[2 * q][2], o[2 * q + 1][0], o[2 * q + 1][2]);
-            *reinterpret_cast<float4 *>(w1 + 4 * q) =
-                make_float4(o[2 * q][1], o[2 * q][3], o[2 * q + 1][1], o[2 * q + 1][3]);
-        }
-        if (g == 0) {
-            comb_m[kg * ROWS + sr0] = m0;
-            comb_l[kg * ROWS + sr0] = l0;
-            comb_m[kg * ROWS + sr1] = m1;
-            comb_l[kg * ROWS + sr1] = l1;
+        for (int u = 0; u < SW; ++u) {
+            const int w = kg * ROWS + 8 * u + sr0;
+            float *w0 = &comb_o[w * kDecD + 16 * g], *w1 = w0 + kDecD;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int i = 8 * u + 2 * q;
+                *reinterpret_cast<float4 *>(w0 + 4 * q) = make_float4(o[i][0], o[i][2], o[i + 1][0], o[i + 1][2]);
+                *reinterpret_cast<float4 *>(w1 + 4 * q) = make_float4(o[i][1], o[i][3], o[i + 1][1], o[i + 1][3]);
+            }
+            if (g == 0) {
+                comb_m[w] = ms[u][0] == kNoKey ? -INFINITY : ms[u][0];
+                comb_l[w] = ls[u][0];
+                comb_m[w + 1] = ms[u][1] == kNoKey ? -INFINITY : ms[u][1];
+                comb_l[w + 1] = ls[u][1];
+            }
         }
     } else if constexpr (KV8) {
         // undo the output permutation: o[nt][e] is dim 16 (2c + (e & 1)) + nt
@@ -882,7 +934,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8>::CTAS) decode_spl
             *reinterpret_cast<float2 *>(&comb_o[(kg * ROWS + r1) * kDecD + d]) = make_float2(o[nd][2], o[nd][3]);
         }
     }
-    if (!SW && (lane & 3) == 0) {
+    if (SW == 0 && (lane & 3) == 0) {
         comb_m[kg * ROWS + r0] = m0;
         comb_l[kg * ROWS + r0] = l0;
         comb_m[kg * ROWS + r1] = m1;
@@ -1056,10 +1108,10 @@ static int plan_decode(int B, int Q, int Hqo, int Hkv, int D, int max_seq_len, i
     return PKV_OK;
 }
 
-template <typename T, int MT, int LAYOUT, bool KV8, bool SW = false, int EXT = 0>
+template <typename T, int MT, int LAYOUT, bool KV8, int SW = 0, int EXT = 0>
 static int launch_split(const DecodeParams &p, dim3 grid, cudaStream_t st, bool pdl) {
-    constexpr int ROWS = 16 * MT, NKG = 4 / MT;
-    constexpr int kDecStages = DecCfg<MT, KV8>::STAGES;
+    constexpr int ROWS = DecCfg<MT, KV8, SW>::ROWS, NKG = 4 / MT;
+    constexpr int kDecStages = DecCfg<MT, KV8, SW>::STAGES;
     const size_t smem = kDecStages * DecSmem<KV8>::STAGE + ROWS * kDecRowBytes +
                         kDecStages * kDecTile + 2 * NKG * ROWS * sizeof(float) +
                         (EXT ? p.pages_cap : kDecMaxPages) * sizeof(int) +
@@ -1076,11 +1128,17 @@ static int launch_split(const DecodeParams &p, dim3 grid, cudaStream_t st, bool 
 template <typename T, int LAYOUT, bool KV8, int EXT = 0>
 static int launch_split_mt(int MT, const DecodeParams &p, dim3 grid, cudaStream_t st, bool pdl) {
     if constexpr (KV8) {
-        if (p.R <= 8) return launch_split<T, 1, LAYOUT, true, true, EXT>(p, grid, st, pdl);  // swapped operands
+        if (p.R <= 8) return launch_split<T, 1, LAYOUT, true, 1, EXT>(p, grid, st, pdl);  // swapped operands
+        if constexpr (EXT > 0) {
+            if (p.R <= 16) return launch_split<T, 1, LAYOUT, true, 2, EXT>(p, grid, st, pdl);
+            if (p.R <= 32) return launch_split<T, 1, LAYOUT, true, 4, EXT>(p, grid, st, pdl);
+        }
     }
-    if (MT == 1) return launch_split<T, 1, LAYOUT, KV8, false, EXT>(p, grid, st, pdl);
-    if (MT == 2) return launch_split<T, 2, LAYOUT, KV8, false, EXT>(p, grid, st, pdl);
-    return launch_split<T, 4, LAYOUT, KV8, false, EXT>(p, grid, st, pdl);
+    if constexpr (EXT == 0 || !KV8) {
+        if (MT == 1) return launch_split<T, 1, LAYOUT, KV8, 0, EXT>(p, grid, st, pdl);
+        if (MT == 2) return launch_split<T, 2, LAYOUT, KV8, 0, EXT>(p, grid, st, pdl);
+    }
+    return launch_split<T, 4, LAYOUT, KV8, 0, EXT>(p, grid, st, pdl);
 }
 
 // The split kernel under a window with first tokens and / or over a cache

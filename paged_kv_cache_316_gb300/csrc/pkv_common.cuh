@@ -135,6 +135,14 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
                  : "r"(addr));
 }
 
+// Transpose of an 8 x 8 matrix of 16-bit elements held as MMA fragments (lane
+// (g, c) = (lane / 4, lane % 4): row g, columns 2c and 2c + 1).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(d) : "r"(a));
+    return d;
+}
+
 // D(16x8, fp32) += A(16x16, row) * B(16x8, col) with 16-bit inputs of type T.
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,

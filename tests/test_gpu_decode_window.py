@@ -141,6 +141,10 @@ SCALED = [
     ([3000, 12000, 5], 16, 16, 8, 2, wl.NHD, torch.bfloat16, 1, -1, 0, True, "5d"),    # several splits
     ([5000, 9000], 8, 8, 7, 1, wl.HND, torch.float16, 1, 4000, 300, False, "5d"),      # splits, window, first tokens
     ([900, 2000, 40], 64, 16, 16, 2, wl.NHD, torch.float16, 2, 300, 70, True, "5d"),
+    ([1300, 64, 2500], 16, 16, 24, 8, wl.HND, torch.bfloat16, 3, -1, 0, False, "5d"),  # 9 rows
+    ([777, 1500], 32, 16, 8, 1, wl.NHD, torch.bfloat16, 4, 500, 40, True, "5d"),       # 32 rows
+    ([900, 100], 16, 8, 17, 1, wl.HND, torch.float16, 1, -1, 0, False, "5d"),          # 17 rows
+    ([900, 100], 16, 8, 33, 1, wl.HND, torch.float16, 1, 200, 3, False, "5d"),         # 33 rows
 ]
 
 
