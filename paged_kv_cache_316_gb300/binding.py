@@ -366,8 +366,10 @@ def _scale_arg(scale, device):
 
 
 def paged_decode_workspace_size(batch_size, q_len_per_req, num_qo_heads, num_kv_heads,
-                                head_dim, max_seq_len, page_size, window_left=-1, first_tokens=0) -> int:
-    if first_tokens:
+                                head_dim, max_seq_len, page_size, window_left=-1, first_tokens=None) -> int:
+    """Workspace of paged_decode; with first_tokens given (0 too), of one with
+    first_tokens or kv_scales."""
+    if first_tokens is not None:
         return int(load_library().paged_decode_window_workspace_size(
             batch_size, q_len_per_req, num_qo_heads, num_kv_heads, head_dim,
             max_seq_len, page_size, window_left, first_tokens))

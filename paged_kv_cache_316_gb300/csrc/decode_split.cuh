@@ -976,6 +976,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8, SW>::CTAS) decode
                 sc_o = 0.f;
                 lse_v = -INFINITY;
             }
+            if (EXT && lsum != lsum) sc_o = lse_v = lsum;  // a NaN among the visible keys
             const int64_t orow = (qrow0 + t) * p.Hqo + h;
             if (dbg_in(orow * kDecD + d, 4, p.num_tokens * p.Hqo * kDecD, p.err))
                 store4(static_cast<T *>(p.out) + orow * kDecD + d, a0 * sc_o, a1 * sc_o, a2 * sc_o, a3 * sc_o);
@@ -983,11 +984,11 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8, SW>::CTAS) decode
         } else {
             const int64_t prow =
                 (static_cast<int64_t>(b * p.Hkv + kvh) * p.n_split_max + s) * p.R + r;
-            const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+            const float inv = lsum > 0.f ? 1.f / lsum : (EXT && lsum != lsum ? lsum : 0.f);
             if (dbg_in(prow, 1, p.ws_rows, p.err)) {
                 *reinterpret_cast<float4 *>(p.ws_o + prow * kDecD + d) =
                     make_float4(a0 * inv, a1 * inv, a2 * inv, a3 * inv);
-                if (d == 0) p.ws_lse[prow] = lsum > 0.f ? M + fast_log2(lsum) : -INFINITY;
+                if (d == 0) p.ws_lse[prow] = lsum > 0.f ? M + fast_log2(lsum) : (EXT && lsum != lsum ? lsum : -INFINITY);
             }
         }
     }
@@ -1028,7 +1029,12 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const DecodeParams p)
     if (!dbg_in(base, static_cast<int64_t>(n_split - 1) * p.R + 1, p.ws_rows, p.err) ||
         !dbg_in(n_split, 0, p.n_split_max, p.err))
         return;
-    for (int s = 0; s < n_split; ++s) M = fmaxf(M, p.ws_lse[base + static_cast<int64_t>(s) * p.R]);
+    float nan = 0.f;
+    for (int s = 0; s < n_split; ++s) {
+        const float x = p.ws_lse[base + static_cast<int64_t>(s) * p.R];
+        M = fmaxf(M, x);
+        if (FIRST && x != x) nan = x;
+    }
     const int d = lane * 4;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float den = 0.f;
@@ -1046,11 +1052,13 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const DecodeParams p)
         if (p.sinks) den += fast_exp2(p.sinks[h] * kLog2e - M);
     }
     const float bmm2 = p.bmm2_dev ? __ldg(p.bmm2_dev) : p.bmm2;
-    const float sc = den > 0.f ? bmm2 / den : 0.f;
+    float sc = den > 0.f ? bmm2 / den : 0.f;
+    float lse_v = den > 0.f ? (M + fast_log2(den)) * kLn2 : -INFINITY;
+    if (FIRST && nan != nan) sc = lse_v = nan;  // a NaN among the visible keys
     const int64_t orow = (qrow0 + t) * p.Hqo + h;
     if (!dbg_in(orow * kDecD + d, 4, p.num_tokens * p.Hqo * kDecD, p.err)) return;
     store4(static_cast<T *>(p.out) + orow * kDecD + d, acc.x * sc, acc.y * sc, acc.z * sc, acc.w * sc);
-    if (p.lse && lane == 0) p.lse[orow] = den > 0.f ? (M + fast_log2(den)) * kLn2 : -INFINITY;
+    if (p.lse && lane == 0) p.lse[orow] = lse_v;
 }
 
 struct DecodePlan {

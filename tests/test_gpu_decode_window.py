@@ -219,12 +219,38 @@ def test_device_scales_and_dependent_launch_give_the_same_bits():
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
-def test_unit_scales_are_the_plain_e4m3_decode():
+def test_unit_scales_agree_with_the_plain_e4m3_decode():
     c = make([45, 700], 16, 8, 2, wl.HND, torch.bfloat16, 36, e4m3=True)
-    plain = call(c, 0.05)
+    compare(c, *call(c, 0.05), 0.05)
     c["scales"] = torch.ones(c["pt"].num_pages, 2, 2, 2)
-    got = call(c, 0.05)
-    assert torch.equal(plain[0], got[0]) and torch.equal(plain[1], got[1])
+    compare(c, *call(c, 0.05), 0.05)
+
+
+@pytest.mark.parametrize("B, lens", [(1, [40000]), (3, [20000, 1, 9000]), (200, None)])
+def test_runs_that_span_many_pieces(B, lens):
+    """One long run over all CTAs; and more requests than threads, many empty."""
+    g = wl.generator(B)
+    if lens is None:
+        lens = [0 if i % 3 == 0 else int(x) for i, x in enumerate(torch.randint(0, 900, (B,), generator=g))]
+    c = make(lens, 16, 4, 1, wl.HND, torch.bfloat16, B, scaled=True, G=16, sinks=True)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out, lse = call(c, 0.1, 1.0, err)
+    assert int(err.item()) == (QLEN if 0 in lens else 0)
+    compare(c, out, lse, 0.1)
+
+
+@pytest.mark.parametrize("scaled", [False, True])
+@pytest.mark.parametrize("L", [100, 3000])  # one CTA, and parts that are joined
+def test_nan_and_infinity_among_the_visible_keys(scaled, L):
+    """A visible NaN makes its rows NaN, as the formula does; other heads and requests stay clean."""
+    c = make([L, L], 16, 8, 2, wl.HND, torch.bfloat16, 39, scaled=scaled, G=16, poison=False, window=None or -1)
+    page = c["pt"].pages[0][3]
+    raw = c["pool"].view(torch.uint8) if scaled else c["pool"]
+    raw[page, 0, 1, 5, 7] = 0x7F if scaled else float("nan")  # request 0, head 1: a key
+    kw = {} if scaled else dict(first=1, window=L)  # (the window path over a 16-bit cache)
+    out, lse = call(dict(c, **kw), 0.05)
+    assert torch.isnan(out[0, 4:].float()).all() and torch.isnan(lse[0, 4:]).all()
+    assert torch.isfinite(out[0, :4].float()).all() and torch.isfinite(out[1].float()).all()
 
 
 def test_graph_on_another_stream_follows_its_inputs():

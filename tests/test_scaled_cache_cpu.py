@@ -59,7 +59,7 @@ def _decode(lib, **over):  # noqa: F811
     (dict(block=4), 2), (dict(block=32), 2), (dict(block=0), 2), (dict(ss=7), 2), (dict(ks=None), 1),
     (dict(vs=None), 1), (dict(ks=None, vs=None), 1), (dict(rows=3), 2), (dict(mq=0), 2), (dict(D=64), 3),
     (dict(S=24), 3), (dict(mq=17, rows=100), 3), (dict(q=None), 1), (dict(ws=None, L=100000), 1),
-    (dict(wsb=16, L=100000, win=-1), 4), (dict(bts=2), 2), (dict(stride=2 * 8 * 16 * 128 + 8), 2),
+    (dict(wsb=16, L=100000, win=-1), 4), (dict(L=(1 << 30) + 1, bts=1 << 28), 3), (dict(bts=2), 2), (dict(stride=2 * 8 * 16 * 128 + 8), 2),
     (dict(ks=None, vs=None, block=0, dtype=0, out=None), 1), (dict(rows=0, B=0), 0),
 ])
 def test_decode_window_refuses(lib, over, status):  # noqa: F811
