@@ -250,15 +250,22 @@ def split_scales(kv_scales, num_pages: int, num_heads: int, page_size: int, devi
 
 def _same_device(*tensors):
     """All given tensors live on the current CUDA device: the library
-    launches there."""
-    here = None
+    launches there.  Returns that device's index."""
+    here = torch.cuda.current_device() if tensors[0].is_cuda else -2
     for t in tensors:
-        if t is not None:
-            dev = t.get_device()
-            if dev >= 0 and here is None:
-                here = torch.cuda.current_device()
-            if dev < 0 or dev != here:
-                raise PagedKVError("tensor arguments must live on the current CUDA device")
+        if t is not None and t.get_device() != here:
+            raise PagedKVError("tensor arguments must live on the current CUDA device")
+    return here
+
+
+def _stream_on(stream, device: int) -> int:
+    """_stream when the current device's index is known."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device)
+    return _stream(stream)
+
+
+_addr = torch.Tensor.data_ptr
 
 
 # ---- index helpers ------------------------------------------------------------------
@@ -345,12 +352,14 @@ def paged_append_scaled(append_key, append_value, batch_indices, positions, page
     if kv_indptr.numel() != B + 1:
         raise PagedKVError(f"kv_indptr must have {B + 1} entries")
     ks, vs, ss, block = split_scales(kv_scales, P, H, S, base.device)
-    _same_device(base, append_key, append_value, batch_indices, positions, kv_indices, kv_indptr,
-                 kv_last_page_len, err_word)
-    _check(load_library().paged_append_scaled(
-        _ptr(append_key), _ptr(append_value), nnz, _ptr(batch_indices), _ptr(positions), kp, vp, stride, P,
-        ks, vs, ss, block, _ptr(kv_indices), _ptr(kv_indptr), _ptr(kv_last_page_len), B, H, D, S, layout, dtype,
-        _ptr(err_word), _stream(stream)))
+    device = _same_device(base, append_key, append_value, batch_indices, positions, kv_indices, kv_indptr,
+                          kv_last_page_len, err_word)
+    status = load_library().paged_append_scaled(
+        _addr(append_key), _addr(append_value), nnz, _addr(batch_indices), _addr(positions), kp, vp, stride, P, ks, vs,
+        ss, block, _addr(kv_indices), _addr(kv_indptr), _addr(kv_last_page_len), B, H, D, S, layout, dtype,
+        None if err_word is None else _addr(err_word), _stream_on(stream, device))
+    if status:
+        _check(status)
 
 
 # ---- decode -------------------------------------------------------------------------------
@@ -474,46 +483,69 @@ def _decode_window(query, kv_cache, workspace, block_tables, seq_lens, max_seq_l
     block scales."""
     layout = _layout_code(kv_layout)
     kp, vp, stride, P, Hkv, S, D, base = split_cache(kv_cache, layout)
-    rows, Hqo, Dq = query.shape
+    shape = query.shape
+    rows, Hqo, Dq = shape
     if Dq != D:
         raise PagedKVError("query head_dim differs from the cache's")
+    if seq_lens.dim() != 1:
+        raise PagedKVError("seq_lens must be a contiguous 1-D tensor of 32-bit lengths")
     B = seq_lens.shape[0]
     dtype = _decode_dtype(query, base)
     if isinstance(kv_cache, (tuple, list)) and (kv_cache[1].dtype != base.dtype or
                                                 kv_cache[1].get_device() != base.get_device()):
         raise PagedKVError("K and V caches hold the same type on the same device")
-    ks = vs = None
+    ks = vs = cum = sink_ptr = lse_ptr = err_ptr = None
     ss = block = 0
     if kv_scales is not None:
         if dtype not in (F16_E4M3, BF16_E4M3):
             raise PagedKVError("kv_scales belong to a float8_e4m3fn cache")
         ks, vs, ss, block = split_scales(kv_scales, P, Hkv, S, base.device)
-    if out is None:
-        out = torch.empty_like(query)
     if (cum_seq_lens_q is None) != (max_q_len is None):
         raise PagedKVError("cum_seq_lens_q and max_q_len go together")
     if cum_seq_lens_q is None:
         max_q = q_len_per_req
-        _check_decode_args(query, out, lse, block_tables, seq_lens, B * max_q)
+        if rows < B * max_q:
+            raise PagedKVError(f"query has {rows} rows; the requests need {B * max_q}")
     else:
         max_q = int(max_q_len)
         if cum_seq_lens_q.dtype != torch.int32 or tuple(cum_seq_lens_q.shape) != (B + 1,) \
                 or not cum_seq_lens_q.is_contiguous():
             raise PagedKVError(f"cum_seq_lens_q must be contiguous int32 [{B + 1}]")
-        _check_decode_args(query, out, lse, block_tables, seq_lens, 0)
-    if not seq_lens.is_contiguous():
-        raise PagedKVError("seq_lens must be contiguous")
-    if sinks is not None and (sinks.dtype != torch.float32 or sinks.numel() != Hqo or not sinks.is_contiguous()):
-        raise PagedKVError(f"sinks must be contiguous float32 [{Hqo}]")
-    s1, s1_dev = _scale_arg(bmm1_scale, query.device)
-    s2, s2_dev = _scale_arg(bmm2_scale, query.device)
-    _same_device(query, base, workspace, block_tables, seq_lens, cum_seq_lens_q, sinks, out, lse, err_word)
-    _check(load_library().paged_decode_window(
-        query.data_ptr(), rows, kp, vp, stride, P, ks, vs, ss, block, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), block_tables.data_ptr(), block_tables.stride(0),
-        seq_lens.data_ptr(), B, max_seq_len, s1, s2, s1_dev, s2_dev, window_left, first_tokens, _ptr(sinks), max_q,
-        _ptr(cum_seq_lens_q), Hqo, Hkv, D, S, layout, dtype, 1 if enable_pdl else 0, out.data_ptr(), _ptr(lse),
-        _ptr(err_word), _stream(stream)))
+        cum = _ptr(cum_seq_lens_q)
+    if not query.is_contiguous():
+        raise PagedKVError("query must be contiguous [rows, num_qo_heads, head_dim]")
+    if out is None:
+        out = torch.empty_like(query)
+    elif out.shape != shape or out.dtype != query.dtype or not out.is_contiguous():
+        raise PagedKVError("out must be a contiguous tensor of the query's shape and dtype")
+    if lse is not None:
+        if lse.dtype != torch.float32 or lse.shape != shape[:2] or not lse.is_contiguous():
+            raise PagedKVError(f"lse must be a contiguous float32 [{rows}, {Hqo}] tensor")
+        lse_ptr = _addr(lse)
+    if seq_lens.element_size() != 4 or not seq_lens.is_contiguous():
+        raise PagedKVError("seq_lens must be a contiguous 1-D tensor of 32-bit lengths")
+    bt_stride = block_tables.stride()
+    if len(bt_stride) != 2 or bt_stride[1] != 1 or block_tables.dtype != torch.int32 or block_tables.shape[0] < B:
+        raise PagedKVError("block_tables must be int32 [>= batch_size, pages] with unit column stride")
+    if sinks is not None:
+        if sinks.dtype != torch.float32 or sinks.numel() != Hqo or not sinks.is_contiguous():
+            raise PagedKVError(f"sinks must be contiguous float32 [{Hqo}]")
+        sink_ptr = _addr(sinks)
+    s1, s2, s1_dev, s2_dev = bmm1_scale, bmm2_scale, None, None
+    if type(s1) is not float:
+        s1, s1_dev = _scale_arg(s1, query.device)
+    if type(s2) is not float:
+        s2, s2_dev = _scale_arg(s2, query.device)
+    if err_word is not None:
+        err_ptr = _ptr(err_word)
+    device = _same_device(query, base, workspace, block_tables, seq_lens, cum_seq_lens_q, sinks, out, lse, err_word)
+    status = load_library().paged_decode_window(
+        _addr(query), rows, kp, vp, stride, P, ks, vs, ss, block, _addr(workspace), workspace.nbytes,
+        _addr(block_tables), bt_stride[0], _addr(seq_lens), B, max_seq_len, s1, s2, s1_dev, s2_dev, window_left,
+        first_tokens, sink_ptr, max_q, cum, Hqo, Hkv, D, S, layout, dtype, 1 if enable_pdl else 0, _addr(out), lse_ptr,
+        err_ptr, _stream_on(stream, device))
+    if status:
+        _check(status)
     return out
 
 
