@@ -379,6 +379,10 @@ size_t paged_decode_window_workspace_size(int32_t batch_size, int32_t q_len_per_
  *    (NaN to 2^-48).  bmm1_scale and bmm2_scale apply on top.
  *  - workspace: >= paged_decode_window_workspace_size(...) bytes, 256-byte
  *    aligned; calls that may overlap on the GPU take one each.
+ *  - A NaN or infinity in a key or value that no query of the request sees has
+ *    no effect.  A NaN among the visible ones makes the rows that see it NaN
+ *    (out and lse); one in the value of a key that only some of a request's
+ *    queries see may reach its other queries.
  * Everything else, including errors, is as paged_decode_ex (cum_seq_lens_q
  * NULL: max_q_len tokens for every request).
  */
@@ -605,6 +609,9 @@ size_t paged_prefill_scaled_workspace_size(int32_t batch_size, int32_t num_qo_he
  *    cache that paged_append_scaled filled from it do; else rounded once.
  *  - batch_offsets_*: as paged_prefill_ex (each may be NULL; offsets of K and
  *    V with contiguous K/V only).
+ *  - Keys and values that no query of the request sees may hold anything; a
+ *    NaN or infinity in a value that some of its queries see may reach others.
+ *    Calls that may overlap on the GPU take a workspace each.
  * Device errors as paged_prefill, and PKV_DEV_ERR_SCALE (see
  * paged_decode_window).
  */

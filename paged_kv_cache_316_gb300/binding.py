@@ -352,6 +352,8 @@ def paged_append_scaled(append_key, append_value, batch_indices, positions, page
     if kv_indptr.numel() != B + 1:
         raise PagedKVError(f"kv_indptr must have {B + 1} entries")
     ks, vs, ss, block = split_scales(kv_scales, P, H, S, base.device)
+    if ks == vs and P > 0:
+        raise PagedKVError("K and V take scales of their own")
     device = _same_device(base, append_key, append_value, batch_indices, positions, kv_indices, kv_indptr,
                           kv_last_page_len, err_word)
     status = load_library().paged_append_scaled(

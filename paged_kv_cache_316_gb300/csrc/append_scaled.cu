@@ -16,6 +16,12 @@
 // it (cp.async, the next run in flight while one is quantised; a lane reads
 // only what it copied, so no barrier is needed), so every new value is read
 // once.  Longer runs and other widths are read twice, the second time from L2.
+//
+// HBM bounds it: two bytes read and one written an element.  1024 requests, 66k
+// tokens of 32 heads: 283 us, 5.7 TB/s, 84% of the measured copy rate (one warp
+// an entry and head, two reads: 1064 us; run list once per CTA and runs in
+// registers: 380; staged one run ahead: 299; two ahead: 287).  One token for
+// each of 64 requests: 3.3 us, a launch and three dependent reads.
 #include <type_traits>
 
 #include "pkv_common.cuh"
@@ -27,14 +33,21 @@ struct AppendScaledParams {
     uint8_t *cache[2];
     float *scales[2];
     int64_t nnz, page_stride, max_num_pages, scale_stride;
+    int64_t kv_extent, scale_extent;  // elements a cache / scale pointer spans
     const int32_t *batch_indices, *positions, *kv_indices, *kv_indptr, *kv_last_page_len;
     int B, H, D, page_shift, block_shift;
     int entries;  // entries a CTA takes, at most kAsEntries
     int32_t *err;
 };
 
-constexpr int kAsWarps = 8;  // two CTAs of 8 warps per SM: three measured slower
+// CTAs of 8 warps, 16 entries each.  Blocks of more than 8 tokens: two CTAs
+// per SM (what three stages of 4 KB a warp leave room for; with fewer
+// registers three measured slower, 328 against 299 us).  Blocks of 8: half the
+// stage, four CTAs per SM (16 prompts: 23.1 us, 24.7 with three, 26.7 with two).
+// 8 or 32 entries a CTA: 306 / 293 against 286 us.
+constexpr int kAsWarps = 8;
 constexpr int kAsEntries = 16;
+constexpr int kAsCtas4 = 4;
 constexpr int kAsMinExp = -40, kAsMaxExp = 40;
 
 // The pattern of infinity without sign: magnitudes from it on are not finite.
@@ -191,15 +204,14 @@ __device__ __forceinline__ int list_runs(const AppendScaledParams &p, int64_t i0
     return __popc(leaders);
 }
 
-constexpr int kAsHeld = 8;                        // staged 16-byte chunks of a lane
-constexpr int kAsStage = kAsHeld * 32 * 16;       // bytes of one warp's stage
 constexpr int kAsStages = 3;
-constexpr int kAsSmem = kAsWarps * kAsStages * kAsStage;
 
 // D128: rows of 128 elements (16 chunks of 16 bytes), short runs staged;
 // else any width, p.D / 8 chunks.
-template <typename T, int LAYOUT, bool D128>
-__global__ void __launch_bounds__(kAsWarps * 32, 2) append_scaled_kernel(const AppendScaledParams p) {
+template <typename T, int LAYOUT, int HELD>
+__global__ void __launch_bounds__(kAsWarps * 32, HELD == 4 ? kAsCtas4 : 2) append_scaled_kernel(const AppendScaledParams p) {
+    constexpr bool D128 = HELD > 0;
+    constexpr int kAsHeld = D128 ? HELD : 1, kAsStage = kAsHeld * 32 * 16;  // bytes of one warp's stage
     extern __shared__ __align__(16) uint8_t stage_mem[];
     __shared__ AppendRun runs[kAsEntries];
     __shared__ int n_runs;
@@ -249,12 +261,14 @@ __global__ void __launch_bounds__(kAsWarps * 32, 2) append_scaled_kernel(const A
     next(run3, hk3);
     int st = 0;
     for (int run = 0, hk = hk0; run < total_runs;) {
-        const AppendRun r = runs[run];
-        const int n = r.n, in_block = r.slot & (G - 1);
+        AppendRun r = runs[run];
+        int n = r.n;
+        const int in_block = r.slot & (G - 1);
         const int z = hk >= p.H ? 1 : 0, h = hk - z * p.H;
         float *scale = p.scales[z] + r.page * p.scale_stride + (static_cast<int64_t>(h) << (p.page_shift - p.block_shift)) +
                        (r.slot >> p.block_shift);
-        float was = in_block > 0 ? *scale : 0.f;
+        const bool scale_in = dbg_in(scale - p.scales[z], 1, p.scale_extent, p.err);
+        float was = in_block > 0 && scale_in ? *scale : 0.f;
         issue(run3, hk3, st == 0 ? 2 : st - 1);
         next(run3, hk3);
         const uint16_t *src = source(r, hk);
@@ -296,7 +310,12 @@ __global__ void __launch_bounds__(kAsWarps * 32, 2) append_scaled_kernel(const A
             was = s;
         }
         __syncwarp();
-        if (lane == 0) *scale = s;
+        if (lane == 0 && scale_in) *scale = s;
+        if constexpr (kDebugBounds) {  // the block's rows and its scale lie in the pool (else nothing is touched)
+            const int64_t row = kv_row_offset<LAYOUT>(r.page, p.page_stride, h, r.slot - in_block, p.H, S, p.D);
+            const int64_t step_d = LAYOUT == PKV_HND ? p.D : src_row;
+            if (!dbg_in(row, (in_block + n - 1) * step_d + p.D, p.kv_extent, p.err)) n = 0;
+        }
         uint8_t *dst = p.cache[z] + kv_row_offset<LAYOUT>(r.page, p.page_stride, h, r.slot, p.H, S, p.D);
         const int64_t dst_row = LAYOUT == PKV_HND ? p.D : src_row;
         if (s > was) {  // earlier tokens of the block, rounded again under the larger scale
@@ -380,6 +399,12 @@ extern "C" int paged_append_scaled(const void *append_key, const void *append_va
     p.page_stride = page_stride;
     p.max_num_pages = max_num_pages;
     p.scale_stride = scale_page_stride;
+    p.kv_extent = max_num_pages > 0
+                      ? (max_num_pages - 1) * page_stride + static_cast<int64_t>(num_kv_heads) * page_size * head_dim
+                      : 0;
+    p.scale_extent = max_num_pages > 0
+                         ? (max_num_pages - 1) * scale_page_stride + (static_cast<int64_t>(num_kv_heads) << (ps - bs))
+                         : 0;
     p.batch_indices = batch_indices;
     p.positions = positions;
     p.kv_indices = kv_indices;
@@ -400,18 +425,24 @@ extern "C" int paged_append_scaled(const void *append_key, const void *append_va
     const int most_y = (2 * num_kv_heads + kAsWarps - 1) / kAsWarps;
     const int64_t gy = (want + gx - 1) / gx;
     const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy < most_y ? gy : most_y));
-    const bool d128 = head_dim == 128;
-    auto pick = [&](auto k128, auto any) { return d128 ? k128 : any; };
+    // rows of 128 elements: staged runs of up to 8 rows (blocks of 8) or 16
+    const int held = head_dim != 128 ? 0 : (scale_block == 8 ? 4 : 8);
+    auto pick = [&](auto k8, auto k4, auto any) { return held == 8 ? k8 : (held == 4 ? k4 : any); };
+    auto by_layout = [&](auto hnd, auto nhd) { return layout == PKV_HND ? hnd : nhd; };
+    using B = __nv_bfloat16;
+    using F = __half;
     auto kern = dtype == PKV_BF16
-                    ? (layout == PKV_HND ? pick(append_scaled_kernel<__nv_bfloat16, PKV_HND, true>,
-                                                append_scaled_kernel<__nv_bfloat16, PKV_HND, false>)
-                                         : pick(append_scaled_kernel<__nv_bfloat16, PKV_NHD, true>,
-                                                append_scaled_kernel<__nv_bfloat16, PKV_NHD, false>))
-                    : (layout == PKV_HND
-                           ? pick(append_scaled_kernel<__half, PKV_HND, true>, append_scaled_kernel<__half, PKV_HND, false>)
-                           : pick(append_scaled_kernel<__half, PKV_NHD, true>, append_scaled_kernel<__half, PKV_NHD, false>));
-    const size_t smem = d128 ? kAsSmem : 0;
-    if (d128 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+                    ? by_layout(pick(append_scaled_kernel<B, PKV_HND, 8>, append_scaled_kernel<B, PKV_HND, 4>,
+                                     append_scaled_kernel<B, PKV_HND, 0>),
+                                pick(append_scaled_kernel<B, PKV_NHD, 8>, append_scaled_kernel<B, PKV_NHD, 4>,
+                                     append_scaled_kernel<B, PKV_NHD, 0>))
+                    : by_layout(pick(append_scaled_kernel<F, PKV_HND, 8>, append_scaled_kernel<F, PKV_HND, 4>,
+                                     append_scaled_kernel<F, PKV_HND, 0>),
+                                pick(append_scaled_kernel<F, PKV_NHD, 8>, append_scaled_kernel<F, PKV_NHD, 4>,
+                                     append_scaled_kernel<F, PKV_NHD, 0>));
+    const size_t smem = static_cast<size_t>(kAsWarps) * kAsStages * held * 32 * 16;
+    if (smem > 48 * 1024 - 1024 &&
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return PKV_ERR_CUDA;
     kern<<<grid, kAsWarps * 32, smem, static_cast<cudaStream_t>(stream)>>>(p);
     note_launches(1);

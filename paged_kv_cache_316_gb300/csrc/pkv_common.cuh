@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "pagedkv.h"
 
 namespace pkv {
@@ -70,10 +72,15 @@ inline int ilog2_exact(int x) {  // -1 unless x is a power of two
     return s;
 }
 
+// SMs of the current device (looked up once per device: a fixed property).
 inline int num_sms() {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices];
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+    if (dev < kDevices && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+    if (dev < kDevices) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 

@@ -174,7 +174,7 @@ def test_refusals():
     for o in (dict(k=k.float()), dict(v=v.half()), dict(k=k[:, :1]), dict(cache=cache.view(torch.uint8)),
               dict(sc=sc.double()), dict(sc=sc[:-1]), dict(sc=sc.cpu()), dict(bi=bi[:1]), dict(pos=pos.long()),
               dict(indptr=indptr[:1]), dict(last=last.long()), dict(k=k.cpu()),
-              dict(k=k.transpose(1, 2).contiguous().transpose(1, 2))):
+              dict(k=k.transpose(1, 2).contiguous().transpose(1, 2)), dict(sc=sc[:, :1].expand(-1, 2, -1, -1))):
         with pytest.raises(pk.PagedKVError):
             call(**o)
     call()
