@@ -198,6 +198,11 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     return d;
 }
 
+// The n low bits set (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+    return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
+
 // Wait for this thread's tensor-memory loads, with the 32 destination
 // registers as operands so that no use of them can be scheduled before it.
 __device__ __forceinline__ void tmem_wait_ld_regs(uint32_t (&r)[32]) {
@@ -827,20 +832,24 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 32; ++c) ra[c] = __float_as_uint(__uint_as_float(ra[c]) * sc);
             }
-            if (!warp_full) {
+            if constexpr (WIN) {
+                // one bit for each column: at most lim, and not of the keys
+                // [first_tokens, row_lo); a chunk that the whole warp sees
+                // (most of a boundary tile) is left as it is
+                if (!warp_full) {
+                    const int j = j0 + 32 * i;
+                    const uint32_t hidden = ~low_bits(lim - j + 1) | (low_bits(row_lo - j) & ~low_bits(p.first_tokens - j));
+                    if (__any_sync(0xffffffffu, hidden != 0u)) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (hidden & (1u << c)) ra[c] = __float_as_uint(-INFINITY);
+                    }
+                }
+            } else if (!warp_full) {
                 const int lr = lim - (j0 + 32 * i);  // last visible column of the chunk
 #pragma unroll
                 for (int c = 0; c < 32; ++c)
                     if (c > lr) ra[c] = __float_as_uint(-INFINITY);
-                if constexpr (WIN) {
-                    // columns of the keys [first_tokens, row_lo)
-                    const int ca = max(p.first_tokens - (j0 + 32 * i), 0), cb = row_lo - (j0 + 32 * i);
-                    if (cb > ca) {
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (c >= ca && c < cb) ra[c] = __float_as_uint(-INFINITY);
-                    }
-                }
             }
         };
         auto chunk_max = [&](const uint32_t(&ra)[32]) {
