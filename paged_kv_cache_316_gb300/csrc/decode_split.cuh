@@ -300,8 +300,41 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8, SW>::CTAS) decode
     constexpr int RSTEP = MT * 32 / LPR;              // rows between a thread's rows
     constexpr int NLOAD = KPW * LPR / (MT * 32);      // rows per thread per tile
     const int64_t row_step = (LAYOUT == PKV_HND ? kDecD : static_cast<int64_t>(p.Hkv) * kDecD) * RSTEP;
+    // (EXT over an E4M3 cache, 16-key slices: the common case with everything
+    // but the page's and the slot's offset worked out once; kvalid of a stage
+    // is rewritten only after a tile that had rows without a key)
+    constexpr bool SLICE16 = EXT > 0 && SW > 0;
+    const int64_t row_bytes = LAYOUT == PKV_HND ? kDecD : static_cast<int64_t>(p.Hkv) * kDecD;
+    const uint8_t *lane_k = kc8 + (LAYOUT == PKV_HND ? static_cast<int64_t>(kvh) * S : static_cast<int64_t>(kvh)) * kDecD +
+                            (lane >> 3) * row_bytes + (lane & 7) * 16;
+    const int64_t v_from_k = vc8 - kc8;
+    const uint32_t slice_even = swz8(kw0 + (lane >> 3), lane & 7), slice_odd = swz8(kw0 + (lane >> 3) + 4, lane & 7);
+    uint32_t dirty = 0xffffffffu;  // bit s: kvalid of stage s may hold zeros
     auto load_tile = [&](int stage, int j0) {
         const uint32_t dst = smem_u32(smem + stage * STAGE_BYTES);
+        if constexpr (SLICE16) {
+            const int js = j0 + kw0, pi = (js >> p.page_shift) - page_base(j0);
+            if (p.page_shift >= 4 && keys_in(js, 16) && dbg_in(pi, 1, pages_cap, p.err)) {
+                const int page = pages_s[pi];
+                if (page >= 0) {
+                    const uint8_t *ks = lane_k + (page * p.page_stride + (js & (S - 1)) * row_bytes);
+                    const uint8_t *vs = ks + v_from_k;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t o = ((k & 1) ? slice_odd : slice_even) + (k >> 1) * (8 * kDec8RowBytes);
+                        const bool in = dbg_in(ks + k * row_step - kc8, 16, p.kv_extent, p.err);
+                        cp_async_16(dst + o, in ? ks + k * row_step : kc8, in);
+                        cp_async_16(dst + kDec8TileBytes + o, in ? vs + k * row_step : vc8, in);
+                    }
+                    if ((dirty >> stage) & 1u) {
+                        if (lane < 16) kvalid[stage * kDecTile + kw0 + lane] = 1;
+                        dirty &= ~(1u << stage);
+                    }
+                    return;
+                }
+            }
+            dirty |= 1u << stage;
+        }
         {
             const int r0 = kw0 + gtid / LPR, c = gtid % LPR;
             const int jA = j0 + r0, jZ = jA + (NLOAD - 1) * RSTEP;
@@ -491,8 +524,11 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8, SW>::CTAS) decode
     }
 
     uint32_t qa[SW ? 1 : 8][4];
-    uint32_t qb[SW ? SW : 1][8][2];  // (SW) Q^T fragments of each 8-row tile
-    if constexpr (SW > 0) {
+    constexpr bool QSMEM = SW == 4;  // (32 rows: read per tile, the registers hold the output)
+    uint32_t qb[SW && !QSMEM ? SW : 1][8][2];  // (SW) Q^T fragments of each 8-row tile
+    const uint8_t *q_lane = q_s + (lane >> 2) * kDecRowBytes;
+    if constexpr (QSMEM) {
+    } else if constexpr (SW > 0) {
         // B operand of the swapped QK (Q^T, k = head dim, n = query row): lane
         // (g, c) holds row 8u + g, dims 32c + 4kk + {0, 1} and {2, 3} of k-step
         // kk (the permuted order of the K rows, below)
@@ -623,7 +659,16 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8, SW>::CTAS) decode
                     const uint32_t a[4] = {widen_e4m3x2<TM>(wa[kk] & 0xffffu), widen_e4m3x2<TM>(wb[kk] & 0xffffu),
                                            widen_e4m3x2<TM>(wa[kk] >> 16), widen_e4m3x2<TM>(wb[kk] >> 16)};
 #pragma unroll
-                    for (int u = 0; u < SW; ++u) mma16816<TM>(sc[u][kk & (CH - 1)], a, qb[u][kk][0], qb[u][kk][1]);
+                    for (int u = 0; u < SW; ++u) {
+                        if constexpr (QSMEM) {
+                            // row 8u + g, dims 32c + 4kk .. + 3 (16-byte chunk 4c + kk / 2, swizzled by g)
+                            const uint2 q2 = *reinterpret_cast<const uint2 *>(
+                                q_lane + u * (8 * kDecRowBytes) + (((4 * c + (kk >> 1)) ^ g) << 4) + (kk & 1) * 8);
+                            mma16816<TM>(sc[u][kk & (CH - 1)], a, q2.x, q2.y);
+                        } else {
+                            mma16816<TM>(sc[u][kk & (CH - 1)], a, qb[u][kk][0], qb[u][kk][1]);
+                        }
+                    }
                 }
             }
             float kmA = scale_log2, kmB = scale_log2, lvA = 0.f, lvB = 0.f, ivA = 1.f, ivB = 1.f;
