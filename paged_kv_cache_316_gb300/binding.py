@@ -144,14 +144,14 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+_DTYPES = {torch.float16: F16, torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3}
+
+
 def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.float16:
-        return F16
-    if t.dtype == torch.bfloat16:
-        return BF16
-    if t.dtype == torch.float8_e4m3fn:
-        return E4M3
-    raise PagedKVError(f"unsupported element type {t.dtype}")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise PagedKVError(f"unsupported element type {t.dtype}")
+    return code
 
 
 def _decode_dtype(query: torch.Tensor, cache: torch.Tensor) -> int:
@@ -177,6 +177,8 @@ def _layout_code(kv_layout) -> int:
 
 def _rows_contiguous(t) -> bool:
     """t[0].is_contiguous(), from the shape and strides."""
+    if t.is_contiguous():
+        return True
     n = 1
     shape, stride = t.shape, t.stride()
     for i in range(len(shape) - 1, 0, -1):
@@ -208,7 +210,8 @@ def split_cache(kv_cache, layout: int):
         kp = kv_cache.data_ptr()
         vp = kp + kv_cache.stride(1) * kv_cache.element_size()
         shape = kv_cache.shape[2:]
-    _ptr(base)
+    if not base.is_cuda:
+        raise PagedKVError("tensor arguments must live on a CUDA device")
     if layout == HND:
         H, S, D = shape
     else:
@@ -220,7 +223,7 @@ def base_dtype(kv_cache) -> torch.dtype:
     return (kv_cache[0] if isinstance(kv_cache, (tuple, list)) else kv_cache).dtype
 
 
-def split_scales(kv_scales, num_pages: int, num_heads: int, page_size: int, device):
+def split_scales(kv_scales, num_pages: int, num_heads: int, page_size: int, device: int):
     """(k_ptr, v_ptr, page stride, block) of the block scales of an E4M3
     cache: one float32 tensor [pages, 2, heads, page_size // block] or a
     (k, v) tuple of [pages, heads, page_size // block]."""
@@ -230,22 +233,22 @@ def split_scales(kv_scales, num_pages: int, num_heads: int, page_size: int, devi
         if k.dim() != 3 or v.shape != shape or v.stride() != stride:
             raise PagedKVError("K and V scales must be [pages, heads, blocks] of the same shape and strides")
         same = v.dtype == torch.float32 and v.get_device() == k.get_device()
-        vp = _ptr(v)
+        vp = v.data_ptr()
     else:
         k = kv_scales
         shape, stride = k.shape, k.stride()
         if k.dim() != 4 or shape[1] != 2:
             raise PagedKVError("a single kv_scales tensor must be [pages, 2, heads, blocks]")
         vp = k.data_ptr() + 4 * stride[1]
-        shape, stride, same = (shape[0],) + tuple(shape[2:]), (stride[0],) + tuple(stride[2:]), True
+        shape, stride, same = (shape[0], shape[2], shape[3]), (stride[0], stride[2], stride[3]), True
     P, H, blocks = shape
     if P != num_pages or H != num_heads or blocks < 1 or page_size % blocks:
         raise PagedKVError(f"scales must be [{num_pages}, {num_heads}, page_size // block] for each of K and V")
-    if not same or k.dtype != torch.float32 or k.device != device:
+    if not same or k.dtype != torch.float32 or k.get_device() != device:
         raise PagedKVError("scales are float32 on the cache's device")
     if (blocks > 1 and stride[2] != 1) or (H > 1 and stride[1] != blocks):
         raise PagedKVError("the scales of a page must be contiguous")
-    return _ptr(k), vp, stride[0] if P > 1 else max(H * blocks, stride[0]), page_size // blocks
+    return k.data_ptr(), vp, stride[0] if P > 1 else max(H * blocks, stride[0]), page_size // blocks
 
 
 def _same_device(*tensors):
@@ -351,7 +354,7 @@ def paged_append_scaled(append_key, append_value, batch_indices, positions, page
             raise PagedKVError("kv_indices/kv_indptr/kv_last_page_len must be contiguous int32")
     if kv_indptr.numel() != B + 1:
         raise PagedKVError(f"kv_indptr must have {B + 1} entries")
-    ks, vs, ss, block = split_scales(kv_scales, P, H, S, base.device)
+    ks, vs, ss, block = split_scales(kv_scales, P, H, S, base.get_device())
     if ks == vs and P > 0:
         raise PagedKVError("K and V take scales of their own")
     device = _same_device(base, append_key, append_value, batch_indices, positions, kv_indices, kv_indptr,
@@ -501,7 +504,7 @@ def _decode_window(query, kv_cache, workspace, block_tables, seq_lens, max_seq_l
     if kv_scales is not None:
         if dtype not in (F16_E4M3, BF16_E4M3):
             raise PagedKVError("kv_scales belong to a float8_e4m3fn cache")
-        ks, vs, ss, block = split_scales(kv_scales, P, Hkv, S, base.device)
+        ks, vs, ss, block = split_scales(kv_scales, P, Hkv, S, base.get_device())
     if (cum_seq_lens_q is None) != (max_q_len is None):
         raise PagedKVError("cum_seq_lens_q and max_q_len go together")
     if cum_seq_lens_q is None:
@@ -719,7 +722,7 @@ def _prefill_window(q, k_cache, v_cache, scale, workspace, max_q, max_kv, lens_q
     if kv_scales is not None:
         if k_cache.dtype != torch.float8_e4m3fn or v_cache.dtype != torch.float8_e4m3fn or block_tables is None:
             raise PagedKVError("kv_scales belong to paged float8_e4m3fn caches")
-        ks, vs, ss, block = split_scales(kv_scales, P, Hkv, S, k_cache.device)
+        ks, vs, ss, block = split_scales(kv_scales, P, Hkv, S, k_cache.get_device())
         dtype = F16_E4M3 if dtype == F16 else BF16_E4M3
     elif k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
         raise PagedKVError("the caches hold the query's type, or float8_e4m3fn with kv_scales")

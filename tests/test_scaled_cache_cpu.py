@@ -81,7 +81,7 @@ def test_window_workspace_counts_the_first_tokens(lib):  # noqa: F811
 def test_binding_refuses_before_the_library():
     import paged_kv_cache_316_gb300 as pk
     from paged_kv_cache_316_gb300.binding import split_scales
-    dev = torch.device("cpu")
+    dev = -1  # (the device index of a CPU tensor)
     for bad in (torch.zeros(4, 3, 8, 1), torch.zeros(4, 2, 8), torch.zeros(5, 2, 8, 1), torch.zeros(4, 2, 7, 1),
                 torch.zeros(4, 2, 8, 3), torch.zeros(4, 2, 8, 1, dtype=torch.float16),
                 torch.zeros(4, 2, 8, 4)[..., ::2], torch.zeros(4, 2, 2, 8).transpose(2, 3),
