@@ -298,7 +298,7 @@ def make_parts(rank: int, dev):
             pk.paged_decode(c.query, kv, ws, bt, sl, c.max_seq_len, bmm1_scale=c.bmm1_scale,
                             bmm2_scale=c.bmm2_scale, window_left=c.window_left, sinks=sinks,
                             kv_layout="HND", q_len_per_req=c.q_len_per_req, out=out)
-        p = Part(name, run, decode_bytes(c), "GB/s", "hbm", "decode.cu")
+        p = Part(name, run, decode_bytes(c), "GB/s", "hbm", "decode_split.cuh")
         p.case, p.ws, p.bt, p.sl, p.sinks = c, ws, bt, sl, sinks
         return p
 
@@ -344,7 +344,7 @@ def make_next_parts(rank: int, dev):
         pk.paged_decode(c.query, kv, ws, bt, sl, c.max_seq_len, bmm1_scale=c.bmm1_scale,
                         window_left=c.window_left, sinks=sinks, kv_layout=c.pool.layout,
                         cum_seq_lens_q=cum, max_q_len=c.q_len_per_req, out=out)
-    parts = [Part("decode_varlen", run, decode_bytes(c), "GB/s", "hbm", "decode.cu")]
+    parts = [Part("decode_varlen", run, decode_bytes(c), "GB/s", "hbm", "decode_split.cuh")]
 
     # the ragged prefill with contiguous (non-paged) K/V, d_qk 128
     pc = wl.ragged_prefill(seed=rank_seed(rank), d_qk=128, device=dev)
@@ -376,7 +376,7 @@ def make_next_parts(rank: int, dev):
     def run_fp8():
         pk.paged_decode(c8.query, c8.pool.storage[0], ws8, bt8, sl8, c8.max_seq_len,
                         bmm1_scale=c8.bmm1_scale, kv_layout=c8.pool.layout, out=out8)
-    parts.append(Part("decode_llama_e4m3", run_fp8, decode_bytes(c8), "GB/s", "hbm", "decode.cu"))
+    parts.append(Part("decode_llama_e4m3", run_fp8, decode_bytes(c8), "GB/s", "hbm", "decode_split.cuh"))
 
     # the append sweep point in E4M3
     a8 = wl.append_sweep(4096, seed=1 + rank_seed(rank), layout=wl.NHD, device=dev, fill="empty",

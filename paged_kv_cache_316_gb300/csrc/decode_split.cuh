@@ -14,6 +14,22 @@
 // the Q query tokens of a request form R = group * Q rows, padded to
 // 16 * MT rows of one mma.sync m16n8k16 A operand, so each K/V row read
 // from HBM feeds every query row that needs it.
+//
+// The kernel takes two extensions (EXT; their own translation unit,
+// decode_window.cu): a window that keeps the first tokens visible, and an
+// E4M3 cache with a scale for each block of keys and head.  Every visible key
+// is read once, so HBM bounds them: 128 requests, one token, a window of 4096
+// keys and 128 first tokens over a 16-bit cache: 315 us, 97% of the measured
+// copy rate.  Over an E4M3 cache, with half the bytes, the work around a key
+// counts: 64 requests of up to 8192 keys, 4 rows: 97.7 us, 86%; 96 requests
+// of 4 tokens, 32 rows: 227 us, 47%, bound by the issue of register MMAs (64
+// a warp and tile, 8 cycles each) and the softmax between them with two warps
+// to a scheduler.  Tried and slower: the work of all requests laid end to end
+// and cut evenly (105 / 266 us: the SMs do not stream at one rate), QK of the
+// next tile ahead of the softmax (249 us: a warp issues in order), QK and PV on
+// tcgen05 from fp16 tiles widened in shared memory (343 us: 4,000 cycles a
+// tile of fences, barriers and waits, at most two CTAs per SM by tensor
+// memory), splits of half and a quarter of the length (no change).
 #pragma once
 
 #include <math.h>

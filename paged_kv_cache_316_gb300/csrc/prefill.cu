@@ -37,6 +37,17 @@
 // (setmaxnreg).  Every wait is bounded; a wait that gives up sets
 // PKV_DEV_ERR_TIMEOUT, the other roles stop, the copies in flight are
 // waited for, tensor memory is freed and the CTA returns.
+//
+// A sliding window that keeps the first tokens visible (WIN) leaves out the
+// key tiles that no row of a query tile sees, so an item's work follows the
+// window and not the sequence: 2048 queries at the end of 32768 keys, window
+// 4096, 32 heads: 129.5 us, 1.07 PFLOP/s over the visible pairs, 55% of the
+// measured bf16 rate (256 items on 152 SMs fill two rounds to 84%).  8 ragged
+// prompts, d_qk 192, window 778 and 33 first tokens: 179 us, 40%: an item is 11
+// tiles of 96 keys for 8.5 tiles' worth of visible pairs, and its start and end
+// take as long as three.  The softmax masks with one word of bits for 32
+// columns and leaves alone what the whole warp sees (per-column compares:
+// 138 and 206 us).
 #include <math.h>
 
 #include <type_traits>
