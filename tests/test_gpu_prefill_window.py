@@ -99,6 +99,10 @@ WINDOW = [
     ([100, 50], [800, 50], 32, 4, 2, 128, wl.HND, torch.bfloat16, 200, 5, False),        # keys after the query too
     ([300], [300], 16, 4, 2, 128, wl.HND, torch.float16, 5000, 3, True),                 # longer than the request
     ([40, 0, 70], [30, 20, 600], 16, 4, 2, 128, wl.HND, torch.bfloat16, 60, 2, True),    # more queries than keys
+    ([260], [900], 8, 4, 2, 128, wl.HND, torch.bfloat16, 333, 13, True),                 # small boxes, a tile of both parts
+    ([130, 257], [2000, 777], 16, 2, 1, 192, wl.NHD, torch.float16, 250, 100, True),     # first tokens end inside a tile
+    ([300], [1500], 128, 2, 2, 128, wl.NHD, torch.bfloat16, 129, 127, True),             # first tokens end a key early
+    ([150], [700], 64, 4, 1, 192, wl.HND, torch.bfloat16, 40, 200, False),
 ]
 
 
@@ -125,6 +129,7 @@ SCALED = [
     ([100, 50], [800, 50], 64, 32, 6, 2, 128, wl.NHD, torch.bfloat16, -1, 0, False),
     ([129, 40], [1025, 1200], 256, 128, 3, 1, 128, wl.HND, torch.float16, 150, 70, True),
     ([257, 33], [1300, 600], 8, 8, 6, 2, 192, wl.HND, torch.bfloat16, 99, 5, True),
+    ([200], [1111], 16, 16, 4, 2, 128, wl.NHD, torch.float16, 333, 77, True),
 ]
 
 
