@@ -181,6 +181,10 @@ def _rows_contiguous(t) -> bool:
         return True
     n = 1
     shape, stride = t.shape, t.stride()
+    if len(shape) == 4:  # (a view of K or V in a [pages, 2, ..] pool)
+        a, b = shape[3], shape[2] * shape[3]
+        if stride[3] == 1 and stride[2] == a and stride[1] == b:
+            return True
     for i in range(len(shape) - 1, 0, -1):
         if shape[i] != 1 and stride[i] != n:
             return t.numel() == 0
@@ -711,47 +715,59 @@ def _prefill_window(q, k_cache, v_cache, scale, workspace, max_q, max_kv, lens_q
     """paged_prefill under a window and / or over caches with block scales."""
     P, Hkv, S, dv = dims
     total_q, Hqo, d_qk = q.shape
+    qdt = q.dtype
     dtype = _dtype_code(q)
-    if dtype not in (F16, BF16) or any(x is not None for x in scalar_scales) or o_data_type not in (None, q.dtype):
+    sq, sk, sv = scalar_scales
+    if dtype > BF16 or sq is not None or sk is not None or sv is not None or (o_data_type is not None and
+                                                                              o_data_type != qdt):
         raise PagedKVError("window_left, first_tokens and kv_scales take a 16-bit query and output and no "
                            "q_scale / k_scale / v_scale")
     if not q.is_contiguous():
         raise PagedKVError("q must be contiguous [total_q, num_qo_heads, d_qk]")
     ks = vs = None
     ss = block = 0
+    kdt = k_cache.dtype
     if kv_scales is not None:
-        if k_cache.dtype != torch.float8_e4m3fn or v_cache.dtype != torch.float8_e4m3fn or block_tables is None:
+        if kdt != torch.float8_e4m3fn or block_tables is None:
             raise PagedKVError("kv_scales belong to paged float8_e4m3fn caches")
         ks, vs, ss, block = split_scales(kv_scales, P, Hkv, S, k_cache.get_device())
         dtype = F16_E4M3 if dtype == F16 else BF16_E4M3
-    elif k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
+    elif kdt != qdt:
         raise PagedKVError("the caches hold the query's type, or float8_e4m3fn with kv_scales")
-    if v_cache.shape[:-1] != k_cache.shape[:-1]:
-        raise PagedKVError("K and V caches must have the same pages, heads and page size")
+    if v_cache.dtype != kdt or v_cache.shape[:-1] != k_cache.shape[:-1]:
+        raise PagedKVError("K and V caches must have the same type, pages, heads and page size")
     if not (_rows_contiguous(k_cache) and _rows_contiguous(v_cache)):
         raise PagedKVError("each page must be contiguous")
     if out is None:
-        out = torch.empty((total_q, Hqo, dv), dtype=q.dtype, device=q.device)
+        out = torch.empty((total_q, Hqo, dv), dtype=qdt, device=q.device)
+    elif tuple(out.shape) != (total_q, Hqo, dv) or out.dtype != qdt or not out.is_contiguous():
+        raise PagedKVError(f"out must be a contiguous {qdt} [{total_q}, {Hqo}, {dv}] tensor")
     if lse is None:
         lse = torch.empty((total_q, Hqo), dtype=torch.float32, device=q.device)
-    if tuple(out.shape) != (total_q, Hqo, dv) or out.dtype != q.dtype or not out.is_contiguous():
-        raise PagedKVError(f"out must be a contiguous {q.dtype} [{total_q}, {Hqo}, {dv}] tensor")
-    if tuple(lse.shape) != (total_q, Hqo) or lse.dtype != torch.float32 or not lse.is_contiguous():
+    elif tuple(lse.shape) != (total_q, Hqo) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise PagedKVError(f"lse must be a contiguous float32 [{total_q}, {Hqo}] tensor")
     B = lens_q.shape[0]
-    for t in (lens_q, lens_kv) + tuple(o for o in offsets if o is not None):
-        if t.dtype != torch.int32 or tuple(t.shape) != (B,) or not t.is_contiguous():
+    off_ptrs = (None, None, None, None)
+    lens = (lens_q, lens_kv)
+    oq, oo, ok, ov = offsets
+    if oq is not None or oo is not None or ok is not None or ov is not None:
+        lens += tuple(o for o in offsets if o is not None)
+        off_ptrs = tuple(_ptr(o) for o in offsets)
+    for t in lens:
+        if t.dtype != torch.int32 or t.dim() != 1 or t.numel() != B or not t.is_contiguous():
             raise PagedKVError(f"lengths and batch offsets must be contiguous int32 [{B}]")
-    bt_stride = 0
+    bt_ptr, bt_stride = None, 0
     if block_tables is not None:
-        if block_tables.dim() != 2 or block_tables.shape[0] < B or block_tables.dtype != torch.int32 \
-                or block_tables.stride(1) != 1:
+        bt = block_tables.stride()
+        if len(bt) != 2 or bt[1] != 1 or block_tables.shape[0] < B or block_tables.dtype != torch.int32:
             raise PagedKVError("block_tables must be int32 [>= batch_size, pages] with unit column stride")
-        bt_stride = block_tables.stride(0)
-    _same_device(q, k_cache, v_cache, workspace, lens_q, lens_kv, block_tables, out, lse, err_word, *offsets)
-    _check(load_library().paged_prefill_window(
-        _ptr(q), total_q, _ptr(k_cache), _ptr(v_cache), k_cache.stride(0), v_cache.stride(0), P, ks, vs, ss, block,
-        scale, _ptr(workspace), workspace.numel() * workspace.element_size(), max_q, max_kv, _ptr(lens_q),
-        _ptr(lens_kv), _ptr(block_tables), bt_stride, B, int(causal), window_left, first_tokens, Hqo, Hkv, d_qk, dv, S,
-        layout, dtype, _ptr(out), _ptr(lse), *(_ptr(o) for o in offsets), _ptr(err_word), _stream(stream)))
+        bt_ptr, bt_stride = _addr(block_tables), bt[0]
+    device = _same_device(q, k_cache, v_cache, workspace, block_tables, out, lse, err_word, *lens)
+    status = load_library().paged_prefill_window(
+        _addr(q), total_q, _addr(k_cache), _addr(v_cache), k_cache.stride(0), v_cache.stride(0), P, ks, vs, ss, block,
+        scale, _addr(workspace), workspace.nbytes, max_q, max_kv, _addr(lens_q), _addr(lens_kv), bt_ptr, bt_stride, B,
+        1 if causal else 0, window_left, first_tokens, Hqo, Hkv, d_qk, dv, S, layout, dtype, _addr(out), _addr(lse),
+        *off_ptrs, None if err_word is None else _addr(err_word), _stream_on(stream, device))
+    if status:
+        _check(status)
     return out, lse
