@@ -536,6 +536,8 @@ def _decode_window(query, kv_cache, workspace, block_tables, seq_lens, max_seq_l
     bt_stride = block_tables.stride()
     if len(bt_stride) != 2 or bt_stride[1] != 1 or block_tables.dtype != torch.int32 or block_tables.shape[0] < B:
         raise PagedKVError("block_tables must be int32 [>= batch_size, pages] with unit column stride")
+    if block_tables.shape[1] * S < max_seq_len:  # (a view's row stride may be wider than its columns)
+        raise PagedKVError("block_tables has fewer columns than max_seq_len needs")
     if sinks is not None:
         if sinks.dtype != torch.float32 or sinks.numel() != Hqo or not sinks.is_contiguous():
             raise PagedKVError(f"sinks must be contiguous float32 [{Hqo}]")
@@ -761,6 +763,8 @@ def _prefill_window(q, k_cache, v_cache, scale, workspace, max_q, max_kv, lens_q
         bt = block_tables.stride()
         if len(bt) != 2 or bt[1] != 1 or block_tables.shape[0] < B or block_tables.dtype != torch.int32:
             raise PagedKVError("block_tables must be int32 [>= batch_size, pages] with unit column stride")
+        if block_tables.shape[1] * S < max_kv:  # (a view's row stride may be wider than its columns)
+            raise PagedKVError("block_tables has fewer columns than max_sequence_kv needs")
         bt_ptr, bt_stride = _addr(block_tables), bt[0]
     device = _same_device(q, k_cache, v_cache, workspace, block_tables, out, lse, err_word, *lens)
     status = load_library().paged_prefill_window(

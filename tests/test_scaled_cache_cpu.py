@@ -109,3 +109,29 @@ def _prefill(lib, **over):  # noqa: F811
 ])
 def test_prefill_window_refuses(lib, over, status):  # noqa: F811
     assert _prefill(lib, **over) == status
+
+
+def test_binding_counts_the_columns_of_a_sliced_table(monkeypatch):
+    import paged_kv_cache_316_gb300 as pk
+    from paged_kv_cache_316_gb300 import binding
+    # (tensors on the CPU)
+    monkeypatch.setattr(binding, "split_cache", lambda c, layout: (0, 0, c.stride(0), 4, 8, 16, 128, c))
+    monkeypatch.setattr(binding, "_same_device", lambda *t: (_ for _ in ()).throw(pk.PagedKVError("past the shapes")))
+    cache = torch.zeros(4, 2, 8, 16, 128, dtype=torch.float8_e4m3fn)
+    sc = torch.ones(4, 2, 8, 1)
+    bt = torch.zeros(2, 8, dtype=torch.int32)[:, 4:]  # 4 columns, rows 8 apart
+    lens = torch.tensor([64, 64], dtype=torch.int32)
+    ws = torch.zeros(1 << 16, dtype=torch.uint8)
+    q = torch.zeros(2, 32, 128, dtype=torch.bfloat16)
+
+    def decode(n):
+        return pk.paged_decode(q, cache, ws, bt, lens, n, kv_scales=sc)
+
+    def prefill(n):
+        return pk.paged_prefill(q, cache[:, 0], cache[:, 1], 0.1, ws, 1, n, torch.ones_like(lens), lens, bt,
+                                kv_scales=sc)
+    for call in (decode, prefill):
+        with pytest.raises(pk.PagedKVError, match="fewer columns"):
+            call(65)
+        with pytest.raises(pk.PagedKVError, match="past the shapes"):
+            call(64)
