@@ -214,6 +214,26 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
     return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
 }
 
+// 4 x 4 transpose of 16-byte pieces over four neighbouring lanes: piece i of
+// lane q becomes what was piece q of lane i.
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4][4]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int d = 1; d <= 2; d *= 2) {
+        const bool up = lane & d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & d) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[i][e] : w[i + d][e], d);
+                w[i][e] = up ? got : w[i][e];
+                w[i + d][e] = up ? w[i + d][e] : got;
+            }
+        }
+    }
+}
+
 // Wait for this thread's tensor-memory loads, with the 32 destination
 // registers as operands so that no use of them can be scheduled before it.
 __device__ __forceinline__ void tmem_wait_ld_regs(uint32_t (&r)[32]) {
@@ -1000,7 +1020,12 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
             const bool valid = qi < it.qb && grow >= 0 && grow < p.total_q;
             if (kDebugBounds && qi < it.qb) dbg_in(grow, 1, p.total_q, p.err);
             const float inv = l > 0.f ? (p.v_scale ? __ldg(p.v_scale) : 1.f) / l : 0.f;
-            T *orow = static_cast<T *>(p.out) + (grow * p.Hqo + h) * kPfDV;
+            // A lane holds a row; four lanes trade 16-byte pieces so that a
+            // store instruction writes 64 bytes of 8 rows, whole sectors, and
+            // not 16 bytes of 32 rows (a line per lane and cycle).
+            const int r4 = r & ~3;
+            T *orow4 = static_cast<T *>(p.out) + ((static_cast<int64_t>(it.orow_base) + r4) * p.Hqo + h) * kPfDV + (r & 3) * 8;
+            const unsigned valid4 = __ballot_sync(0xffffffffu, valid) >> (lane & ~3);
 #pragma unroll
             for (int c = 0; c < kPfDV / 32; ++c) {
                 uint32_t ro[32];
@@ -1011,15 +1036,17 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) ro[e] = 0u;
                 }
-                if (valid) {
+                uint32_t w[4][4];  // [piece][word]
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        auto o = [&](int e) { return __uint_as_float(ro[q * 8 + e]) * inv; };
-                        uint4 w = make_uint4(pack2<T>(o(0), o(1)), pack2<T>(o(2), o(3)), pack2<T>(o(4), o(5)),
-                                             pack2<T>(o(6), o(7)));
-                        *reinterpret_cast<uint4 *>(orow + c * 32 + q * 8) = w;
-                    }
-                }
+                for (int e = 0; e < 16; ++e)
+                    w[e >> 2][e & 3] =
+                        pack2<T>(__uint_as_float(ro[2 * e]) * inv, __uint_as_float(ro[2 * e + 1]) * inv);
+                transpose4(w);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if ((valid4 >> i) & 1u)
+                        *reinterpret_cast<uint4 *>(orow4 + static_cast<int64_t>(i) * p.Hqo * kPfDV + c * 32) =
+                            make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
             }
             if (valid) p.lse[grow * p.Hqo + h] = l > 0.f ? (m_used + fast_log2(l)) * kLn2 : -INFINITY;
             tc_fence_before();  // O read before the next item's first PV_X overwrites it
