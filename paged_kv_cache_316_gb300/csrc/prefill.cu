@@ -38,16 +38,22 @@
 // PKV_DEV_ERR_TIMEOUT, the other roles stop, the copies in flight are
 // waited for, tensor memory is freed and the CTA returns.
 //
+// The roles' unrolled loops share the instruction caches, so what a tile does
+// not always need stays out of the loops' way: boxes, rare rescales, masks and
+// the epilogue are rolled loops (16 ragged prompts: 499 -> 465 us, d_qk 192
+// 585 -> 575; the MMA issue code rolled over the two blocks instead: slower,
+// 504 and 642, it sits between P and the next S).
+//
 // A sliding window that keeps the first tokens visible (WIN) leaves out the
 // key tiles that no row of a query tile sees, so an item's work follows the
 // window and not the sequence: 2048 queries at the end of 32768 keys, window
-// 4096, 32 heads: 129.5 us, 1.07 PFLOP/s over the visible pairs, 55% of the
+// 4096, 32 heads: 117.6 us, 1.18 PFLOP/s over the visible pairs, 60% of the
 // measured bf16 rate (256 items on 152 SMs fill two rounds to 84%).  8 ragged
-// prompts, d_qk 192, window 778 and 33 first tokens: 179 us, 40%: an item is 11
-// tiles of 96 keys for 8.5 tiles' worth of visible pairs, and its start and end
-// take as long as three.  The softmax masks with one word of bits for 32
-// columns and leaves alone what the whole warp sees (per-column compares:
-// 138 and 206 us).
+// prompts, d_qk 192, window 778 and 33 first tokens: 158.5 us, 45%: an item is 11
+// tiles of 96 keys for 8.5 tiles' worth of visible pairs, and between two items
+// the tensor cores wait about two tiles' time for Q (Q per block, from either
+// producer or from a warp of its own: no gain).  The masks are words of one bit
+// a column (per-column compares: 138 and 206 us where the words gave 129.5 and 179).
 #include <math.h>
 
 #include <type_traits>
@@ -572,52 +578,51 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
                     const int t = t_base + j;
                     const int pg = pg_next;
                     if (j + 1 < it.n_tiles) pg_next = lookup(j + 1);
-                    int pages[16];
-    #pragma unroll
-                    for (int i = 0; i < 16; ++i) pages[i] = __shfl_sync(0xffffffffu, pg, i);
-                    if (leader) {
-                        const int st = t % NS, us = t / NS;
-                        if (us > 0 && !mbar_wait(is_k ? b_kempty(st) : v_empty(st), (us - 1) & 1, abort_flag, wlim)) {
-                            give_up();
-                            ok = false;
-                        } else {
-                            const uint32_t full = is_k ? b_kfull(st) : v_full(st);
-                            mbar_expect_tx(full, is_k ? KB : (F8 ? V8B : VB));
-                            const int j0 = pf_key<WIN>(it, j, BN);
-    #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                if (i >= nbox) break;
-                                const int r0 = i * RB;
-                                const int slot0 = p.contiguous ? (is_k ? it.kv_k : it.kv_v) + j0 + r0
-                                                               : (j0 + r0) & (S - 1);
-                                const int ca = LAYOUT == PKV_HND ? slot0 : it.kvh;
-                                const int cb = LAYOUT == PKV_HND ? it.kvh : slot0;
-                                // (debug build) a box starts on a pool page or on the
-                                // zero-fill page and stays inside its page; the tensor
-                                // map bounds every copy in hardware, so the copy is
-                                // issued regardless and the barrier's byte count holds
-                                if (kDebugBounds && !p.contiguous) {
-                                    dbg_in(pages[i], 1, p.max_num_pages + 1, p.err);
-                                    dbg_in(slot0, RB, S, p.err);
-                                }
-                                if (is_k && K5 && p.k5) {  // every atom of the page part in one copy
-                                    tma_load_5d(k_s + st * KB + r0 * (QA * 128), &tm_k, full, 0, 0, 0, slot0 >> 3,
-                                                pages[i] * p.k5_ratio + it.kvh);
-                                } else if (is_k) {
-                                    for (int c = 0; c < QA; ++c)
-                                        tma_load_4d(k_s + st * KB + c * (BN * 128) + r0 * 128, &tm_k, full,
-                                                    c * (128 / ES), ca, cb, pages[i]);
-                                } else if (F8) {  // one 128-byte atom: a whole E4M3 row
-                                    tma_load_4d(v8_s + st * V8B + r0 * 128, &tm_v, full, 0, ca, cb, pages[i]);
-                                } else {
-                                    for (int c = 0; c < kPfDV / 64; ++c)
-                                        tma_load_4d(v_s + st * VB + c * (BN * 128) + r0 * 128, &tm_v, full, c * 64, ca,
-                                                    cb, pages[i]);
-                                }
-                            }
-                            t_next = t + 1;
-                            if (is_k && j == 0) load_q();
+                    const int st = t % NS, us = t / NS;
+                    if (leader && us > 0 && !mbar_wait(is_k ? b_kempty(st) : v_empty(st), (us - 1) & 1, abort_flag, wlim)) {
+                        give_up();
+                        ok = false;
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok, leader_lane);
+                    if (!ok) break;
+                    const uint32_t full = is_k ? b_kfull(st) : v_full(st);
+                    if (leader) mbar_expect_tx(full, is_k ? KB : (F8 ? V8B : VB));
+                    const int j0 = pf_key<WIN>(it, j, BN);
+                    // (a rolled loop: sixteen boxes unrolled crowd the softmax
+                    // warps' code out of the instruction cache)
+#pragma unroll 1
+                    for (int i = 0; i < nbox; ++i) {
+                        const int page = __shfl_sync(0xffffffffu, pg, i);
+                        if (!leader) continue;
+                        const int r0 = i * RB;
+                        const int slot0 = p.contiguous ? (is_k ? it.kv_k : it.kv_v) + j0 + r0 : (j0 + r0) & (S - 1);
+                        const int ca = LAYOUT == PKV_HND ? slot0 : it.kvh;
+                        const int cb = LAYOUT == PKV_HND ? it.kvh : slot0;
+                        // (debug build) a box starts on a pool page or on the
+                        // zero-fill page and stays inside its page; the tensor
+                        // map bounds every copy in hardware, so the copy is
+                        // issued regardless and the barrier's byte count holds
+                        if (kDebugBounds && !p.contiguous) {
+                            dbg_in(page, 1, p.max_num_pages + 1, p.err);
+                            dbg_in(slot0, RB, S, p.err);
                         }
+                        if (is_k && K5 && p.k5) {  // every atom of the page part in one copy
+                            tma_load_5d(k_s + st * KB + r0 * (QA * 128), &tm_k, full, 0, 0, 0, slot0 >> 3,
+                                        page * p.k5_ratio + it.kvh);
+                        } else if (is_k) {
+                            for (int c = 0; c < QA; ++c)
+                                tma_load_4d(k_s + st * KB + c * (BN * 128) + r0 * 128, &tm_k, full, c * (128 / ES), ca,
+                                            cb, page);
+                        } else if (F8) {  // one 128-byte atom: a whole E4M3 row
+                            tma_load_4d(v8_s + st * V8B + r0 * 128, &tm_v, full, 0, ca, cb, page);
+                        } else {
+                            for (int c = 0; c < kPfDV / 64; ++c)
+                                tma_load_4d(v_s + st * VB + c * (BN * 128) + r0 * 128, &tm_v, full, c * 64, ca, cb, page);
+                        }
+                    }
+                    if (leader) {
+                        t_next = t + 1;
+                        if (is_k && j == 0) load_q();
                     }
                     ok = __shfl_sync(0xffffffffu, ok, leader_lane);
                     if (!ok) break;
@@ -856,33 +861,21 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
         auto wait_warp = [&](uint32_t bar, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, wlim));
         };
-        // scores of chunk i of the tile at key offset j0: scaled if the scale
-        // is not positive, masked past the row's last key
-        auto scale_mask = [&](int i, int j0, bool warp_full, int lim, int row_lo, uint32_t(&ra)[32]) {
-            if (!pos_scale) {
-#pragma unroll
-                for (int c = 0; c < 32; ++c) ra[c] = __float_as_uint(__uint_as_float(ra[c]) * sc);
-            }
-            if constexpr (WIN) {
-                // one bit for each column: at most lim, and not of the keys
-                // [first_tokens, row_lo); a chunk that the whole warp sees
-                // (most of a boundary tile) is left as it is
-                if (!warp_full) {
-                    const int j = j0 + 32 * i;
-                    const uint32_t hidden = ~low_bits(lim - j + 1) | (low_bits(row_lo - j) & ~low_bits(p.first_tokens - j));
-                    if (__any_sync(0xffffffffu, hidden != 0u)) {
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (hidden & (1u << c)) ra[c] = __float_as_uint(-INFINITY);
-                    }
-                }
-            } else if (!warp_full) {
-                const int lr = lim - (j0 + 32 * i);  // last visible column of the chunk
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    if (c > lr) ra[c] = __float_as_uint(-INFINITY);
-            }
+        // the columns of chunk i of the tile at key offset j0 that a row does not
+        // see, one bit each: past its last key and (WIN) the keys
+        // [first_tokens, row_lo); a chunk that the whole warp sees is left alone
+        auto hidden_of = [&](int i, int j0, int lim, int row_lo) {
+            const int j = j0 + 32 * i;
+            uint32_t hidden = ~low_bits(lim - j + 1);
+            if constexpr (WIN) hidden |= low_bits(row_lo - j) & ~low_bits(p.first_tokens - j);
+            return hidden;
         };
+        // Where the masks are applied.  Both ways measured: the loop without them
+        // is short enough for the instruction cache at d_qk 128 (8 ragged prompts
+        // 199 against 202 us); at d_qk 192, with a quarter fewer scores a tile,
+        // the detour of the masked tiles costs more (164 against 159 us).
+        constexpr bool MASK_FIRST = DQK == 128;
+
         auto chunk_max = [&](const uint32_t(&ra)[32]) {
             float m3[4];
 #pragma unroll
@@ -940,6 +933,27 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
                 tc_fence_after();
                 const bool warp_full = __all_sync(0xffffffffu, j0 + BN - 1 <= lim &&
                                                                       (!WIN || j0 >= row_lo || j0 + BN <= p.first_tokens));
+                // Rare work is done in place first, in a rolled loop, out of the way
+                // of the common tile's code: a scale that is not positive, and
+                // (MASK_FIRST) the mask of a tile with keys that a row of the warp
+                // does not see.
+                if (!pos_scale || (MASK_FIRST && !warp_full)) {
+#pragma unroll 1
+                    for (int i = 0; i < NCH; ++i) {
+                        const uint32_t hidden = MASK_FIRST ? hidden_of(i, j0, lim, row_lo) : 0u;
+                        if (pos_scale && !__any_sync(0xffffffffu, hidden != 0u)) continue;
+                        uint32_t ra[32];
+                        tmem_ld32(s_addr + 32 * i, ra);
+                        tmem_wait_ld_regs(ra);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            if (!pos_scale) ra[c] = __float_as_uint(__uint_as_float(ra[c]) * sc);
+                            if (MASK_FIRST && (hidden & (1u << c))) ra[c] = __float_as_uint(-INFINITY);
+                        }
+                        tmem_st32(s_addr + 32 * i, ra);
+                    }
+                    tmem_wait_st();
+                }
                 uint32_t rs[NCH][32];
 #pragma unroll
                 for (int i = 0; i < NCH; ++i) tmem_ld32(s_addr + 32 * i, rs[i]);
@@ -948,7 +962,14 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
                 float mh = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < NCH; ++i) {
-                    scale_mask(i, j0, warp_full, lim, row_lo, rs[i]);
+                    if (!MASK_FIRST && !warp_full) {
+                        const uint32_t hidden = hidden_of(i, j0, lim, row_lo);
+                        if (__any_sync(0xffffffffu, hidden != 0u)) {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (hidden & (1u << c)) rs[i][c] = __float_as_uint(-INFINITY);
+                        }
+                    }
                     mh = fmaxf(mh, chunk_max(rs[i]));
                 }
                 const float mt = pos_scale ? mh * sc : mh;
@@ -995,7 +1016,7 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
                 // complete (S_X(t) is), and at the item's first tile O is
                 // about to be overwritten anyway
                 if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < kPfDV / 32; ++c) {
                         uint32_t ro[32];
                         tmem_ld32(o_addr + c * 32, ro);
@@ -1026,7 +1047,7 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
             const int r4 = r & ~3;
             T *orow4 = static_cast<T *>(p.out) + ((static_cast<int64_t>(it.orow_base) + r4) * p.Hqo + h) * kPfDV + (r & 3) * 8;
             const unsigned valid4 = __ballot_sync(0xffffffffu, valid) >> (lane & ~3);
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < kPfDV / 32; ++c) {
                 uint32_t ro[32];
                 if (have) {
