@@ -196,31 +196,31 @@ def split_cache(kv_cache, layout: int):
     """(k_ptr, v_ptr, page_stride, num_pages, num_heads, page_size, head_dim)
     for a 5-D [P, 2, ...] tensor or a (k, v) tuple of 4-D tensors."""
     if isinstance(kv_cache, (tuple, list)):
-        k, v = kv_cache
-        if k.shape != v.shape or k.stride(0) != v.stride(0):
+        base, v = kv_cache
+        shape, stride = base.shape, base.stride(0)
+        if v.shape != shape or v.stride(0) != stride:
             raise PagedKVError("K and V caches must have the same shape and page stride")
-        base = k
-        kp, vp = k.data_ptr(), v.data_ptr()
-        for t in (k, v):
-            if not _rows_contiguous(t):
-                raise PagedKVError("each page must be contiguous")
-        shape = k.shape[1:]
-    else:
-        if kv_cache.dim() != 5 or kv_cache.shape[1] != 2:
-            raise PagedKVError("a single kv_cache tensor must be [pages, 2, ...]")
-        if not _rows_contiguous(kv_cache):
+        if not (_rows_contiguous(base) and _rows_contiguous(v)):
             raise PagedKVError("each page must be contiguous")
+        kp, vp = base.data_ptr(), v.data_ptr()
+        P, H, S, D = shape
+    else:
         base = kv_cache
-        kp = kv_cache.data_ptr()
-        vp = kp + kv_cache.stride(1) * kv_cache.element_size()
-        shape = kv_cache.shape[2:]
+        shape = base.shape
+        if len(shape) != 5 or shape[1] != 2:
+            raise PagedKVError("a single kv_cache tensor must be [pages, 2, ...]")
+        if not _rows_contiguous(base):
+            raise PagedKVError("each page must be contiguous")
+        strides = base.stride()
+        stride = strides[0]
+        kp = base.data_ptr()
+        vp = kp + strides[1] * base.element_size()
+        P, _, H, S, D = shape
     if not base.is_cuda:
         raise PagedKVError("tensor arguments must live on a CUDA device")
-    if layout == HND:
-        H, S, D = shape
-    else:
-        S, H, D = shape
-    return kp, vp, base.stride(0), base.shape[0], H, S, D, base
+    if layout != HND:
+        H, S = S, H
+    return kp, vp, stride, P, H, S, D, base
 
 
 def base_dtype(kv_cache) -> torch.dtype:
@@ -234,14 +234,14 @@ def split_scales(kv_scales, num_pages: int, num_heads: int, page_size: int, devi
     if isinstance(kv_scales, (tuple, list)):
         k, v = kv_scales
         shape, stride = k.shape, k.stride()
-        if k.dim() != 3 or v.shape != shape or v.stride() != stride:
+        if len(shape) != 3 or v.shape != shape or v.stride() != stride:
             raise PagedKVError("K and V scales must be [pages, heads, blocks] of the same shape and strides")
         same = v.dtype == torch.float32 and v.get_device() == k.get_device()
         vp = v.data_ptr()
     else:
         k = kv_scales
         shape, stride = k.shape, k.stride()
-        if k.dim() != 4 or shape[1] != 2:
+        if len(shape) != 4 or shape[1] != 2:
             raise PagedKVError("a single kv_scales tensor must be [pages, 2, heads, blocks]")
         vp = k.data_ptr() + 4 * stride[1]
         shape, stride, same = (shape[0], shape[2], shape[3]), (stride[0], stride[2], stride[3]), True
@@ -496,7 +496,7 @@ def _decode_window(query, kv_cache, workspace, block_tables, seq_lens, max_seq_l
     rows, Hqo, Dq = shape
     if Dq != D:
         raise PagedKVError("query head_dim differs from the cache's")
-    if seq_lens.dim() != 1:
+    if seq_lens.dim() != 1 or seq_lens.element_size() != 4 or not seq_lens.is_contiguous():
         raise PagedKVError("seq_lens must be a contiguous 1-D tensor of 32-bit lengths")
     B = seq_lens.shape[0]
     dtype = _decode_dtype(query, base)
@@ -531,12 +531,10 @@ def _decode_window(query, kv_cache, workspace, block_tables, seq_lens, max_seq_l
         if lse.dtype != torch.float32 or lse.shape != shape[:2] or not lse.is_contiguous():
             raise PagedKVError(f"lse must be a contiguous float32 [{rows}, {Hqo}] tensor")
         lse_ptr = _addr(lse)
-    if seq_lens.element_size() != 4 or not seq_lens.is_contiguous():
-        raise PagedKVError("seq_lens must be a contiguous 1-D tensor of 32-bit lengths")
-    bt_stride = block_tables.stride()
-    if len(bt_stride) != 2 or bt_stride[1] != 1 or block_tables.dtype != torch.int32 or block_tables.shape[0] < B:
+    bt_shape, bt_stride = block_tables.shape, block_tables.stride()
+    if len(bt_shape) != 2 or bt_stride[1] != 1 or block_tables.dtype != torch.int32 or bt_shape[0] < B:
         raise PagedKVError("block_tables must be int32 [>= batch_size, pages] with unit column stride")
-    if block_tables.shape[1] * S < max_seq_len:  # (a view's row stride may be wider than its columns)
+    if bt_shape[1] * S < max_seq_len:  # (a view's row stride may be wider than its columns)
         raise PagedKVError("block_tables has fewer columns than max_seq_len needs")
     if sinks is not None:
         if sinks.dtype != torch.float32 or sinks.numel() != Hqo or not sinks.is_contiguous():
