@@ -50,9 +50,11 @@
 // 4096, 32 heads: 117.6 us, 1.18 PFLOP/s over the visible pairs, 60% of the
 // measured bf16 rate (256 items on 152 SMs fill two rounds to 84%).  8 ragged
 // prompts, d_qk 192, window 778 and 33 first tokens: 158.5 us, 45%: an item is 11
-// tiles of 96 keys for 8.5 tiles' worth of visible pairs, and between two items
-// the tensor cores wait about two tiles' time for Q (Q per block, from either
-// producer or from a warp of its own: no gain).  The masks are words of one bit
+// tiles of 96 keys for 8.5 tiles' worth of visible pairs, and its first S comes
+// 4,600 cycles after the last P of the item before, 1,500 within an item: Q (96
+// KB) lands last.  (Q per block, from either producer or a warp of its own, Q
+// ahead of the first K tile, the next item taken a tile early: no gain.)  The
+// masks are words of one bit
 // a column (per-column compares: 138 and 206 us where the words gave 129.5 and 179).
 #include <math.h>
 
@@ -1043,7 +1045,8 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
             const float inv = l > 0.f ? (p.v_scale ? __ldg(p.v_scale) : 1.f) / l : 0.f;
             // A lane holds a row; four lanes trade 16-byte pieces so that a
             // store instruction writes 64 bytes of 8 rows, whole sectors, and
-            // not 16 bytes of 32 rows (a line per lane and cycle).
+            // not 16 bytes of 32 rows (a line per lane and cycle): 499 against
+            // 512 us for 16 ragged prompts, 585 against 610 at d_qk 192.
             const int r4 = r & ~3;
             T *orow4 = static_cast<T *>(p.out) + ((static_cast<int64_t>(it.orow_base) + r4) * p.Hqo + h) * kPfDV + (r & 3) * 8;
             const unsigned valid4 = __ballot_sync(0xffffffffu, valid) >> (lane & ~3);
