@@ -577,7 +577,8 @@ int paged_prefill_fp8(const void *q, int64_t total_q, const void *k_cache,
  * paged_prefill_scaled_workspace_size -- bytes of device workspace that
  * paged_prefill_window needs over E4M3 caches with block scales: the plain
  * prefill's and room for the dequantised keys and values
- * (batch_size * max_sequence_kv tokens in 16 bits).
+ * (batch_size * max_sequence_kv tokens in 16 bits, and two floats for each
+ * request and kv head).
  */
 size_t paged_prefill_scaled_workspace_size(int32_t batch_size, int32_t num_qo_heads,
                                            int32_t num_kv_heads,
@@ -604,9 +605,11 @@ size_t paged_prefill_scaled_workspace_size(int32_t batch_size, int32_t num_qo_he
  *    layout for K and V, whatever d_qk and d_vo are); strides in E4M3
  *    elements, multiples of 16; workspace >=
  *    paged_prefill_scaled_workspace_size(...).  Keys and values are
- *    dequantised to the query's 16-bit type first: exact when the scales are
- *    powers of two and the products lie in that type's range, as those of a
- *    cache that paged_append_scaled filled from it do; else rounded once.
+ *    dequantised to the query's 16-bit type first, in fp16 divided by a power
+ *    of two that is given back in fp32, so that no product leaves fp16's
+ *    range.  Exact when the scales are powers of two, else rounded once; fp16
+ *    resolves 2^-31 of the largest scale among the request's visible blocks of
+ *    the head (K and V apart): a product is off by at most half of that too.
  *  - batch_offsets_*: as paged_prefill_ex (each may be NULL; offsets of K and
  *    V with contiguous K/V only).
  *  - Keys and values that no query of the request sees may hold anything; a

@@ -140,18 +140,20 @@ struct PrefillParams {
     // WIN: the query at position p sees key j iff j >= p - window_left or
     // j < first_tokens (and, causal, j <= p)
     int window_left, first_tokens;
+    // fp16 over dequantised caches: the power of two that each request and kv
+    // head's keys, then values, were multiplied by ([2][B][Hkv]), or NULL
+    const float *kv_factor;
 };
 
 // cu_q / cu_kv = exclusive prefix sums of the query / kv lengths and
 // cu_items = U x the exclusive prefix sum of the 128-row query tiles (one
 // warp, 32 requests at a time); flags lengths above their maxima and requests with fewer keys
 // than queries; zeroes the work-item counter.
-__global__ void prefill_plan_kernel(const int32_t *__restrict__ lq, const int32_t *__restrict__ lkv,
-                                    int B, int U, int max_q, int max_kv, int32_t *__restrict__ cu_q,
-                                    int32_t *__restrict__ cu_items, int32_t *__restrict__ cu_kv,
-                                    int32_t *err, int *work_counter) {
+__device__ __forceinline__ void plan_requests(const int32_t *__restrict__ lq, const int32_t *__restrict__ lkv, int B,
+                                              int U, int max_q, int max_kv, int32_t *__restrict__ cu_q,
+                                              int32_t *__restrict__ cu_items, int32_t *__restrict__ cu_kv,
+                                              int32_t *err, int *work_counter) {
     const int lane = threadIdx.x;
-    pdl_launch_dependents();  // the main kernel may start its prologue meanwhile
     int carry = 0, carry_t = 0, carry_k = 0;
     for (int b0 = 0; b0 < B; b0 += 32) {
         int b = b0 + lane;
@@ -189,6 +191,12 @@ __global__ void prefill_plan_kernel(const int32_t *__restrict__ lq, const int32_
         *work_counter = 0;
     }
 }
+__global__ void prefill_plan_kernel(const int32_t *__restrict__ lq, const int32_t *__restrict__ lkv, int B, int U,
+                                    int max_q, int max_kv, int32_t *__restrict__ cu_q, int32_t *__restrict__ cu_items,
+                                    int32_t *__restrict__ cu_kv, int32_t *err, int *work_counter) {
+    pdl_launch_dependents();  // the main kernel may start its prologue meanwhile
+    plan_requests(lq, lkv, B, U, max_q, max_kv, cu_q, cu_items, cu_kv, err, work_counter);
+}
 
 template <typename T>
 struct IsBf16 {
@@ -216,6 +224,9 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
+
+// 1 / x for x a power of two in fp32's normal range
+__device__ __forceinline__ float inverse_pow2(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
 
 // The n low bits set (none for n <= 0, all for n >= 32).
 __device__ __forceinline__ uint32_t low_bits(int n) {
@@ -856,10 +867,14 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * qd) << 16);
         const uint32_t s_addr = t_lane + X * S_STRIDE;
         const uint32_t o_addr = t_lane + O_COL + X * kPfDV;
-        const float sc = p.scale_log2 * (p.q_scale ? __ldg(p.q_scale) : 1.f) * (p.k_scale ? __ldg(p.k_scale) : 1.f);
+        float sc = p.scale_log2 * (p.q_scale ? __ldg(p.q_scale) : 1.f) * (p.k_scale ? __ldg(p.k_scale) : 1.f);
         const bool pos_scale = sc > 0.f;  // max on raw scores, one FFMA scales and shifts
         const float k_mul = pos_scale ? sc : 1.f;
-        const float2 kk2 = make_float2(k_mul, k_mul);
+        float2 kk2 = make_float2(k_mul, k_mul);
+        // (fp16: sc and the output follow the item's factors, kv_factor)
+        constexpr bool FACTOR = std::is_same<T, __half>::value && !F8;
+        const float sc_all = sc;
+        float v_mul = 1.f;
         auto wait_warp = [&](uint32_t bar, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, wlim));
         };
@@ -926,6 +941,12 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
             const int lim = p.causal ? min(pos, it.kvb - 1) : it.kvb - 1;  // last visible key
             // (WIN) the row does not see the keys [first_tokens, row_lo)
             const int row_lo = WIN ? max(0, pos - p.window_left) : 0;
+            if (FACTOR && p.kv_factor) {
+                const float *f = p.kv_factor + static_cast<int64_t>(it.b) * p.Hkv + it.kvh;
+                sc = sc_all * inverse_pow2(f[0]);
+                if (pos_scale) kk2 = make_float2(sc, sc);
+                v_mul = inverse_pow2(f[static_cast<int64_t>(p.B) * p.Hkv]);
+            }
             float m_used = -INFINITY, l = 0.f;
             for (int j = 0; j < n; ++j) {
                 const int t = t_base + j, tx = tx_base + j;
@@ -1042,7 +1063,8 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
             const int64_t grow = static_cast<int64_t>(it.orow_base) + r;
             const bool valid = qi < it.qb && grow >= 0 && grow < p.total_q;
             if (kDebugBounds && qi < it.qb) dbg_in(grow, 1, p.total_q, p.err);
-            const float inv = l > 0.f ? (p.v_scale ? __ldg(p.v_scale) : 1.f) / l : 0.f;
+            float inv = l > 0.f ? (p.v_scale ? __ldg(p.v_scale) : 1.f) / l : 0.f;
+            if constexpr (FACTOR) inv *= v_mul;
             // A lane holds a row; four lanes trade 16-byte pieces so that a
             // store instruction writes 64 bytes of 8 rows, whole sectors, and
             // not 16 bytes of 32 rows (a line per lane and cycle): 499 against
@@ -1152,7 +1174,66 @@ struct WidenKvParams {
     int64_t scale_stride;
     int block_shift, window_left, first_tokens, bn, max_q;
     const int32_t *seq_lens_q;
+    // fp16: [2][B][Hkv] powers of two that the products are multiplied by
+    float *factor;
 };
+
+// The plan, and beside it (fp16 over caches with block scales) the factors.
+// A product of a code and its scale may lie outside fp16's range: an fp16
+// value from 63488 on rounds to the code 256 under the scale 2^8, 65536, and a
+// caller's scales may be anything in [2^-48, 2^48].  So CTA (1 + z Hkv + h, b)
+// takes the largest scale 2^e (rounded up) of the blocks of K (z 0) or V (z 1)
+// of head h that hold a key some query of request b sees, and the products are
+// held times 2^(7 - e): at most 448 * 2^7 = 57344.  The logit scale and the
+// output take the inverse in fp32, all exact.  fp16's smallest step is then
+// 2^(e - 31): products under scales down to 2^(e - 22) lose nothing, under
+// smaller ones at most 2^(e - 32).  The scan runs beside the plan's one warp:
+// no launch more.
+constexpr int kFactorThreads = 256;
+__global__ void __launch_bounds__(kFactorThreads)
+    prefill_plan_factor_kernel(const int32_t *__restrict__ lq, const int32_t *__restrict__ lkv, int B, int U, int max_q,
+                               int max_kv, int32_t *__restrict__ cu_q, int32_t *__restrict__ cu_items,
+                               int32_t *__restrict__ cu_kv, int32_t *err, int *work_counter, const WidenKvParams w) {
+    pdl_launch_dependents();
+    if (blockIdx.x == 0) {
+        if (blockIdx.y == 0 && threadIdx.x < 32)
+            plan_requests(lq, lkv, B, U, max_q, max_kv, cu_q, cu_items, cu_kv, err, work_counter);
+        return;
+    }
+    const int b = blockIdx.y, z = (blockIdx.x - 1) / w.Hkv, h = (blockIdx.x - 1) - z * w.Hkv;
+    const int kvb = min(max(lkv[b], 0), max_kv);
+    const int G = 1 << w.block_shift, per_page_shift = w.page_shift - w.block_shift;
+    // blocks [0, n1) and [b2, the end): those with keys below first_tokens or from lo on
+    int n1 = 0, b2 = 0;
+    if (w.window_left >= 0) {
+        const int lo = kvb - min(max(lq[b], 0), max_q) - w.window_left;
+        if (lo > w.first_tokens) {
+            n1 = (w.first_tokens + G - 1) >> w.block_shift;
+            b2 = max(lo >> w.block_shift, n1);
+        }
+    }
+    const int n = n1 + max(((kvb + G - 1) >> w.block_shift) - b2, 0);
+    const int32_t *bt = w.block_tables + b * w.bt_stride;
+    float most = 0.f;
+    for (int i = threadIdx.x; i < n; i += kFactorThreads) {
+        const int blk = i < n1 ? i : b2 + i - n1;
+        const int page = bt[blk >> per_page_shift];
+        if (page < 0 || page >= w.max_num_pages) continue;  // (flagged where its keys are dequantised)
+        most = fmaxf(most, checked_scale(w.scales[z][page * w.scale_stride + (static_cast<int64_t>(h) << per_page_shift) +
+                                                     (blk & ((1 << per_page_shift) - 1))],
+                                         nullptr));
+    }
+    __shared__ uint32_t warp_most[kFactorThreads / 32];
+    uint32_t u = __reduce_max_sync(0xffffffffu, __float_as_uint(most));  // (patterns of numbers >= 0 are in order)
+    if ((threadIdx.x & 31) == 0) warp_most[threadIdx.x >> 5] = u;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < kFactorThreads / 32; ++i) u = max(u, warp_most[i]);
+        const int e = static_cast<int>(u >> 23) - 127 + ((u & 0x7fffffu) != 0);
+        w.factor[(static_cast<int64_t>(z) * B + b) * w.Hkv + h] =
+            u == 0 ? 1.f : __uint_as_float(static_cast<uint32_t>(7 - e + 127) << 23);
+    }
+}
 constexpr int kWidenTok = 32;  // keys per CTA of the cache widening
 // with scales: each key's rows are three dependent reads away (page, row,
 // scale), so shorter CTAs keep more of them in flight (two requests of 512
@@ -1163,12 +1244,14 @@ constexpr int kDequantTok = 8;
 // becomes 32 bytes of the packed 16-bit tensor.  A page id outside the pool
 // flags PKV_DEV_ERR_PAGE and its rows widen to zeros, as the 16-bit path's
 // zero-filled rows.
-// SCL: the values are multiplied by their block's scale (one rounding to T,
-// none when the scale is a power of two and the product is in T's range).
+// SCL: the values are multiplied by their block's scale and (fp16) by their
+// head's factor: one rounding to T, none for a scale that is a power of two
+// (fp16: and less than 2^22 below the head's largest).
 template <typename T, int LAYOUT, bool SCL = false>
 __global__ void __launch_bounds__(256) prefill_widen_kv_kernel(const WidenKvParams w) {
     constexpr int kTok = SCL ? kDequantTok : kWidenTok;
-    pdl_wait();  // cu_kv
+    constexpr bool FACTOR = SCL && std::is_same<T, __half>::value;
+    pdl_wait();  // cu_kv, the factors
     pdl_launch_dependents();
     const int b = blockIdx.y, z = blockIdx.z;
     const int kvb = min(max(w.seq_lens_kv[b], 0), w.max_kv);
@@ -1216,6 +1299,7 @@ __global__ void __launch_bounds__(256) prefill_widen_kv_kernel(const WidenKvPara
                                          (static_cast<int64_t>(h) << (w.page_shift - w.block_shift)) +
                                          ((j & (S - 1)) >> w.block_shift)),
                                    w.err);
+            if constexpr (FACTOR) sc *= w.factor[(static_cast<int64_t>(z) * gridDim.y + b) * w.Hkv + h];
         }
         const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
         uint32_t o[8];
@@ -1501,9 +1585,15 @@ static int prefill_impl(const void *q, int64_t total_q, const void *k_cache,
     int32_t *cu_kv = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + 2 * cu_bytes);
     int *work_counter = reinterpret_cast<int *>(static_cast<char *>(workspace) + 3 * cu_bytes);
     const int pairs = (num_qo_heads / num_kv_heads + 1) / 2;  // head pairs per kv head
-    prefill_plan_kernel<<<1, 32, 0, st>>>(actual_seq_lens_q, actual_seq_lens_kv, batch_size, num_kv_heads * pairs,
-                                          max_token_per_sequence, max_sequence_kv, cu_q, cu_items, cu_kv, err_word,
-                                          work_counter);
+    const bool factor = f8 && f8->scaled && dtype == PKV_F16;
+    if (factor)
+        prefill_plan_factor_kernel<<<dim3(1 + 2 * num_kv_heads, batch_size), kFactorThreads, 0, st>>>(
+            actual_seq_lens_q, actual_seq_lens_kv, batch_size, num_kv_heads * pairs, max_token_per_sequence,
+            max_sequence_kv, cu_q, cu_items, cu_kv, err_word, work_counter, f8->widen);
+    else
+        prefill_plan_kernel<<<1, 32, 0, st>>>(actual_seq_lens_q, actual_seq_lens_kv, batch_size, num_kv_heads * pairs,
+                                              max_token_per_sequence, max_sequence_kv, cu_q, cu_items, cu_kv, err_word,
+                                              work_counter);
     ++launches;
     if (f8 && f8->kv8) {
         // widen the E4M3 caches (needs cu_kv); the main kernel then reads them
@@ -1566,6 +1656,7 @@ static int prefill_impl(const void *q, int64_t total_q, const void *k_cache,
     p.k5_ratio = k5_ratio;
     p.window_left = window_left;
     p.first_tokens = first_tokens;
+    p.kv_factor = factor ? f8->widen.factor : nullptr;
     const int n_qt = (max_token_per_sequence + kPfRows - 1) / kPfRows;
     const int64_t items = static_cast<int64_t>(n_qt) * num_kv_heads * pairs * batch_size;
     if (n_qt > 0) {
@@ -1751,6 +1842,11 @@ extern "C" int paged_prefill_fp8(const void *q, int64_t total_q, const void *k_c
 
 // ---- a window with first tokens; E4M3 caches with block scales -------------------
 
+// after the fp8 path's areas: the fp16 factors
+static size_t prefill_factor_bytes(int B, int Hkv) {
+    return round_up(2 * static_cast<size_t>(B) * Hkv * sizeof(float), 256);
+}
+
 extern "C" size_t paged_prefill_scaled_workspace_size(int32_t batch_size, int32_t num_qo_heads, int32_t num_kv_heads,
                                                       int32_t max_token_per_sequence, int32_t max_sequence_kv,
                                                       int32_t d_qk, int32_t d_vo) {
@@ -1759,7 +1855,8 @@ extern "C" size_t paged_prefill_scaled_workspace_size(int32_t batch_size, int32_
         return 0;
     size_t a, b, c;
     return prefill_fp8_ws_bytes(batch_size, num_qo_heads, num_kv_heads, max_sequence_kv, 0, d_qk, d_vo, false, true, &a,
-                                &b, &c);
+                                &b, &c) +
+           prefill_factor_bytes(batch_size, num_kv_heads);
 }
 
 extern "C" int paged_prefill_window(const void *q, int64_t total_q, const void *k_cache, const void *v_cache,
@@ -1821,11 +1918,14 @@ extern "C" int paged_prefill_window(const void *q, int64_t total_q, const void *
     const size_t need = prefill_fp8_ws_bytes(batch_size, num_qo_heads, num_kv_heads, max_sequence_kv, total_q, d_qk,
                                              d_vo, false, true, &q_off, &k_off, &v_off);
     if (!workspace) return PKV_ERR_NULL;
-    if (workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)) return PKV_ERR_WORKSPACE;
+    if (workspace_bytes < need + prefill_factor_bytes(batch_size, num_kv_heads) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255))
+        return PKV_ERR_WORKSPACE;
     char *ws = static_cast<char *>(workspace);
     PrefillFp8 f8;
     f8.kv8 = true;
     f8.scaled = true;
+    f8.widen.factor = reinterpret_cast<float *>(ws + need);
     f8.layout = layout;
     WidenKvParams &w = f8.widen;
     w.src[0] = static_cast<const uint8_t *>(k_cache);
