@@ -612,8 +612,11 @@ size_t paged_prefill_scaled_workspace_size(int32_t batch_size, int32_t num_qo_he
  *    the head (K and V apart): a product is off by at most half of that too.
  *  - batch_offsets_*: as paged_prefill_ex (each may be NULL; offsets of K and
  *    V with contiguous K/V only).
- *  - Keys and values that no query of the request sees may hold anything; a
- *    NaN or infinity in a value that some of its queries see may reach others.
+ *  - Keys and values that no query of the request sees may hold anything.  A
+ *    NaN key, or a logit of plus infinity, makes the rows that see it NaN, out
+ *    and lse; a NaN in a value that column of their out, an infinity infinite
+ *    or NaN, lse not.  A NaN or infinity in a value that some of the request's
+ *    queries see may reach that column of others.
  *    Calls that may overlap on the GPU take a workspace each.
  * Device errors as paged_prefill, and PKV_DEV_ERR_SCALE (see
  * paged_decode_window).

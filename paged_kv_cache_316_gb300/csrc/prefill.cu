@@ -143,6 +143,9 @@ struct PrefillParams {
     // fp16 over dequantised caches: the power of two that each request and kv
     // head's keys, then values, were multiplied by ([2][B][Hkv]), or NULL
     const float *kv_factor;
+    // a row whose sum is NaN (a visible key is NaN) has NaN as its lse too;
+    // else -inf, as paged_prefill has always given
+    int nan_lse;
 };
 
 // cu_q / cu_kv = exclusive prefix sums of the query / kv lengths and
@@ -1063,7 +1066,8 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
             const int64_t grow = static_cast<int64_t>(it.orow_base) + r;
             const bool valid = qi < it.qb && grow >= 0 && grow < p.total_q;
             if (kDebugBounds && qi < it.qb) dbg_in(grow, 1, p.total_q, p.err);
-            float inv = l > 0.f ? (p.v_scale ? __ldg(p.v_scale) : 1.f) / l : 0.f;
+            const float no_sum = l != l && p.nan_lse ? l : 0.f;
+            float inv = l > 0.f ? (p.v_scale ? __ldg(p.v_scale) : 1.f) / l : no_sum;
             if constexpr (FACTOR) inv *= v_mul;
             // A lane holds a row; four lanes trade 16-byte pieces so that a
             // store instruction writes 64 bytes of 8 rows, whole sectors, and
@@ -1094,7 +1098,7 @@ __global__ void __launch_bounds__(PfRoles<DQK>::kThreads, 1)
                         *reinterpret_cast<uint4 *>(orow4 + static_cast<int64_t>(i) * p.Hqo * kPfDV + c * 32) =
                             make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
             }
-            if (valid) p.lse[grow * p.Hqo + h] = l > 0.f ? (m_used + fast_log2(l)) * kLn2 : -INFINITY;
+            if (valid) p.lse[grow * p.Hqo + h] = l > 0.f ? (m_used + fast_log2(l)) * kLn2 : no_sum - INFINITY;
             tc_fence_before();  // O read before the next item's first PV_X overwrites it
             t_base += n;
             tx_base += n;
@@ -1485,7 +1489,7 @@ static int prefill_impl(const void *q, int64_t total_q, const void *k_cache,
                              void *out, float *lse, int32_t *err_word, void *stream,
                              const int32_t *off_q, const int32_t *off_o, const int32_t *off_k,
                              const int32_t *off_v, PrefillFp8 *f8 = nullptr, int32_t window_left = -1,
-                             int32_t first_tokens = 0) {
+                             int32_t first_tokens = 0, bool nan_lse = false) {
     // no block table: contiguous K/V of max_num_pages rows, page strides are row strides
     const bool contiguous = block_tables == nullptr;
     if (contiguous) {
@@ -1657,6 +1661,7 @@ static int prefill_impl(const void *q, int64_t total_q, const void *k_cache,
     p.window_left = window_left;
     p.first_tokens = first_tokens;
     p.kv_factor = factor ? f8->widen.factor : nullptr;
+    p.nan_lse = nan_lse ? 1 : 0;
     const int n_qt = (max_token_per_sequence + kPfRows - 1) / kPfRows;
     const int64_t items = static_cast<int64_t>(n_qt) * num_kv_heads * pairs * batch_size;
     if (n_qt > 0) {
@@ -1886,7 +1891,7 @@ extern "C" int paged_prefill_window(const void *q, int64_t total_q, const void *
                             actual_seq_lens_kv, block_tables, block_table_stride, batch_size, causal, num_qo_heads,
                             num_kv_heads, d_qk, d_vo, page_size, layout, dtype, out, lse, err_word, stream,
                             batch_offsets_q, batch_offsets_o, batch_offsets_k, batch_offsets_v, nullptr, window_left,
-                            first_tokens);
+                            first_tokens, true);
     }
     // E4M3 caches with block scales: dequantised into the workspace, packed
     // request by request, and read from there as contiguous 16-bit K/V
@@ -1958,5 +1963,5 @@ extern "C" int paged_prefill_window(const void *q, int64_t total_q, const void *
                         max_token_per_sequence, max_sequence_kv, actual_seq_lens_q, actual_seq_lens_kv, nullptr, 0,
                         batch_size, causal, num_qo_heads, num_kv_heads, d_qk, d_vo, 1, PKV_NHD, out_dtype, out, lse,
                         err_word, stream, batch_offsets_q, batch_offsets_o, nullptr, nullptr, &f8, window_left,
-                        first_tokens);
+                        first_tokens, true);
 }
