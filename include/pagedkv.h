@@ -380,9 +380,11 @@ size_t paged_decode_window_workspace_size(int32_t batch_size, int32_t q_len_per_
  *  - workspace: >= paged_decode_window_workspace_size(...) bytes, 256-byte
  *    aligned; calls that may overlap on the GPU take one each.
  *  - A NaN or infinity in a key or value that no query of the request sees has
- *    no effect.  A NaN among the visible ones makes the rows that see it NaN
- *    (out and lse); one in the value of a key that only some of a request's
- *    queries see may reach its other queries.
+ *    no effect.  A NaN key, or a logit of plus infinity, makes the rows that
+ *    see it NaN, out and lse (paged_decode and paged_decode_ex do not promise
+ *    it).  A NaN in a value makes that column of their out NaN, an infinity
+ *    infinite or NaN, lse not; where only some of a request's queries see it,
+ *    it may reach that column of others.
  * Everything else, including errors, is as paged_decode_ex (cum_seq_lens_q
  * NULL: max_q_len tokens for every request).
  */

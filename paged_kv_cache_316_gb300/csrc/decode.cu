@@ -117,7 +117,7 @@ static int decode_impl(const void *query, const void *k_cache, const void *v_cac
     p.k_scales = p.v_scales = nullptr;
     p.scale_stride = 0;
     p.block_shift = p.pages_cap = p.scales_cap = 0;
-    if (scaled || (first_tokens > 0 && window_left >= 0)) {
+    if (ext) {  // (also without scales and window: a NaN key then has the same effect)
         // a split of `chunk` keys may start and end inside a page (block), in
         // both parts of its run
         p.pages_cap = ((pl.chunk >> p.page_shift) + 5) & ~1;  // (even: the scale list after it is 8-byte aligned)

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import _plain
+import test_gpu_decode_window as dw
 import test_gpu_prefill_window as pw
 from paged_kv_cache_316_gb300 import workloads as wl
 
@@ -66,3 +67,60 @@ def test_prefill_value(case):
     assert torch.isnan(o[:n, Hq // 2:, 7]).all()
     o[:n, Hq // 2:, 7] = 0
     assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+
+
+DECODE = [
+    # L, block (None: 16-bit cache), E4M3 without block scales, Hq, dtype, window, first, sinks
+    (100, None, False, 8, torch.bfloat16, 5000, 1, False),
+    (3000, None, False, 8, torch.float16, 5000, 1, True),       # several splits
+    (100, None, False, 8, torch.bfloat16, -1, 3, False),        # no window: the first tokens have no effect
+    (3000, None, False, 8, torch.float16, -1, 3, False),
+    (3000, None, True, 8, torch.bfloat16, -1, 3, True),
+    (100, 16, False, 8, torch.bfloat16, -1, 0, False),
+    (3000, 8, False, 32, torch.float16, -1, 0, True),
+    (3000, 16, False, 32, torch.bfloat16, 2500, 9, False),
+]
+D_IDS = [f"d{i}" for i in range(len(DECODE))]
+
+
+def decode_case(case):
+    L, G, e4m3, Hq, dtype, window, first, sinks = case
+    c = dw.make([L, L], 16, Hq, 2, wl.HND, dtype, 39, scaled=bool(G), G=G, e4m3=e4m3, sinks=sinks, window=window,
+                first=first, poison=False)
+    return c, (c["pool"].view(torch.uint8) if G or e4m3 else c["pool"]), Hq // 2
+
+
+D_BAD = [(i, bad) for i, c in enumerate(DECODE) for bad in (NAN, INF) if bad != INF or not (c[1] or c[2])]
+
+
+@pytest.mark.parametrize("every", [False, True])  # one key; or one in each 16, so that every split has some
+@pytest.mark.parametrize("case, bad", [(DECODE[i], bad) for i, bad in D_BAD], ids=[f"d{i}-{bad}" for i, bad in D_BAD])
+def test_decode_key(case, every, bad):
+    c, raw, half = decode_case(case)
+    c["query"][..., 7] = c["query"][..., 7].abs() + 0.125  # (an infinite logit has one sign)
+    pages = c["pt"].pages[0] if every else c["pt"].pages[0][-2:-1]
+    raw[pages, 0, 1, 1, 7] = 0x7F if raw.dtype == torch.uint8 else bad
+    out, lse = dw.call(c, 0.05)
+    assert torch.isnan(out[0, half:].float()).all() and torch.isnan(lse[0, half:]).all()
+    # the other head and request are those of a cache without it
+    raw[pages, 0, 1, 1, 7] = 0
+    want = dw.call(c, 0.05)
+    assert torch.equal(out[0, :half], want[0][0, :half]) and torch.equal(out[1], want[0][1])
+    assert torch.equal(lse[0, :half], want[1][0, :half]) and torch.equal(lse[1], want[1][1])
+    dw.compare(c, *want, 0.05)
+
+
+@pytest.mark.parametrize("case", DECODE, ids=D_IDS)
+def test_decode_value(case):
+    """A NaN in a value: that column of out, no other, and not lse; so an infinity, which may stay one."""
+    c, raw, half = decode_case(case)
+    bads = [0x7F] if raw.dtype == torch.uint8 else [NAN, INF]
+    page = c["pt"].pages[0][-2]
+    for bad in bads:
+        raw[page, 1, 1, 3, 7] = bad
+        out, lse = dw.call(c, 0.05)
+        o = out.cpu().float()
+        assert not torch.isfinite(o[0, half:, 7]).any()
+        assert bad is INF or torch.isnan(o[0, half:, 7]).all()
+        o[0, half:, 7] = 0
+        assert torch.isfinite(o).all() and torch.isfinite(lse).all()
