@@ -200,6 +200,8 @@ def split_cache(kv_cache, layout: int):
         shape, stride = base.shape, base.stride(0)
         if v.shape != shape or v.stride(0) != stride:
             raise PagedKVError("K and V caches must have the same shape and page stride")
+        if v.dtype != base.dtype or v.get_device() != base.get_device():
+            raise PagedKVError("K and V caches hold the same type on the same device")
         if not (_rows_contiguous(base) and _rows_contiguous(v)):
             raise PagedKVError("each page must be contiguous")
         kp, vp = base.data_ptr(), v.data_ptr()
@@ -500,9 +502,6 @@ def _decode_window(query, kv_cache, workspace, block_tables, seq_lens, max_seq_l
         raise PagedKVError("seq_lens must be a contiguous 1-D tensor of 32-bit lengths")
     B = seq_lens.shape[0]
     dtype = _decode_dtype(query, base)
-    if isinstance(kv_cache, (tuple, list)) and (kv_cache[1].dtype != base.dtype or
-                                                kv_cache[1].get_device() != base.get_device()):
-        raise PagedKVError("K and V caches hold the same type on the same device")
     ks = vs = cum = sink_ptr = lse_ptr = err_ptr = None
     ss = block = 0
     if kv_scales is not None:
