@@ -67,6 +67,8 @@ static int decode_impl(const void *query, const void *k_cache, const void *v_cac
     if (batch_size == 0) return PKV_OK;
     if (!query || !k_cache || !v_cache || !block_tables || !seq_lens || !out) return PKV_ERR_NULL;
     if (scaled && (!ext->k_scales || !ext->v_scales)) return PKV_ERR_NULL;
+    if (scaled && ((reinterpret_cast<uintptr_t>(ext->k_scales) | reinterpret_cast<uintptr_t>(ext->v_scales)) & 3))
+        return PKV_ERR_INVALID_ARG;
     if (!aligned16(query) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
         (page_stride % (kv8 ? 16 : 8)))  // 16-byte page starts
         return PKV_ERR_INVALID_ARG;
