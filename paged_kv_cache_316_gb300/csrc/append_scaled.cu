@@ -17,11 +17,13 @@
 // only what it copied, so no barrier is needed), so every new value is read
 // once.  Longer runs and other widths are read twice, the second time from L2.
 //
-// HBM bounds it: two bytes read and one written an element.  1024 requests, 66k
-// tokens of 32 heads: 283 us, 5.7 TB/s, 84% of the measured copy rate (one warp
-// an entry and head, two reads: 1064 us; run list once per CTA and runs in
-// registers: 380; staged one run ahead: 299; two ahead: 287).  One token for
-// each of 64 requests: 3.3 us, a launch and three dependent reads.
+// HBM bounds it: two bytes read and one written an element.  Times of the call
+// replayed from a graph (launched from the host a call takes 11 us at least):
+// 1024 requests, 66k tokens of 32 heads: 286 us, 5.7 TB/s, 84% of the measured
+// copy rate (one warp an entry and head, two reads: 1064 us; run list once per
+// CTA and runs in registers: 380; staged one run ahead: 299; two ahead: 287).
+// One token for each of 64 requests: 3.5 us, a launch and three dependent reads.
+// Measured with blocks of 8 and 16 and 128 elements a row only.
 #include <type_traits>
 
 #include "pkv_common.cuh"
@@ -43,7 +45,7 @@ struct AppendScaledParams {
 // CTAs of 8 warps, 16 entries each.  Blocks of more than 8 tokens: two CTAs
 // per SM (what three stages of 4 KB a warp leave room for; with fewer
 // registers three measured slower, 328 against 299 us).  Blocks of 8: half the
-// stage, four CTAs per SM (16 prompts: 23.1 us, 24.7 with three, 26.7 with two).
+// stage, four CTAs per SM (16 prompts: 23.5 us, 24.7 with three, 26.7 with two).
 // 8 or 32 entries a CTA: 306 / 293 against 286 us.
 constexpr int kAsWarps = 8;
 constexpr int kAsEntries = 16;

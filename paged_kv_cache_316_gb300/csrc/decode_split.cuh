@@ -15,13 +15,21 @@
 // 16 * MT rows of one mma.sync m16n8k16 A operand, so each K/V row read
 // from HBM feeds every query row that needs it.
 //
+// Roundings: a weight is rounded to the MMA's 16-bit type for its product with
+// V (bf16 or fp16 as the cache, fp16 over an E4M3 cache: register MMAs take
+// 16-bit operands at twice TF32's rate, and V has no more bits), the output
+// once at the end; scores, maxima, sums, O, the splits' partials and the LSE
+// are fp32.  Against 64 bits the output is off by 1.3 times what its own
+// rounding gives where the weights have its type, by no more than its own
+// rounding with weights in fp16 and a bf16 output.
+//
 // The kernel takes two extensions (EXT; their own translation unit,
 // decode_window.cu): a window that keeps the first tokens visible, and an
 // E4M3 cache with a scale for each block of keys and head.  Every visible key
 // is read once, so HBM bounds them: 128 requests, one token, a window of 4096
 // keys and 128 first tokens over a 16-bit cache: 315 us, 97% of the measured
 // copy rate.  Over an E4M3 cache, with half the bytes, the work around a key
-// counts: 64 requests of up to 8192 keys, 4 rows: 97.7 us, 86%; 96 requests
+// counts: 64 requests of up to 8192 keys, 4 rows: 98 us, 85%; 96 requests
 // of 4 tokens, 32 rows: 227 us, 47%, bound by the issue of register MMAs (64
 // a warp and tile, 8 cycles each) and the softmax between them with two warps
 // to a scheduler.  Tried and slower: the work of all requests laid end to end
@@ -29,7 +37,8 @@
 // next tile ahead of the softmax (249 us: a warp issues in order), QK and PV on
 // tcgen05 from fp16 tiles widened in shared memory (343 us: 4,000 cycles a
 // tile of fences, barriers and waits, at most two CTAs per SM by tensor
-// memory), splits of half and a quarter of the length (no change).
+// memory), splits of half and a quarter of the length (no change).  Times of
+// the call replayed from a graph.
 #pragma once
 
 #include <math.h>
@@ -625,7 +634,8 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8, SW>::CTAS) decode
     // its weight on the stored V row is e^z_j vs(j).  The running maximum is
     // kept over z_j + log vs(j), so that P_j = e^(z_j + log vs(j) - m), the
     // weight that goes into the fp16 MMA, is at most 2^8 whatever the scales
-    // are; the denominator sums P_j / vs(j) in fp32, and m + log of that sum
+    // are (a key whose weight times V scale is below 2^-25 of the row's largest
+    // adds nothing to the output: fp16's smallest number); the denominator sums P_j / vs(j) in fp32, and m + log of that sum
     // is the log-sum-exp of the z_j.  Eight consecutive keys share a scale
     // (blocks are at least 8 keys), so a score costs one FFMA as without
     // scales and a sum term one FFMA in place of an add.

@@ -33,6 +33,10 @@
 //           tiles, V tiles arrive as E4M3 in a byte ring and this warp widens
 //           each one exactly to fp16 in the 16-bit V stage layout, so that
 //           PV stays a 16-bit MMA with P in fp16.
+// Roundings: a weight is rounded to P's 16-bit type, the one that V has beside
+// it in the MMA, and the output once at the end; scores, maxima, sums, O and the
+// LSE are fp32.  Against 64 bits the output is off by 1.3 to 1.4 times what its
+// own rounding gives.
 // The softmax warps run with 200 registers and the others with 104
 // (setmaxnreg).  Every wait is bounded; a wait that gives up sets
 // PKV_DEV_ERR_TIMEOUT, the other roles stop, the copies in flight are
@@ -46,16 +50,16 @@
 //
 // A sliding window that keeps the first tokens visible (WIN) leaves out the
 // key tiles that no row of a query tile sees, so an item's work follows the
-// window and not the sequence: 2048 queries at the end of 32768 keys, window
-// 4096, 32 heads: 117.6 us, 1.18 PFLOP/s over the visible pairs, 60% of the
-// measured bf16 rate (256 items on 152 SMs fill two rounds to 84%).  8 ragged
-// prompts, d_qk 192, window 778 and 33 first tokens: 158.5 us, 45%: an item is 11
-// tiles of 96 keys for 8.5 tiles' worth of visible pairs, and its first S comes
-// 4,600 cycles after the last P of the item before, 1,500 within an item: Q (96
-// KB) lands last.  (Q per block, from either producer or a warp of its own, Q
-// ahead of the first K tile, the next item taken a tile early: no gain.)  The
-// masks are words of one bit
-// a column (per-column compares: 138 and 206 us where the words gave 129.5 and 179).
+// window and not the sequence (times of the call replayed from a graph): 2048
+// queries at the end of 32768 keys, window 4096, 32 heads: 118 us, 1.16 PFLOP/s
+// over the visible pairs, 60% of the measured bf16 rate (256 items on 152 SMs
+// fill two rounds to 84%).  8 ragged prompts, d_qk 192, window 778 and 33 first
+// tokens: 159.5 us, 45%: an item is 11 tiles of 96 keys for 8.5 tiles' worth of
+// visible pairs, and its first S comes 4,600 cycles after the last P of the item
+// before, 1,500 within an item: Q (96 KB) lands last.  (Q per block, from either
+// producer or a warp of its own, Q ahead of the first K tile, the next item taken
+// a tile early: no gain.)  The masks are words of one bit a column (per-column
+// compares: 138 and 206 us where the words gave 129.5 and 179).
 #include <math.h>
 
 #include <type_traits>
@@ -1192,7 +1196,8 @@ struct WidenKvParams {
 // output take the inverse in fp32, all exact.  fp16's smallest step is then
 // 2^(e - 31): products under scales down to 2^(e - 22) lose nothing, under
 // smaller ones at most 2^(e - 32).  The scan runs beside the plan's one warp:
-// no launch more.
+// no launch more; with it and the factors' reads eight ragged prompts take 203
+// us where they took 199 (replayed from a graph).
 constexpr int kFactorThreads = 256;
 __global__ void __launch_bounds__(kFactorThreads)
     prefill_plan_factor_kernel(const int32_t *__restrict__ lq, const int32_t *__restrict__ lkv, int B, int U, int max_q,
@@ -1240,8 +1245,9 @@ __global__ void __launch_bounds__(kFactorThreads)
 }
 constexpr int kWidenTok = 32;  // keys per CTA of the cache widening
 // with scales: each key's rows are three dependent reads away (page, row,
-// scale), so shorter CTAs keep more of them in flight (two requests of 512
-// queries over 11k keys: 99.7 us in all, 100.4 with 16, 101.9 with 32, 106 with 64)
+// scale), so shorter CTAs keep more of them in flight (the pass by itself, two
+// requests with 11k keys, bf16: 13.8 us, 14.6 with 16, 15.3 with 32; eight ragged
+// prompts in blocks of 32, fp16: 20.8, 20.2, 21.5)
 constexpr int kDequantTok = 8;
 
 // CTA (key block, request, K or V): every 16-byte source chunk of its keys
