@@ -640,6 +640,141 @@ int paged_prefill_window(const void *q, int64_t total_q, const void *k_cache,
                          const int32_t *batch_offsets_o, const int32_t *batch_offsets_k,
                          const int32_t *batch_offsets_v, int32_t *err_word, void *stream);
 
+/*
+ * paged_rotary -- RMS norm of every head of queries and keys (where weights
+ * are given), then a rotation by the token's position, onto rows: what a
+ * cache or an attention call takes that is not reached by
+ * paged_append_rotary (paged_append_scaled, contiguous prefill).  For a head
+ * row x of head_dim elements at position p:
+ *   y = x / sqrt(mean(x^2) + eps) * weight          (weight NULL: y = x)
+ *   of the rotated dimensions [rotary_start, rotary_start + rotary_dim), pair
+ *   i is (y[2i], y[2i + 1]) with interleaved, else (y[i], y[i + rotary_dim / 2]);
+ *   (u, v) -> magnitude * (u cos a - v sin a, v cos a + u sin a),
+ *   a = p * frequencies[i];   the other dimensions stay y.
+ * fp32 throughout, one rounding at the end (nearest even).  Angles lose
+ * nothing to the position's size: they are counted in 2^-64 of a turn.
+ *   query / key: nnz rows of [num_qo_heads][head_dim] / [num_kv_heads]
+ *   [head_dim], *_stride elements from token to token (slices of a fused
+ *   projection); query_out / key_out: contiguous rows.  An output may be its
+ *   own contiguous input.  positions: [nnz] int32 (any value); frequencies:
+ *   [rotary_dim / 2] float64, radians a step (the scaling of long contexts is
+ *   in them and in magnitude); weights: [head_dim] in the rows' type.
+ * Host errors: head_dim or rotary_dim not a multiple of 16, rotary_start not
+ * of 8, a range past the head, a stride below a row or not a multiple of 8, a
+ * base not 16-byte aligned, eps < 0 or NaN -> PKV_ERR_INVALID_ARG; head_dim
+ * above 256 -> PKV_ERR_UNSUPPORTED.  dtype: PKV_F16 / PKV_BF16.
+ */
+int paged_rotary(const void *query, const void *key, int64_t query_stride,
+                 int64_t key_stride, int64_t nnz, const int32_t *positions,
+                 const double *frequencies, int32_t rotary_dim,
+                 int32_t rotary_start, int32_t interleaved, float magnitude,
+                 const void *query_weight, const void *key_weight, float eps,
+                 int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
+                 int32_t dtype, void *query_out, void *key_out, void *stream);
+
+/*
+ * paged_append_rotary -- paged_rotary and paged_append in one pass: queries
+ * are normalised and rotated onto query_out, keys normalised, rotated and
+ * written to their pages, values written to theirs.  Cache and entry
+ * arguments, errors of entries and what stays untouched are paged_append's;
+ * the rest is paged_rotary's.  rotary_positions ([nnz] int32, may be NULL:
+ * `positions`) gives other positions to the rotation than to the pages.  The
+ * query row of an entry that is skipped is written all the same.
+ * page_size: a power of two up to 65536; head_dim a multiple of 16 up to 256.
+ */
+int paged_append_rotary(const void *query, const void *key, const void *value,
+                        int64_t query_stride, int64_t key_stride,
+                        int64_t value_stride, int64_t nnz,
+                        const int32_t *batch_indices, const int32_t *positions,
+                        const int32_t *rotary_positions, void *k_cache,
+                        void *v_cache, int64_t page_stride,
+                        int64_t max_num_pages, const int32_t *kv_indices,
+                        const int32_t *kv_indptr,
+                        const int32_t *kv_last_page_len, int32_t batch_size,
+                        const double *frequencies, int32_t rotary_dim,
+                        int32_t rotary_start, int32_t interleaved,
+                        float magnitude, const void *query_weight,
+                        const void *key_weight, float eps, int32_t num_qo_heads,
+                        int32_t num_kv_heads, int32_t head_dim,
+                        int32_t page_size, int32_t layout, int32_t dtype,
+                        void *query_out, int32_t *err_word, void *stream);
+
+/*
+ * paged_decode_shared_workspace_size -- bytes of device workspace
+ * paged_decode_shared needs (partial outputs of the prefixes' slices and of
+ * the own keys' splits); 0 for sizes it refuses.
+ */
+size_t paged_decode_shared_workspace_size(int32_t batch_size,
+                                          int32_t q_len_per_req,
+                                          int32_t num_qo_heads,
+                                          int32_t num_kv_heads, int32_t head_dim,
+                                          int32_t num_groups,
+                                          int32_t max_prefix_len,
+                                          int32_t max_seq_len, int32_t page_size);
+
+/*
+ * paged_decode_shared -- paged_decode for a batch whose requests share
+ * prefixes, each prefix read once for all of its requests.  The requests
+ * group_indptr[g] .. group_indptr[g + 1] - 1 form group g; a query sees the
+ * prefix_lens[g] keys in the pages of prefix_tables[g], all of them, and then
+ * its request's own keys, of which seq_lens[b] counts the q_len_per_req newest
+ * tokens too and token t sees keys j <= seq_lens[b] - q_len_per_req + t.
+ * Requests from group_indptr[num_groups] on have no prefix.  With
+ * z_j = bmm1_scale <q, k_j> over both sets of keys,
+ *   out = bmm2_scale * sum e^z_j v_j / (sum e^z_j + e^sink),
+ *   lse = log(sum e^z_j + e^sink)                 (nothing visible: 0, -inf).
+ *   group_indptr: [num_groups + 1] int32, from 0 in ascending order (groups
+ *   may be empty); prefix_lens: [num_groups] int32; prefix_tables:
+ *   [num_groups][prefix_table_stride] int32; entries past a prefix's pages
+ *   are not read.  Own keys begin on a page of their own.  The other arguments
+ *   are paged_decode's (bmm*_scale_dev: paged_decode_ex's); query and out have
+ *   batch_size * q_len_per_req rows, 16 bits, over 16-bit caches.
+ *   workspace: >= paged_decode_shared_workspace_size(...) bytes, 256-byte
+ *   aligned, always needed; calls that overlap on the GPU need one each.
+ * Host errors as paged_decode's (head_dim 128, page_size a power of two from
+ * 8 to 256, at most 64 rows num_qo_heads / num_kv_heads * q_len_per_req).
+ * Device errors: bad page id -> PKV_DEV_ERR_PAGE (its keys count as zeros in a
+ * prefix, as none among the own keys); group_indptr out of order or beyond the
+ * batch -> PKV_DEV_ERR_BATCH and no request has a prefix; a length above its
+ * maximum or a negative prefix length -> PKV_DEV_ERR_LEN, clamped;
+ * seq_lens[b] < q_len_per_req -> PKV_DEV_ERR_QLEN (tokens before the own keys
+ * see the prefix alone); PKV_DEV_ERR_TIMEOUT as paged_prefill's.
+ */
+int paged_decode_shared(const void *query, const void *k_cache,
+                        const void *v_cache, int64_t page_stride,
+                        int64_t max_num_pages, void *workspace,
+                        size_t workspace_bytes, const int32_t *prefix_tables,
+                        int32_t prefix_table_stride, const int32_t *prefix_lens,
+                        const int32_t *group_indptr, int32_t num_groups,
+                        int32_t max_prefix_len, const int32_t *block_tables,
+                        int32_t block_table_stride, const uint32_t *seq_lens,
+                        int32_t batch_size, int32_t max_seq_len,
+                        float bmm1_scale, float bmm2_scale,
+                        const float *bmm1_scale_dev, const float *bmm2_scale_dev,
+                        const float *sinks, int32_t q_len_per_req,
+                        int32_t num_qo_heads, int32_t num_kv_heads,
+                        int32_t head_dim, int32_t page_size, int32_t layout,
+                        int32_t dtype, void *out, float *lse, int32_t *err_word,
+                        void *stream);
+
+/*
+ * paged_merge_states -- attention over separate parts of the keys, merged:
+ * outs[i] / lses[i] (host arrays of num_states device pointers) are the output
+ * rows [rows][head_dim] and log-sum-exps [rows] of part i, `rows` counting
+ * (token, head) pairs:
+ *   lse = log sum_i e^lses[i],  out = sum_i e^(lses[i] - lse) outs[i].
+ * A part whose lse is -inf counts for nothing, whatever its output holds; all
+ * of them: 0 and -inf.  out / lse may be those of one of the parts.  A sink
+ * belongs to one part only.
+ * Host errors: num_states < 1, head_dim not a multiple of 8 ->
+ * PKV_ERR_INVALID_ARG; more than PKV_MERGE_MAX_STATES parts or head_dim above
+ * 256 -> PKV_ERR_UNSUPPORTED.  dtype: PKV_F16 / PKV_BF16.
+ */
+#define PKV_MERGE_MAX_STATES 16
+int paged_merge_states(const void *const *outs, const float *const *lses,
+                       int32_t num_states, int64_t rows, int32_t head_dim,
+                       int32_t dtype, void *out, float *lse, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

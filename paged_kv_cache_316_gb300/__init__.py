@@ -13,9 +13,15 @@ from .binding import (  # noqa: F401
     paged_batch_indices_positions,
     paged_append,
     paged_append_scaled,
+    rotary_frequencies,
+    paged_rotary,
+    paged_append_rotary,
     paged_decode_workspace_size,
     paged_decode,
     paged_decode_noalloc,
+    paged_decode_shared_workspace_size,
+    paged_decode_shared,
+    paged_merge_states,
     paged_prefill_workspace_size,
     paged_prefill_fp8_workspace_size,
     paged_prefill_scaled_workspace_size,

@@ -9,6 +9,7 @@ library has not been built, every call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -68,6 +69,16 @@ _SIGNATURES = {
     "paged_prefill_window": ([_c_p, _i64, _c_p, _c_p, _i64, _i64, _i64, _c_p, _c_p, _i64, _i32, _f32, _c_p, _sz,
                               _i32, _i32, _c_p, _c_p, _c_p, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
                               _i32, _i32, _i32, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p], ctypes.c_int),
+    "paged_rotary": ([_c_p, _c_p, _i64, _i64, _i64, _c_p, _c_p, _i32, _i32, _i32, _f32, _c_p, _c_p, _f32, _i32, _i32,
+                      _i32, _i32, _c_p, _c_p, _c_p], ctypes.c_int),
+    "paged_append_rotary": ([_c_p, _c_p, _c_p, _i64, _i64, _i64, _i64, _c_p, _c_p, _c_p, _c_p, _c_p, _i64, _i64, _c_p,
+                             _c_p, _c_p, _i32, _c_p, _i32, _i32, _i32, _f32, _c_p, _c_p, _f32, _i32, _i32, _i32, _i32,
+                             _i32, _i32, _c_p, _c_p, _c_p], ctypes.c_int),
+    "paged_decode_shared_workspace_size": ([_i32] * 9, _sz),
+    "paged_decode_shared": ([_c_p, _c_p, _c_p, _i64, _i64, _c_p, _sz, _c_p, _i32, _c_p, _c_p, _i32, _i32, _c_p, _i32,
+                             _c_p, _i32, _i32, _f32, _f32, _c_p, _c_p, _c_p, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                             _c_p, _c_p, _c_p, _c_p], ctypes.c_int),
+    "paged_merge_states": ([_c_p, _c_p, _i32, _i64, _i32, _i32, _c_p, _c_p, _c_p], ctypes.c_int),
     "paged_prefill_fp8_workspace_size": ([_i32] * 5 + [_i64] + [_i32] * 4, _sz),
     "paged_prefill_fp8": ([_c_p, _i64, _c_p, _c_p, _i64, _i64, _i64, _f32, _c_p, _c_p, _c_p, _c_p,
                            _sz, _i32, _i32, _c_p, _c_p, _c_p, _i32, _i32, _i32, _i32, _i32, _i32,
@@ -373,6 +384,149 @@ def paged_append_scaled(append_key, append_value, batch_indices, positions, page
         _check(status)
 
 
+# ---- rotation ---------------------------------------------------------------------------
+
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling=None, factor: float = 1.0,
+                       trained_len: int | None = None, fast: float = 32.0, slow: float = 1.0, device="cuda"):
+    """(frequencies, magnitude) for paged_rotary / paged_append_rotary: the
+    angle a pair turns by at each position, float64 [rotary_dim // 2], and
+    what the rotated dimensions are multiplied by.  f_i = base^(-2 i /
+    rotary_dim), then for contexts `factor` times the trained length:
+      None      as they are;
+      "linear"  f_i / factor (positions interpolated);
+      "ntk"     base * factor^(rotary_dim / (rotary_dim - 2)) in place of base;
+      "yarn"    f_i of pairs that turn more than `fast` times over
+                trained_len kept, of those below `slow` turns divided by
+                factor, a linear ramp in the number of turns between them;
+                magnitude 0.1 ln(factor) + 1."""
+    if rotary_dim <= 0 or rotary_dim % 2 or not base > 0 or not factor >= 1:
+        raise PagedKVError("rotary_dim must be positive and even, base positive and factor at least 1")
+    n = rotary_dim // 2
+    magnitude = 1.0
+    if scaling == "ntk":
+        if n == 1:
+            raise PagedKVError("ntk scaling needs two pairs or more")
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    f = base ** (-torch.arange(n, dtype=torch.float64) / n)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        if trained_len is None or trained_len <= 0 or not fast > slow:
+            raise PagedKVError("yarn scaling needs trained_len, and fast above slow")
+        keep = ((trained_len * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+        f = f * (keep + (1 - keep) / factor)
+        magnitude = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "ntk"):
+        raise PagedKVError(f"unknown scaling {scaling!r}")
+    return f.to(device), magnitude
+
+
+def _token_rows(t, name: str):
+    """(heads, head_dim, elements from token to token) of [tokens, heads,
+    head_dim] whose heads are contiguous."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or (shape[2] > 1 and stride[2] != 1) or (shape[1] > 1 and stride[1] != shape[2]):
+        raise PagedKVError(f"{name} must be [tokens, heads, head_dim] with contiguous heads")
+    return shape[1], shape[2], stride[0] if shape[0] > 1 else max(stride[0], shape[1] * shape[2])
+
+
+def _rotary_args(query, key, positions, frequencies, query_weight, key_weight, query_out):
+    """The checks that paged_rotary and paged_append_rotary share: (tokens, q
+    heads, kv heads, head_dim, strides, rotary_dim, query_out, dtype)."""
+    Hq, D, qs = _token_rows(query, "query")
+    Hkv, Dk, ks = _token_rows(key, "key")
+    n = query.shape[0]
+    if key.shape[0] != n or Dk != D:
+        raise PagedKVError("query and key have the same tokens and head_dim")
+    dtype = _dtype_code(query)
+    if dtype > BF16 or key.dtype != query.dtype:
+        raise PagedKVError("query and key are both fp16 or both bf16")
+    if positions.dtype != torch.int32 or positions.numel() < n or not positions.is_contiguous():
+        raise PagedKVError(f"positions must be contiguous int32 with >= {n} entries")
+    if frequencies.dtype != torch.float64 or frequencies.dim() != 1 or not frequencies.is_contiguous():
+        raise PagedKVError("frequencies must be contiguous float64 [rotary_dim // 2]")
+    for w in (query_weight, key_weight):
+        if w is not None and (w.dtype != query.dtype or w.numel() != D or not w.is_contiguous()):
+            raise PagedKVError(f"norm weights must be contiguous [{D}] of the query's type")
+    if query_out is None:
+        query_out = torch.empty((n, Hq, D), dtype=query.dtype, device=query.device)
+    elif query_out.shape != query.shape or query_out.dtype != query.dtype or not query_out.is_contiguous():
+        raise PagedKVError("query_out must be a contiguous tensor of the query's shape and dtype")
+    return n, Hq, Hkv, D, qs, ks, 2 * frequencies.numel(), query_out, dtype
+
+
+def paged_rotary(query, key, positions, frequencies, rotary_start: int = 0, interleaved: bool = False,
+                 magnitude: float = 1.0, query_weight=None, key_weight=None, eps: float = 1e-6, query_out=None,
+                 key_out=None, stream=None):
+    """RMS norm of each head of query [tokens, heads, head_dim] and key
+    (where query_weight / key_weight [head_dim] are given), then the rotation
+    of the dimensions rotary_start .. rotary_start + 2 * len(frequencies) by
+    the tokens' positions (int32): pairs of neighbours with interleaved, else
+    of an element and the one half the rotated part further.  frequencies
+    (float64 radians a position) and magnitude: see rotary_frequencies.
+    Tokens may be slices of a fused projection's rows; an output may be its
+    own contiguous input.  Returns (query_out, key_out)."""
+    n, Hq, Hkv, D, qs, ks, rd, query_out, dtype = _rotary_args(query, key, positions, frequencies, query_weight,
+                                                               key_weight, query_out)
+    if key_out is None:
+        key_out = torch.empty((n, Hkv, D), dtype=key.dtype, device=key.device)
+    elif key_out.shape != key.shape or key_out.dtype != key.dtype or not key_out.is_contiguous():
+        raise PagedKVError("key_out must be a contiguous tensor of the key's shape and dtype")
+    device = _same_device(query, key, positions, frequencies, query_weight, key_weight, query_out, key_out)
+    status = load_library().paged_rotary(
+        _addr(query), _addr(key), qs, ks, n, _addr(positions), _addr(frequencies), rd, rotary_start,
+        1 if interleaved else 0, magnitude, None if query_weight is None else _addr(query_weight),
+        None if key_weight is None else _addr(key_weight), eps, Hq, Hkv, D, dtype, _addr(query_out), _addr(key_out),
+        _stream_on(stream, device))
+    if status:
+        _check(status)
+    return query_out, key_out
+
+
+def paged_append_rotary(query, key, value, batch_indices, positions, paged_kv_cache, kv_indices, kv_indptr,
+                        kv_last_page_len, frequencies, kv_layout="NHD", rotary_start: int = 0,
+                        interleaved: bool = False, magnitude: float = 1.0, query_weight=None, key_weight=None,
+                        eps: float = 1e-6, rotary_positions=None, query_out=None, err_word=None, stream=None):
+    """paged_rotary of query and key and paged_append of the rotated keys and
+    of value, in one pass over them: the queries go to query_out, which is
+    returned, keys and values to their pages.  rotary_positions (int32): other
+    positions for the rotation than `positions`, which place the tokens in
+    their requests."""
+    layout = _layout_code(kv_layout)
+    kp, vp, stride, P, H, S, D, base = split_cache(paged_kv_cache, layout)
+    n, Hq, Hkv, Dq, qs, ks, rd, query_out, dtype = _rotary_args(query, key, positions, frequencies, query_weight,
+                                                                key_weight, query_out)
+    Hv, Dv, vs = _token_rows(value, "value")
+    if Hkv != H or Dq != D or Hv != H or Dv != D or value.shape[0] != n:
+        raise PagedKVError(f"key/value must both be [{n}, {H}, {D}], query heads {D} wide")
+    if base.dtype != query.dtype or value.dtype != query.dtype:
+        raise PagedKVError("query, key, value and the cache hold the same 16-bit type")
+    if batch_indices.dtype != torch.int32 or batch_indices.numel() < n or not batch_indices.is_contiguous():
+        raise PagedKVError(f"batch_indices must be contiguous int32 with >= {n} entries")
+    rp = None
+    if rotary_positions is not None:
+        if rotary_positions.dtype != torch.int32 or rotary_positions.numel() < n or not rotary_positions.is_contiguous():
+            raise PagedKVError(f"rotary_positions must be contiguous int32 with >= {n} entries")
+        rp = _addr(rotary_positions)
+    B = kv_last_page_len.shape[0]
+    for t in (kv_indices, kv_indptr, kv_last_page_len):
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise PagedKVError("kv_indices/kv_indptr/kv_last_page_len must be contiguous int32")
+    if kv_indptr.numel() != B + 1:
+        raise PagedKVError(f"kv_indptr must have {B + 1} entries")
+    device = _same_device(query, key, value, base, batch_indices, positions, rotary_positions, kv_indices, kv_indptr,
+                          kv_last_page_len, frequencies, query_weight, key_weight, query_out, err_word)
+    status = load_library().paged_append_rotary(
+        _addr(query), _addr(key), _addr(value), qs, ks, vs, n, _addr(batch_indices), _addr(positions), rp, kp, vp,
+        stride, P, _addr(kv_indices), _addr(kv_indptr), _addr(kv_last_page_len), B, _addr(frequencies), rd,
+        rotary_start, 1 if interleaved else 0, magnitude, None if query_weight is None else _addr(query_weight),
+        None if key_weight is None else _addr(key_weight), eps, Hq, H, D, S, layout, dtype, _addr(query_out),
+        None if err_word is None else _addr(err_word), _stream_on(stream, device))
+    if status:
+        _check(status)
+    return query_out
+
+
 # ---- decode -------------------------------------------------------------------------------
 
 def _scale_arg(scale, device):
@@ -581,6 +735,112 @@ def paged_decode_noalloc(query, kv_cache, block_tables, seq_lens, max_seq_len: i
         q_len_per_req, Hqo, Hkv, D, S, layout, _decode_dtype(query, base), _ptr(out), _ptr(lse),
         _ptr(err_word), _stream(stream)))
     return out
+
+
+# ---- decode over shared prefixes, merged states --------------------------------------------
+
+def paged_decode_shared_workspace_size(batch_size, q_len_per_req, num_qo_heads, num_kv_heads, head_dim, num_groups,
+                                       max_prefix_len, max_seq_len, page_size) -> int:
+    return int(load_library().paged_decode_shared_workspace_size(
+        batch_size, q_len_per_req, num_qo_heads, num_kv_heads, head_dim, num_groups, max_prefix_len, max_seq_len,
+        page_size))
+
+
+def paged_decode_shared(query, kv_cache, workspace, prefix_tables, prefix_lens, group_indptr, max_prefix_len: int,
+                        block_tables, seq_lens, max_seq_len: int, bmm1_scale: float = 1.0, bmm2_scale: float = 1.0,
+                        sinks=None, kv_layout="HND", q_len_per_req: int = 1, out=None, lse=None, err_word=None,
+                        stream=None):
+    """paged_decode for requests that share prefixes: the requests
+    group_indptr[g] .. group_indptr[g + 1] - 1 (int32 [groups + 1], from 0,
+    ascending) see the prefix_lens[g] (int32) keys of prefix_tables[g] (int32
+    [groups, pages]) before their own, each prefix read once for all of them;
+    requests behind the last group see their own alone.  block_tables /
+    seq_lens / max_seq_len are of the requests' own keys, which begin on a page
+    of their own and end with the q_len_per_req newest tokens.  query and out
+    [batch_size * q_len_per_req, heads, 128] and the cache are fp16 or bf16;
+    scales may be one-element float32 device tensors."""
+    layout = _layout_code(kv_layout)
+    kp, vp, stride, P, Hkv, S, D, base = split_cache(kv_cache, layout)
+    shape = query.shape
+    rows, Hqo, Dq = shape
+    dtype = _dtype_code(query)
+    if Dq != D or not query.is_contiguous():
+        raise PagedKVError(f"query must be contiguous [rows, num_qo_heads, {D}]")
+    if dtype > BF16 or base.dtype != query.dtype:
+        raise PagedKVError("query and cache are both fp16 or both bf16")
+    if seq_lens.dim() != 1 or seq_lens.element_size() != 4 or not seq_lens.is_contiguous():
+        raise PagedKVError("seq_lens must be a contiguous 1-D tensor of 32-bit lengths")
+    B = seq_lens.shape[0]
+    if rows < B * q_len_per_req:
+        raise PagedKVError(f"query has {rows} rows; the requests need {B * q_len_per_req}")
+    G = prefix_lens.shape[0]
+    for t, n in ((prefix_lens, G), (group_indptr, G + 1)):
+        if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+            raise PagedKVError("prefix_lens [groups] and group_indptr [groups + 1] must be contiguous int32")
+    for t, n, longest in ((prefix_tables, G, max_prefix_len), (block_tables, B, max_seq_len)):
+        if t.dim() != 2 or t.dtype != torch.int32 or t.shape[0] < n or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise PagedKVError("page tables must be int32 [rows, pages] with unit column stride")
+        if n and t.shape[1] * S < longest:
+            raise PagedKVError("a page table has fewer columns than its longest sequence needs")
+    if out is None:
+        out = torch.empty_like(query)
+    elif out.shape != shape or out.dtype != query.dtype or not out.is_contiguous():
+        raise PagedKVError("out must be a contiguous tensor of the query's shape and dtype")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != shape[:2] or not lse.is_contiguous()):
+        raise PagedKVError(f"lse must be a contiguous float32 [{rows}, {Hqo}] tensor")
+    if sinks is not None and (sinks.dtype != torch.float32 or sinks.numel() != Hqo or not sinks.is_contiguous()):
+        raise PagedKVError(f"sinks must be contiguous float32 [{Hqo}]")
+    s1, s2, s1_dev, s2_dev = bmm1_scale, bmm2_scale, None, None
+    if type(s1) is not float:
+        s1, s1_dev = _scale_arg(s1, query.device)
+    if type(s2) is not float:
+        s2, s2_dev = _scale_arg(s2, query.device)
+    device = _same_device(query, base, workspace, prefix_tables, prefix_lens, group_indptr, block_tables, seq_lens,
+                          sinks, out, lse, err_word)
+    status = load_library().paged_decode_shared(
+        _addr(query), kp, vp, stride, P, _addr(workspace), workspace.nbytes, _addr(prefix_tables),
+        prefix_tables.stride(0), _addr(prefix_lens), _addr(group_indptr), G, max_prefix_len, _addr(block_tables),
+        block_tables.stride(0), _addr(seq_lens), B, max_seq_len, s1, s2, s1_dev, s2_dev,
+        None if sinks is None else _addr(sinks), q_len_per_req, Hqo, Hkv, D, S, layout, dtype, _addr(out),
+        None if lse is None else _addr(lse), None if err_word is None else _addr(err_word), _stream_on(stream, device))
+    if status:
+        _check(status)
+    return out
+
+
+def paged_merge_states(states, out=None, lse=None, stream=None):
+    """Attention over separate parts of the keys, merged: states is a sequence
+    of up to 16 (out [rows, heads, head_dim], lse float32 [rows, heads]) pairs
+    as paged_decode and paged_prefill give them, over parts that share no key.
+    out / lse may be those of one of the parts.  Returns (out, lse)."""
+    states = list(states)
+    if not states:
+        raise PagedKVError("no states to merge")
+    first = states[0][0]
+    shape = first.shape
+    dtype = _dtype_code(first)
+    if first.dim() != 3 or dtype > BF16:
+        raise PagedKVError("a state's output is [rows, heads, head_dim] in fp16 or bf16")
+    if out is None:
+        out = torch.empty(shape, dtype=first.dtype, device=first.device)
+    if lse is None:
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=first.device)
+    tensors = []
+    for o, l in states + [(out, lse)]:
+        if o.shape != shape or o.dtype != first.dtype or not o.is_contiguous():
+            raise PagedKVError("outputs must be contiguous tensors of the same shape and type")
+        if l.shape != shape[:2] or l.dtype != torch.float32 or not l.is_contiguous():
+            raise PagedKVError(f"log-sum-exps must be contiguous float32 {list(shape[:2])}")
+        tensors += (o, l)
+    device = _same_device(*tensors)
+    n = len(states)
+    pointers = (_c_p * (2 * n))(*[_addr(o) for o, _ in states], *[_addr(l) for _, l in states])
+    at = ctypes.addressof(pointers)
+    status = load_library().paged_merge_states(at, at + n * ctypes.sizeof(_c_p), n, shape[0] * shape[1], shape[2],
+                                               dtype, _addr(out), _addr(lse), _stream_on(stream, device))
+    if status:
+        _check(status)
+    return out, lse
 
 
 # ---- prefill ---------------------------------------------------------------------------------

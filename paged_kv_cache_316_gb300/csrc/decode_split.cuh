@@ -191,10 +191,13 @@ __device__ __forceinline__ void store4(T *dst, float a, float b, float c, float 
 // SW > 0 (an E4M3 cache and at most 8 SW query rows): the MMAs take the keys
 // as their 16-row side, S^T = K Q^T and O^T = V^T P^T (see the tile loop).
 // EXT: 0 all keys or a window; 1 a window and first tokens; 2 the same over
-// an E4M3 cache with a scale for each block of keys and head.
+// an E4M3 cache with a scale for each block of keys and head; 3 the requests'
+// own keys behind a shared prefix (decode_shared.cu): every row goes to the
+// partials, and the grid runs beside the one before it, whose end it awaits
+// before its own.
 template <typename T, int MT, int LAYOUT, bool KV8, int SW = 0, int EXT = 0>
 __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8, SW>::CTAS) decode_split_kernel(const DecodeParams p) {
-    constexpr bool FIRST = EXT >= 1, SCL = EXT == 2;
+    constexpr bool FIRST = EXT == 1 || EXT == 2, SCL = EXT == 2, SHARED = EXT == 3;
     static_assert(!SCL || KV8, "block scales: E4M3 cache");
     constexpr int kDecStages = DecCfg<MT, KV8, SW>::STAGES;
     constexpr int STAGE_BYTES = DecSmem<KV8>::STAGE;
@@ -220,7 +223,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8, SW>::CTAS) decode
 
     // launched as a dependent of the stream's previous kernel (enable_pdl):
     // wait for it before reading anything it may have written
-    pdl_wait();
+    if constexpr (!SHARED) pdl_wait();
     const int s = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int mt = warp % MT, kg = warp / MT;
@@ -256,7 +259,10 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8, SW>::CTAS) decode
     } else {
         decode_split_geometry(L, Q, p.window_left, p.chunk, lo, first, n_split);
     }
-    if (s >= n_split) return;
+    if (s >= n_split) {
+        if constexpr (SHARED) pdl_wait();
+        return;
+    }
     if (L < Q && s == 0 && kvh == 0 && tid == 0) set_err(p.err, PKV_DEV_ERR_QLEN);
     const int k_begin = FIRST ? s * p.chunk : max(lo, first + s * p.chunk);
     const int k_end = FIRST ? min(run.n, (s + 1) * p.chunk) : min(L, first + (s + 1) * p.chunk);
@@ -1031,7 +1037,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8, SW>::CTAS) decode
             a3 += w * x.w;
         }
         const int t = r / p.group, i = r - t * p.group, h = kvh * p.group + i;
-        if (n_split == 1) {
+        if (!SHARED && n_split == 1) {
             float sc_o, lse_v;
             if (p.sinks) {
                 const float sk = p.sinks[h] * kLog2e;
@@ -1063,6 +1069,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8, SW>::CTAS) decode
             }
         }
     }
+    if constexpr (SHARED) pdl_wait();  // whoever waits for this grid waits for the one before it too
 }
 
 // One warp per output row (b*Q + t, h): weights the split partials by
@@ -1193,7 +1200,7 @@ static int launch_split(const DecodeParams &p, dim3 grid, cudaStream_t st, bool 
     constexpr int kDecStages = DecCfg<MT, KV8, SW>::STAGES;
     const size_t smem = kDecStages * DecSmem<KV8>::STAGE + ROWS * kDecRowBytes +
                         kDecStages * kDecTile + 2 * NKG * ROWS * sizeof(float) +
-                        (EXT ? p.pages_cap : kDecMaxPages) * sizeof(int) +
+                        (EXT == 1 || EXT == 2 ? p.pages_cap : kDecMaxPages) * sizeof(int) +
                         (EXT == 2 ? p.scales_cap * sizeof(float2) : 0);
     auto kern = decode_split_kernel<T, MT, LAYOUT, KV8, SW, EXT>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
