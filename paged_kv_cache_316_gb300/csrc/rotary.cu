@@ -15,11 +15,33 @@
 // there, where an fp32 product of position and frequency has lost all).  The
 // upper 32 bits feed sincospif.
 //
-// A warp takes a token and a range of its heads; a lane holds 16 bytes of a
-// row, so D <= 64, 128 and 256 elements take 8, 16 and 32 lanes and a warp 4,
-// 2 and 1 rows at a time.  The token's cosines and sines are computed once by
-// the lanes that share them out, brought to the lanes that need them through
-// shared memory, and kept in registers over the token's heads.
+// Instruction issue bounds it before HBM does, so the work of an element is
+// brought down.  A lane holds both elements of its pairs, a and b (two pieces
+// of four elements half the rotated part apart, or eight neighbours), so that
+//   a' = (1 / rms) (ca a - sb b),   b' = (1 / rms) (cb b + sa a),
+// with the weights, cosines, sines and the magnitude folded into the four
+// factors once a token: two products and a fused product an element, two
+// elements to an instruction, and no exchange between lanes.  The sums of
+// squares of four row groups are reduced together, a quarter of them to a
+// lane.  The token's cosines and sines are computed once by the lanes that
+// share them out and exchanged through shared memory.
+//
+// A warp takes a token and a range of its row groups, queries, keys, then
+// values; D <= 64, 128 and 256 elements take 8, 16 and 32 lanes, so a group is
+// 4, 2 and 1 rows, and a batch four groups.  Batches come through a ring in
+// shared memory (cp.async), on into the warp's next token.
+//
+// Times of the call replayed from a graph (a floor of bytes at 6788 GB/s):
+// 33k tokens of 1024 requests, 32 + 8 heads, norms: 256 us (floor 239); 26k
+// tokens, fp16, half of each head, neighbours: 70.5 (64); 8k rows of 32 + 32
+// heads of 192: 66 (58); 4096 tokens of a fused projection: 22.8 (14.8, and
+// 4 us of launch, first reads and tail); 64 tokens: 4.2, seven: 4.1.
+// On the way: a row's partner by shuffles and loads of four rows, 490 us for
+// the first; rows through the ring one at a time, factors folded, 312; pairs in
+// one lane and sums of squares reduced four at a time, loads into registers,
+// 273.  More in flight is slower: 5 or 6 CTAs on an SM 254 and 307, three
+// stages 255 (with 5 CTAs 261), and the second case 77 us; fewer too (3 CTAs
+// 279): reads and writes of many rows at once leave DRAM's open pages.
 #include "pkv_common.cuh"
 
 namespace pkv {
@@ -29,7 +51,7 @@ struct RotaryParams {
     int64_t src_stride[3];   // elements from token to token
     uint16_t *dst[3];        // query rows; key / value rows or caches
     int64_t nnz;
-    int Hq, Hkv, heads;      // heads: Hq + Hkv, + Hkv with values
+    int Hq, Hkv;
     int D;
     // rotation
     const int32_t *rot_pos;
@@ -43,13 +65,21 @@ struct RotaryParams {
     const int32_t *batch_indices, *positions, *kv_indices, *kv_indptr, *kv_last_page_len;
     int64_t page_stride, max_num_pages, kv_extent;
     int B, page_shift, layout;
-    int per_warp;            // heads a warp takes of its token
-    int parts;               // warps a token is divided among
+    int batches[3];          // batches of kRotU row groups of each tensor
+    int per_part;            // a token's batches are divided among `parts` warps
+    uint32_t parts, tasks;   // tasks: tokens times parts
     int32_t *err;
 };
 
-constexpr int kRotWarps = 8;
-constexpr int kRotMaxHalf = 128;
+constexpr int kRotWarps = 4, kRotCtas = 4;
+constexpr int kRotU = 4;  // row groups in flight
+constexpr int kRotRounds = 3;
+// Stages of the ring, batches in flight less one: a batch is 2 KB a warp, 1 to
+// 2 KB with one row to a group.
+template <int LPR>
+struct RotCfg {
+    static constexpr int STAGES = LPR == 32 ? 3 : 2;
+};
 
 template <typename T>
 __device__ __forceinline__ float2 rot_unpack(uint32_t w);
@@ -61,17 +91,6 @@ template <>
 __device__ __forceinline__ float2 rot_unpack<__nv_bfloat16>(uint32_t w) {
     return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w));
 }
-template <typename T>
-__device__ __forceinline__ void rot_unpack8(const uint4 &v, float (&x)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = rot_unpack<T>(w[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-    }
-}
-
 // The angle of one step in 2^-64 turns.
 __device__ __forceinline__ uint64_t turns_per_step(double f) {
     double t = f * 0.15915494309189535;  // 1 / (2 pi)
@@ -110,120 +129,223 @@ __device__ __forceinline__ int64_t rotary_slot(const RotaryParams &p, int64_t to
     return page * p.page_stride + static_cast<int64_t>(pos & (S - 1)) * (p.layout == PKV_HND ? p.D : p.Hkv * p.D);
 }
 
+// The sums over LPR lanes of four values a lane, as 1 / sqrt(mean + eps).
+template <int LPR>
+__device__ __forceinline__ void inverse_rms4(const float (&s)[4], float inv_d, float eps, float (&inv)[4]) {
+    const int lane = threadIdx.x & 31;
+    const bool b0 = lane & 1, b1 = lane & 2;
+    // lane 0 .. 3 of four take the values 0, 2, 1, 3
+    const float u = (b0 ? s[2] : s[0]) + __shfl_xor_sync(0xffffffffu, b0 ? s[0] : s[2], 1);
+    const float v = (b0 ? s[3] : s[1]) + __shfl_xor_sync(0xffffffffu, b0 ? s[1] : s[3], 1);
+    float q = (b1 ? v : u) + __shfl_xor_sync(0xffffffffu, b1 ? u : v, 2);
+#pragma unroll
+    for (int o = 4; o < LPR; o <<= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+    q = rsqrtf(fmaf(q, inv_d, eps));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) inv[k] = __shfl_sync(0xffffffffu, q, (lane & ~3) + (k >> 1) + 2 * (k & 1));
+}
+
 // LPR lanes to a row; PAIRED: neighbouring elements are a pair (else element
 // i of the rotated part goes with element i + half).
 template <typename T, int LPR, bool PAIRED>
-__global__ void __launch_bounds__(kRotWarps * 32) rotary_kernel(const RotaryParams p) {
-    constexpr int RPW = 32 / LPR;               // rows a warp takes at a time
-    constexpr int NF = kRotMaxHalf / 32 / (LPR == 32 ? 1 : (LPR == 16 ? 2 : 4));  // frequencies of a lane
-    constexpr int NC = PAIRED ? 4 : 8;          // (cos, sin) of a lane's eight elements
-    constexpr int U = 4;                        // loads in flight
-    __shared__ float2 table[kRotWarps][kRotMaxHalf];
+__global__ void __launch_bounds__(kRotWarps * 32, kRotCtas) rotary_kernel(const __grid_constant__ RotaryParams p) {
+    constexpr int RPW = 32 / LPR, STAGES = RotCfg<LPR>::STAGES;  // rows of a group; of the ring
+    constexpr int NF = LPR == 32 ? 4 : (LPR == 16 ? 2 : 1);  // frequencies of a lane
+    __shared__ __align__(16) float2 table[kRotWarps][32 * NF];
+    __shared__ uint64_t steps[32 * NF];
+    extern __shared__ __align__(16) uint4 ring_mem[];
+    auto ring = reinterpret_cast<uint4(*)[STAGES][kRotU][32]>(ring_mem);
+    if (threadIdx.x < p.half) steps[threadIdx.x] = turns_per_step(p.freq[threadIdx.x]);
+    __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = lane & (LPR - 1), sub = lane / LPR;  // 16-byte chunk of the row, row of the warp's
+    const int c = lane & (LPR - 1), sub = lane / LPR;  // the lane's place in its row, its row of the group
     const bool on = c * 8 < p.D;
-    const int i0 = c * 8 - p.start;             // first element's place in the rotated part
-    const bool rot = on && i0 >= 0 && i0 < 2 * p.half;
-    const int t0 = PAIRED ? i0 >> 1 : (i0 < p.half ? i0 : i0 - p.half);  // its first table entry
-    const float sign = !PAIRED && i0 < p.half ? -1.f : 1.f;
-    const int mate = PAIRED || !rot ? lane : (i0 < p.half ? lane + p.half / 8 : lane - p.half / 8);
-    uint64_t step[NF];
+    const uint32_t parts = p.parts, stride = gridDim.x * kRotWarps, task0 = blockIdx.x * kRotWarps + warp;
+    const int all = p.batches[0] + p.batches[1] + p.batches[2];
+    // the stream of batches, STAGES - 1 of them ahead: lane by lane 16 bytes
+    // of the rows, zeros for rows past the last head
+    uint32_t f_task = task0, f_tok = task0 / parts;
+    int f_batch = static_cast<int>(task0 - f_tok * parts) * p.per_part, f_end = min(f_batch + p.per_part, all), f_stage = 0;
+    auto fetch = [&]() {
+        if (f_task < p.tasks) {
+            const int z = f_batch < p.batches[0] ? 0 : (f_batch < p.batches[0] + p.batches[1] ? 1 : 2);
+            const int b = f_batch - (z > 0 ? p.batches[0] : 0) - (z > 1 ? p.batches[1] : 0);
+            const int h0 = b * (kRotU * RPW) + sub, H = z == 0 ? p.Hq : p.Hkv;
+            const uint16_t *src = p.src[z] + f_tok * p.src_stride[z] + (h0 * p.D + c * 8);
+            const uint32_t to = smem_u32(&ring[warp][f_stage][0][lane]);
 #pragma unroll
-    for (int k = 0; k < NF; ++k) step[k] = lane + 32 * k < p.half ? turns_per_step(p.freq[lane + 32 * k]) : 0;
-    const bool norm[2] = {p.weight[0] != nullptr, p.weight[1] != nullptr};
-    float w[2][8];
-#pragma unroll
-    for (int z = 0; z < 2; ++z)
-        if (norm[z] && on)
-            rot_unpack8<T>(reinterpret_cast<const uint4 *>(p.weight[z])[c], w[z]);
-        else
-            for (int e = 0; e < 8; ++e) w[z][e] = 0.f;
+            for (int k = 0; k < kRotU; ++k) {
+                const bool ok = on && h0 + k * RPW < H;
+                cp_async_16(to + k * 512, ok ? src + k * (RPW * p.D) : p.src[0], ok);
+            }
+            if (++f_batch == f_end) {
+                f_task += stride;
+                if (f_task < p.tasks) {
+                    f_tok = f_task / parts;
+                    f_batch = static_cast<int>(f_task - f_tok * parts) * p.per_part;
+                    f_end = min(f_batch + p.per_part, all);
+                }
+            }
+        }
+        cp_async_commit();
+        f_stage = f_stage == STAGES - 1 ? 0 : f_stage + 1;
+    };
+#pragma unroll 1
+    for (int k = 0; k < STAGES - 1; ++k) fetch();
+    int stage = 0;
+    // where the lane's elements are: four pairs of the rotated part (from its
+    // pair t0 on), or two pieces of four outside it (so that neighbouring lanes'
+    // pieces fill whole sectors)
+    int at_a = c * 8, at_b = c * 8 + 4, t0 = -1;
+    if constexpr (PAIRED) {
+        if (c * 8 >= p.start && c * 8 < p.start + 2 * p.half) t0 = (c * 8 - p.start) >> 1;
+    } else if (4 * c < p.half) {
+        t0 = 4 * c;
+        at_a = p.start + t0;
+        at_b = at_a + p.half;
+    } else {
+        at_a = 4 * c - p.half;  // in the first half of what is left, and in its second
+        at_b = at_a + (p.D >> 1) - p.half;
+        if (at_a >= p.start) at_a += 2 * p.half;
+        if (at_b >= p.start) at_b += 2 * p.half;
+    }
+    // the lane's pairs as (a0, a1), (a2, a3) and (b0, b1), (b2, b3)
+    auto split = [](const uint2 &u, const uint2 &v, float2 (&a)[2], float2 (&b)[2]) {
+        if constexpr (PAIRED) {
+            const float2 w0 = rot_unpack<T>(u.x), w1 = rot_unpack<T>(u.y), w2 = rot_unpack<T>(v.x), w3 = rot_unpack<T>(v.y);
+            a[0] = make_float2(w0.x, w1.x);
+            b[0] = make_float2(w0.y, w1.y);
+            a[1] = make_float2(w2.x, w3.x);
+            b[1] = make_float2(w2.y, w3.y);
+        } else {
+            a[0] = rot_unpack<T>(u.x);
+            a[1] = rot_unpack<T>(u.y);
+            b[0] = rot_unpack<T>(v.x);
+            b[1] = rot_unpack<T>(v.y);
+        }
+    };
 
-    const int64_t tasks = p.nnz * p.parts;
-    for (int64_t task = static_cast<int64_t>(blockIdx.x) * kRotWarps + warp; task < tasks;
-         task += static_cast<int64_t>(gridDim.x) * kRotWarps) {
-        const int64_t tok = task / p.parts;
-        const int h0 = static_cast<int>(task - tok * p.parts) * p.per_warp, h1 = min(h0 + p.per_warp, p.heads);
-        // which tensor a head row belongs to, and its head there
-        auto tensor = [&](int h) { return h < p.Hq ? 0 : (h < p.Hq + p.Hkv ? 1 : 2); };
-        auto head_in = [&](int h, int z) { return z == 0 ? h : (z == 1 ? h - p.Hq : h - p.Hq - p.Hkv); };
-        uint4 raw[U];
-        auto load = [&](int h) {  // rows h, h + RPW, ..
-#pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const int hh = h + k * RPW + sub;
-                raw[k] = make_uint4(0u, 0u, 0u, 0u);
-                if (hh < h1 && on) {
-                    const int z = tensor(hh);
-                    raw[k] = *reinterpret_cast<const uint4 *>(p.src[z] + tok * p.src_stride[z] +
-                                                              static_cast<int64_t>(head_in(hh, z)) * p.D + c * 8);
-                }
-            }
-        };
-        load(h0);
+    for (uint32_t task = task0; task < p.tasks; task += stride) {
+        const uint32_t tok = task / parts;
+        int batch = static_cast<int>(task - tok * parts) * p.per_part;
+        const int end = min(batch + p.per_part, all);
         const int pos = p.rot_pos[tok];
+        int64_t place = -1;
+        if (p.batch_indices && end > p.batches[0]) place = rotary_slot(p, tok, lane == 0 && end == all);
+        bool fresh = true;  // the token's table is yet to be written
+        int first = 0;
+#pragma unroll 1
+        for (int z = 0; z < 3; ++z) {
+            const int last = first + p.batches[z], stop = min(end, last);
+            const int H = z == 0 ? p.Hq : p.Hkv;
+            const bool paged = z > 0 && p.batch_indices;
+            uint16_t *dst = p.dst[z] + (paged ? place : static_cast<int64_t>(tok) * H * p.D);
+            const uint32_t hop = paged && p.layout == PKV_HND ? static_cast<uint32_t>(p.D) << p.page_shift : p.D;
+            const bool writes = on && (!paged || place >= 0);
+            const bool norm = z < 2 && p.weight[z];
+            float2 ca[2], sa[2], cb[2], sb[2];
+            bool ready = z == 2;
+            for (; batch < stop; ++batch) {
+                const int h0 = (batch - first) * kRotU * RPW + sub;
+                fetch();
+                cp_async_wait<STAGES - 1>();
+                const uint4 *rows = ring[warp][stage][0];
+                stage = stage == STAGES - 1 ? 0 : stage + 1;
+                if (z == 2) {  // values: as they are, every lane its own bytes
 #pragma unroll
-        for (int k = 0; k < NF; ++k)
-            if (lane + 32 * k < p.half) table[warp][lane + 32 * k] = turned(pos, step[k], p.magnitude);
-        __syncwarp();
-        float2 cs[NC];
-#pragma unroll
-        for (int k = 0; k < NC; ++k) cs[k] = rot ? table[warp][t0 + k] : make_float2(1.f, 0.f);
-        __syncwarp();  // (the table is rewritten for the next token)
-        int64_t slot = -1;
-        if (p.batch_indices && h1 > p.Hq) slot = rotary_slot(p, tok, lane == 0 && h1 == p.heads);
-        for (int h = h0; h < h1; h += U * RPW) {
-            if (h != h0) load(h);
-#pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const int hh = h + k * RPW + sub;
-                if (h + k * RPW >= h1) break;  // (uniform: no row left for any lane)
-                const bool live = hh < h1 && on;
-                const int z = tensor(min(hh, h1 - 1));
-                uint4 out = raw[k];
-                if (__any_sync(0xffffffffu, z < 2)) {
-                    float x[8];
-                    rot_unpack8<T>(raw[k], x);
-                    if (norm[0] || norm[1]) {
-                        float ss = 0.f;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-                        for (int o = 1; o < LPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                        const float inv = rsqrtf(fmaf(ss, p.inv_d, p.eps));
-                        if (z < 2 && norm[z]) {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) x[e] *= inv * (z ? w[1][e] : w[0][e]);
-                        }
+                    for (int k = 0; k < kRotU; ++k) {
+                        const uint32_t o = (h0 + k * RPW) * hop + c * 8;
+                        if (writes && h0 + k * RPW < H && (!paged || dbg_in(place + o, 8, p.kv_extent, p.err)))
+                            *reinterpret_cast<uint4 *>(dst + o) = rows[k * 32 + lane];
                     }
-                    if constexpr (PAIRED) {
-                        if (rot) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float u = x[2 * e], v = x[2 * e + 1];
-                                x[2 * e] = u * cs[e].x - v * cs[e].y;
-                                x[2 * e + 1] = v * cs[e].x + u * cs[e].y;
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float other = __shfl_sync(0xffffffffu, x[e], mate);
-                            if (rot) x[e] = fmaf(x[e], cs[e].x, sign * other * cs[e].y);
-                        }
-                    }
-                    if (z < 2) out = make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
+                    continue;
                 }
-                if (!live) continue;
-                const int64_t hd = static_cast<int64_t>(head_in(hh, z));
-                if (z == 0 || !p.batch_indices) {
-                    const int64_t e = (tok * (z == 0 ? p.Hq : p.Hkv) + hd) * p.D + c * 8;
-                    *reinterpret_cast<uint4 *>(p.dst[z] + e) = out;
-                } else if (slot >= 0) {
-                    const int64_t e = slot + hd * (p.layout == PKV_HND ? p.D << p.page_shift : p.D) + c * 8;
-                    if (dbg_in(e, 8, p.kv_extent, p.err)) *reinterpret_cast<uint4 *>(p.dst[z] + e) = out;
+                __syncwarp();  // every lane's copies have landed
+                uint2 u[kRotU], v[kRotU];
+#pragma unroll
+                for (int k = 0; k < kRotU; ++k) {
+                    const uint16_t *row = reinterpret_cast<const uint16_t *>(rows + k * 32 + sub * LPR);
+                    u[k] = v[k] = make_uint2(0u, 0u);
+                    if (on) {
+                        u[k] = *reinterpret_cast<const uint2 *>(row + at_a);
+                        v[k] = *reinterpret_cast<const uint2 *>(row + at_b);
+                    }
+                }
+                __syncwarp();  // (the stage is copied over by the next fetch)
+                if (!ready) {  // the factors, while the rows arrive
+                    if (fresh) {
+                        __syncwarp();  // (the table of the token before has been read)
+#pragma unroll
+                        for (int k = 0; k < NF; ++k)
+                            if (lane + 32 * k < p.half) table[warp][lane + 32 * k] = turned(pos, steps[lane + 32 * k], p.magnitude);
+                        __syncwarp();
+                        fresh = false;
+                    }
+                    float2 cs[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) cs[e] = t0 >= 0 ? table[warp][t0 + e] : make_float2(1.f, 0.f);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        ca[e] = cb[e] = make_float2(cs[2 * e].x, cs[2 * e + 1].x);
+                        sa[e] = make_float2(cs[2 * e].y, cs[2 * e + 1].y);
+                        sb[e] = make_float2(-cs[2 * e].y, -cs[2 * e + 1].y);
+                    }
+                    if (norm && on) {
+                        const uint16_t *w = static_cast<const uint16_t *>(p.weight[z]);
+                        float2 wa[2], wb[2];
+                        split(*reinterpret_cast<const uint2 *>(w + at_a), *reinterpret_cast<const uint2 *>(w + at_b), wa, wb);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            ca[e] = __fmul2_rn(ca[e], wa[e]);
+                            sa[e] = __fmul2_rn(sa[e], wa[e]);
+                            cb[e] = __fmul2_rn(cb[e], wb[e]);
+                            sb[e] = __fmul2_rn(sb[e], wb[e]);
+                        }
+                    }
+                    ready = true;
+                }
+                float inv[kRotU];
+                if (norm) {
+                    float ss[kRotU];
+#pragma unroll
+                    for (int k = 0; k < kRotU; ++k) {
+                        float2 a[2], b[2];
+                        split(u[k], v[k], a, b);
+                        const float2 q = __ffma2_rn(b[1], b[1], __ffma2_rn(b[0], b[0], __ffma2_rn(a[1], a[1], __fmul2_rn(a[0], a[0]))));
+                        ss[k] = q.x + q.y;
+                    }
+                    inverse_rms4<LPR>(ss, p.inv_d, p.eps, inv);
+                }
+#pragma unroll
+                for (int k = 0; k < kRotU; ++k) {
+                    float2 a[2], b[2], x[2], y[2];
+                    split(u[k], v[k], a, b);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        x[e] = __fmul2_rn(a[e], ca[e]);
+                        y[e] = __fmul2_rn(b[e], cb[e]);
+                        if (t0 >= 0) {  // (outside the rotated part no product with another element)
+                            x[e] = __ffma2_rn(b[e], sb[e], x[e]);
+                            y[e] = __ffma2_rn(a[e], sa[e], y[e]);
+                        }
+                        if (norm) {
+                            x[e] = __fmul2_rn(x[e], make_float2(inv[k], inv[k]));
+                            y[e] = __fmul2_rn(y[e], make_float2(inv[k], inv[k]));
+                        }
+                    }
+                    const uint32_t o = (h0 + k * RPW) * hop;
+                    if (!writes || h0 + k * RPW >= H || (paged && !dbg_in(place + o, p.D, p.kv_extent, p.err))) continue;
+                    if constexpr (PAIRED) {
+                        *reinterpret_cast<uint4 *>(dst + o + at_a) =
+                            make_uint4(pack2<T>(x[0].x, y[0].x), pack2<T>(x[0].y, y[0].y), pack2<T>(x[1].x, y[1].x),
+                                       pack2<T>(x[1].y, y[1].y));
+                    } else {
+                        *reinterpret_cast<uint2 *>(dst + o + at_a) = make_uint2(pack2<T>(x[0].x, x[0].y), pack2<T>(x[1].x, x[1].y));
+                        *reinterpret_cast<uint2 *>(dst + o + at_b) = make_uint2(pack2<T>(y[0].x, y[0].y), pack2<T>(y[1].x, y[1].y));
+                    }
                 }
             }
+            first = last;
         }
     }
 }
@@ -234,7 +356,7 @@ static int check_rotary(const RotaryParams &p, int rotary_dim, int rotary_start,
         rotary_start + static_cast<int64_t>(rotary_dim) > p.D || !(p.eps >= 0.f))
         return PKV_ERR_INVALID_ARG;
     if (p.D % 16 || rotary_dim % 16 || rotary_start % 8) return PKV_ERR_INVALID_ARG;
-    if (p.D > 256 || p.Hq > 65536 || p.Hkv > 65536) return PKV_ERR_UNSUPPORTED;
+    if (p.D > 256 || p.Hq > 16384 || p.Hkv > 16384) return PKV_ERR_UNSUPPORTED;
     if (p.nnz > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
     for (int z = 0; z < 3; ++z)
         if (p.src[z] && (!aligned16(p.src[z]) || p.src_stride[z] % 8 ||
@@ -249,25 +371,29 @@ static int check_rotary(const RotaryParams &p, int rotary_dim, int rotary_start,
 template <typename T>
 static int run_rotary(RotaryParams &p, bool paired, cudaStream_t st) {
     const int rows = p.D <= 64 ? 4 : (p.D <= 128 ? 2 : 1);
-    // A warp takes all heads of a token where there are tokens enough for every
-    // warp that fits the machine; with fewer the heads are divided, down to one
-    // load of four rows a lane.
-    const int64_t want = static_cast<int64_t>(num_sms()) * 4 * kRotWarps;
-    const int least = 4 * rows;
-    const int most_parts = (p.heads + least - 1) / least;
-    int64_t parts = (want + p.nnz - 1) / p.nnz;
-    if (parts > most_parts) parts = most_parts;
-    p.per_warp = static_cast<int>((p.heads + parts - 1) / parts);
-    p.per_warp = (p.per_warp + least - 1) / least * least;
-    p.parts = (p.heads + p.per_warp - 1) / p.per_warp;
-    const int64_t blocks = (p.nnz * p.parts + kRotWarps - 1) / kRotWarps;
-    const int64_t most = static_cast<int64_t>(num_sms()) * 4;
+    const int heads = kRotU * rows;  // of a batch
+    p.batches[0] = (p.Hq + heads - 1) / heads;
+    p.batches[1] = (p.Hkv + heads - 1) / heads;
+    p.batches[2] = p.src[2] ? p.batches[1] : 0;
+    const int all = p.batches[0] + p.batches[1] + p.batches[2];
+    // A token's batches are divided among warps where there are fewer than two
+    // tokens to a warp that fits the machine.
+    const int64_t warps = static_cast<int64_t>(num_sms()) * kRotCtas * kRotWarps;
+    int64_t parts = (warps * kRotRounds + p.nnz - 1) / p.nnz;
+    if (parts > all) parts = all;
+    p.per_part = static_cast<int>((all + parts - 1) / parts);
+    p.parts = (all + p.per_part - 1) / p.per_part;
+    p.tasks = static_cast<uint32_t>(p.nnz * p.parts);  // (several parts only where there are few tokens)
+    const int64_t blocks = (static_cast<int64_t>(p.tasks) + kRotWarps - 1) / kRotWarps;
+    const int64_t most = static_cast<int64_t>(num_sms()) * kRotCtas;
     const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
     auto pick = [&](auto a, auto b) { return paired ? a : b; };
     auto kern = rows == 4 ? pick(rotary_kernel<T, 8, true>, rotary_kernel<T, 8, false>)
                           : (rows == 2 ? pick(rotary_kernel<T, 16, true>, rotary_kernel<T, 16, false>)
                                        : pick(rotary_kernel<T, 32, true>, rotary_kernel<T, 32, false>));
-    kern<<<grid, kRotWarps * 32, 0, st>>>(p);
+    const int stages = rows == 4 ? RotCfg<8>::STAGES : (rows == 2 ? RotCfg<16>::STAGES : RotCfg<32>::STAGES);
+    const int smem = kRotWarps * stages * kRotU * 512;  // (24 KB at most, beside 5 KB of tables)
+    kern<<<grid, kRotWarps * 32, smem, st>>>(p);
     note_launches(1);
     return launch_status();
 }
@@ -292,7 +418,6 @@ extern "C" int paged_rotary(const void *query, const void *key, int64_t query_st
     p.nnz = nnz;
     p.Hq = num_qo_heads;
     p.Hkv = num_kv_heads;
-    p.heads = num_qo_heads + num_kv_heads;
     p.D = head_dim;
     p.rot_pos = positions;
     p.freq = frequencies;
@@ -337,7 +462,6 @@ extern "C" int paged_append_rotary(const void *query, const void *key, const voi
     p.nnz = nnz;
     p.Hq = num_qo_heads;
     p.Hkv = num_kv_heads;
-    p.heads = num_qo_heads + 2 * num_kv_heads;
     p.D = head_dim;
     p.rot_pos = rotary_positions ? rotary_positions : positions;
     p.freq = frequencies;
@@ -355,6 +479,7 @@ extern "C" int paged_append_rotary(const void *query, const void *key, const voi
     if (p.page_shift < 0 || p.page_shift > 16) return PKV_ERR_UNSUPPORTED;
     const int64_t page = static_cast<int64_t>(num_kv_heads) * page_size * head_dim;
     if (page_stride < page || page_stride % 8) return PKV_ERR_INVALID_ARG;
+    if (page > (1 << 30)) return PKV_ERR_UNSUPPORTED;  // (offsets in a page: 32 bits)
     if (nnz == 0) return PKV_OK;
     if (!query || !key || !value || !batch_indices || !positions || !k_cache || !v_cache || !kv_indices || !kv_indptr ||
         !kv_last_page_len || (rotary_dim > 0 && !frequencies) || !query_out)
