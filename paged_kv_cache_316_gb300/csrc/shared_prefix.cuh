@@ -1,0 +1,138 @@
+// shared_prefix.cuh -- how the prefixes of a shared decode are cut into work
+// and where the partial results of a row lie: the part that the prefix kernel
+// (decode_shared.cu) and the kernels that join its partials agree on.
+//
+// Work.  CTAs come in teams of `team` neighbours (1 where nothing is won, see
+// plan_shared).  An item is `team` tiles of a group's tokens (a tile: nb blocks
+// of `tok` tokens), one for each member, at one kv head; it takes nk =
+// ceil(prefix / 128) steps, a step being a tile of 128 keys, which the members
+// read at about the same time: from HBM once.  The items of all groups laid
+// end to end (by group, kv head, tiles of tokens) are W steps, of which team c
+// takes [c per, (c + 1) per): the lengths and sizes are read on the device, so
+// that the cut is even whatever they are, and every kernel that needs it works
+// it out again.  A CTA's run through one item is a segment; only its first can
+// begin inside an item.
+//
+// Partials.  Row (token, head) of the segment that begins the item: index
+// token * Hqo + head; of a segment that continues it: rows + (cta * nb +
+// block) * 128 + row of the block.  One fp32 output row and one base-2 LSE each.
+#pragma once
+
+#include "pkv_common.cuh"
+
+namespace pkv {
+
+constexpr int kShTile = 128;  // keys per step
+constexpr int kShMinSteps = 8;
+
+struct PrefixWork {
+    const int32_t *group_indptr, *prefix_lens;
+    int G, B, Q, Hqo, Hkv, group;
+    int tok, nb;  // tokens of a block (128 / group), blocks of an item
+    int max_prefix;
+    int team, ctas;  // ctas: a multiple of team
+    int full;        // teams that all SMs hold
+    int64_t rows;   // B * Q * Hqo
+    int64_t parts;  // rows + ctas * nb * 128
+    float *ws_o;    // [parts][128]
+    float *ws_lse;  // [parts], base 2
+    int32_t *err;
+};
+
+// One group: its requests [a, b), its prefix of P keys in nk steps, its tiles
+// of tokens and items at a kv head, and the number of its first step.
+struct PrefixGroup {
+    int g, a, b, P, nk, tiles, items;
+    uint32_t base;
+};
+
+__device__ __forceinline__ void read_prefix_group(const PrefixWork &p, int g, PrefixGroup &x) {
+    x.g = g;
+    x.a = p.group_indptr[g];
+    x.b = p.group_indptr[g + 1];
+    x.P = min(max(p.prefix_lens[g], 0), p.max_prefix);
+    x.nk = (x.P + kShTile - 1) / kShTile;
+    const int T = p.nb * p.tok;
+    x.tiles = ((x.b - x.a) * p.Q + T - 1) / T;
+    x.items = (x.tiles + p.team - 1) / p.team;
+}
+
+// All groups, by one warp: returns W and, in `found`, the group for which
+// match(a, b, first step, steps) holds (g = -1: none).  Where group_indptr is
+// not in order no group has work (*bad).
+template <typename F>
+__device__ __forceinline__ uint32_t scan_prefixes(const PrefixWork &p, F match, PrefixGroup &found, bool &bad) {
+    const int lane = threadIdx.x & 31;
+    uint32_t carry = 0;
+    found.g = -1;
+    bad = false;
+    for (int g0 = 0; g0 < p.G; g0 += 32) {
+        const int g = g0 + lane;
+        PrefixGroup x = {};
+        bool wrong = false;
+        if (g < p.G) {
+            read_prefix_group(p, g, x);
+            wrong = x.a < 0 || x.b < x.a || x.b > p.B || (g == 0 && x.a != 0);
+        }
+        if (__any_sync(0xffffffffu, wrong)) bad = true;
+        const uint32_t n = g < p.G && !bad ? static_cast<uint32_t>(x.items) * p.Hkv * x.nk : 0u;
+        uint32_t sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        const unsigned m = __ballot_sync(0xffffffffu, g < p.G && match(x.a, x.b, carry + sum - n, n));
+        if (m && found.g < 0) {
+            const int j = __ffs(m) - 1;
+            found.g = g0 + j;
+            found.a = __shfl_sync(0xffffffffu, x.a, j);
+            found.b = __shfl_sync(0xffffffffu, x.b, j);
+            found.P = __shfl_sync(0xffffffffu, x.P, j);
+            found.nk = __shfl_sync(0xffffffffu, x.nk, j);
+            found.tiles = __shfl_sync(0xffffffffu, x.tiles, j);
+            found.items = __shfl_sync(0xffffffffu, x.items, j);
+            found.base = carry + __shfl_sync(0xffffffffu, sum - n, j);
+        }
+        carry += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (bad) {
+        found.g = -1;
+        return 0;
+    }
+    return carry;
+}
+
+// Steps of a team: all share the work evenly, but none takes fewer than
+// kShMinSteps while half of the SMs would do.
+__device__ __forceinline__ uint32_t prefix_steps_per_team(const PrefixWork &p, uint32_t W) {
+    const uint32_t n = p.ctas / p.team, even = (W + n - 1) / n, half = (2 * W + p.full - 1) / p.full;
+    return max(1u, max(even, min(static_cast<uint32_t>(kShMinSteps), half)));
+}
+
+// The partials of a token's rows at one kv head: the first at `row` (of the
+// kv head's first query head), n in all, the others at extra + i * step.
+struct PrefixParts {
+    int n;
+    int64_t row, extra;
+    int step;
+    __device__ __forceinline__ int64_t at(int i) const { return i == 0 ? row : extra + static_cast<int64_t>(i) * step; }
+};
+__device__ __forceinline__ PrefixParts prefix_parts(const PrefixWork &p, const PrefixGroup &x, uint32_t per, int token,
+                                                    int head, int kvh) {
+    PrefixParts r;
+    r.n = 0;
+    r.row = static_cast<int64_t>(token) * p.Hqo + head;
+    r.extra = 0;
+    r.step = p.team * p.nb * 128;
+    if (x.g < 0 || x.nk == 0) return r;
+    const int T = p.nb * p.tok, tk = token - x.a * p.Q, tile = tk / T, in = tk - tile * T, block = in / p.tok;
+    const int item = tile / p.team, member = tile - item * p.team;
+    const uint32_t s0 = x.base + (static_cast<uint32_t>(kvh) * x.items + item) * x.nk, c0 = s0 / per;
+    r.n = static_cast<int>((s0 + x.nk - 1) / per - c0) + 1;
+    r.extra = p.rows + ((static_cast<int64_t>(c0) * p.team + member) * p.nb + block) * 128 + (in - block * p.tok) * p.group +
+              (head - kvh * p.group);
+    return r;
+}
+
+}  // namespace pkv
