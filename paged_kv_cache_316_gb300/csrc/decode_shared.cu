@@ -4,14 +4,12 @@
 //
 // A row's softmax runs over two sets of keys, so it is taken over each with its
 // log-sum-exp and merged: out = sum_s e^(l_s - L) o_s, L = log sum_s e^(l_s)
-// (+ e^sink).  Two grids, or three:
+// (+ e^sink).  Three grids:
 //   shared_prefix_kernel  the prefixes: all rows of a group that share a kv
 //           head (tokens x query heads) against its keys, on tcgen05;
-//   decode_split_kernel   the requests' own keys (EXT 3), HBM-bound streaming;
-//           it does not wait for the first grid but runs beside its end, and
-//           joins the prefix's partials where a request's keys are one split;
-//   shared_merge_kernel   where they can be several: one warp a row joins the
-//           partials of both.
+//   shared_own_kernel     the requests' own keys (shared_own.cuh), HBM-bound
+//           streaming; it does not wait for the first grid but runs beside it;
+//   shared_merge_kernel   joins the partials of both.
 //
 // The prefix kernel.  One CTA per SM takes an even share of the steps (see
 // shared_prefix.cuh), item by item: NB blocks of 128 rows (row = token * group
@@ -32,13 +30,14 @@
 #include <math.h>
 
 #include "attn_tile.cuh"
-#include "decode_split.cuh"
+#include "shared_own.cuh"
 #include "shared_prefix.cuh"
 #include "sm103_ptx.cuh"
 
 namespace pkv {
 
 constexpr int kShD = 128;
+constexpr int kOwnItems = 5;  // own keys: items of a CTA
 constexpr uint32_t kShTileBytes = kShTile * kShD * 2;  // a K or V tile, a block of Q rows
 template <int NB>
 struct ShCfg {
@@ -486,36 +485,8 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
     }
 }
 
-// One warp per output row of the requests whose own keys are several splits:
-// the partials of its group's prefix and of its own keys, and the sink.
-template <typename T>
-__global__ void __launch_bounds__(128) shared_merge_kernel(const __grid_constant__ DecodeSharedParams p) {
-    const PrefixWork &w = p.prefix;
-    const int lane = threadIdx.x & 31;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (row >= w.rows) return pdl_wait();
-    const int h = static_cast<int>(row % p.Hqo), token = static_cast<int>(row / p.Hqo);
-    const int b = token / p.Q, t = token - b * p.Q, kvh = h / p.group;
-    const uint32_t L_in = p.seq_lens[b];
-    const int L = L_in > static_cast<uint32_t>(p.max_seq_len) ? p.max_seq_len : static_cast<int>(L_in);
-    int k_lo, first, n_own;
-    decode_split_geometry(L, p.Q, -1, p.chunk, k_lo, first, n_own);
-    if (n_own <= 1) return pdl_wait();  // (this grid ends after the ones before it all the same)
-    PrefixGroup x;
-    bool bad;
-    const uint32_t W = scan_prefixes(w, [=](int lo, int hi, uint32_t, uint32_t) { return lo <= b && b < hi; }, x, bad);
-    const PrefixParts parts = prefix_parts(w, x, prefix_steps_per_team(w, W), token, h, kvh);
-    const int64_t own = static_cast<int64_t>(b * p.Hkv + kvh) * p.n_split_max * p.R + t * p.group + (h - kvh * p.group);
-    pdl_wait();
-    if (!dbg_in(own, static_cast<int64_t>(n_own - 1) * p.R + 1, p.ws_rows, p.err)) return;
-    RowSum sum;
-    add_parts(sum, n_own, [&](int i) { return own + static_cast<int64_t>(i) * p.R; }, p.ws_o, p.ws_lse, p.ws_rows, p.err);
-    add_parts(sum, parts.n, [&](int i) { return parts.at(i); }, w.ws_o, w.ws_lse, w.parts, p.err);
-    finish_row<T>(sum, p, row, h, lane * 4, p.bmm2_dev ? __ldg(p.bmm2_dev) : p.bmm2);
-}
-
 struct SharedPlan {
-    DecodePlan own;
+    int R, MT, chunk, n_split_max;  // own keys: rows of an item, tiles of 16 of them, keys and splits
     int nb, tok, team, ctas;
     int64_t rows, parts;
     size_t prefix_o, prefix_lse, own_o, own_lse, bytes;  // offsets in the workspace
@@ -523,11 +494,21 @@ struct SharedPlan {
 
 static int plan_shared(int B, int Q, int Hqo, int Hkv, int D, int G, int max_prefix, int max_seq_len, int page_size,
                        SharedPlan &pl) {
-    if (G < 0 || max_prefix < 0) return PKV_ERR_INVALID_ARG;
-    // own keys up to 512 stay one split: the merge kernel of several costs more
-    const int rc = plan_decode(B, Q, Hqo, Hkv, D, max_seq_len, page_size, -1, pl.own, false, 0, 512);
-    if (rc != PKV_OK) return rc;
+    if (B < 0 || Q < 1 || Hqo < 1 || Hkv < 1 || max_seq_len < 0 || G < 0 || max_prefix < 0 || Hqo % Hkv)
+        return PKV_ERR_INVALID_ARG;
     const int group = Hqo / Hkv;
+    if (B > 65535 || Hkv > 65535 || D != kShD || ilog2_exact(page_size) < 3 || page_size > 256 ||
+        static_cast<int64_t>(group) * Q > 64 || max_seq_len > (1 << 30))
+        return PKV_ERR_UNSUPPORTED;
+    // Own keys: splits short enough that each of two CTAs per SM has several,
+    // which evens out requests of different lengths, but of no fewer than 256
+    // keys.
+    pl.R = group * Q;
+    pl.MT = pl.R <= 16 ? 1 : (pl.R <= 32 ? 2 : 4);
+    const int64_t share = static_cast<int64_t>(B) * Hkv * max_seq_len / (kOwnItems * 2 * num_sms());
+    const int64_t chunk = (share < 256 ? 256 : (share > 4096 ? 4096 : share)) + kOwnTile - 1;
+    pl.chunk = static_cast<int>(chunk / kOwnTile * kOwnTile);
+    pl.n_split_max = own_splits(max_seq_len, pl.chunk);
     if (max_prefix > (1 << 30) || static_cast<int64_t>(B) * Q * Hqo > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
     pl.rows = static_cast<int64_t>(B) * Q * Hqo;
     pl.tok = 128 / group;
@@ -556,23 +537,27 @@ static int plan_shared(int B, int Q, int Hqo, int Hkv, int D, int G, int max_pre
     const int64_t most = tiles * Hkv * nk;  // (a CTA takes one step at least; a team is for more than that)
     pl.ctas = G > 0 && nk > 0 ? static_cast<int>((most < sms ? most : sms) / pl.team * pl.team) : 0;
     pl.parts = pl.ctas > 0 ? pl.rows + static_cast<int64_t>(pl.ctas) * pl.nb * 128 : 0;
-    const size_t slots = static_cast<size_t>(B) * Hkv * pl.own.n_split_max * pl.own.R;
+    const size_t slots = static_cast<size_t>(B) * Hkv * pl.n_split_max * pl.R;
     size_t at = 0;
     pl.prefix_o = at;
     at += round_up(pl.parts * kShD * sizeof(float), 256);
     pl.prefix_lse = at;
     at += round_up(pl.parts * sizeof(float), 256);
     pl.own_o = at;
-    if (pl.own.n_split_max > 1) at += round_up(slots * kShD * sizeof(float), 256);
+    at += round_up(slots * kShD * sizeof(float), 256);
     pl.own_lse = at;
-    if (pl.own.n_split_max > 1) at += round_up(slots * sizeof(float), 256);
-    pl.bytes = at > 0 ? at : 256;
+    at += round_up(slots * sizeof(float), 256);
+    pl.bytes = at;
     return PKV_OK;
 }
 
+struct SharedMaps {
+    CUtensorMap q, k, v;              // the prefix kernel's: queries of a block of rows, the caches
+    CUtensorMap own_q, own_k, own_v;  // the own keys': queries of a request, the caches
+};
+
 template <typename T, int LAYOUT, int NB>
-static int launch_prefix(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const SharedParams &p,
-                         dim3 grid, cudaStream_t st) {
+static int launch_prefix(const SharedMaps &m, const SharedParams &p, dim3 grid, cudaStream_t st) {
     auto kern = shared_prefix_kernel<T, LAYOUT, NB>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(ShCfg<NB>::SMEM)) !=
         cudaSuccess)
@@ -588,34 +573,38 @@ static int launch_prefix(const CUtensorMap &tq, const CUtensorMap &tk, const CUt
         }
         if (!ok) return PKV_ERR_UNSUPPORTED;
     }
-    kern<<<grid, ShCfg<NB>::THREADS, ShCfg<NB>::SMEM, st>>>(tq, tk, tv, p);
+    kern<<<grid, ShCfg<NB>::THREADS, ShCfg<NB>::SMEM, st>>>(m.q, m.k, m.v, p);
     return PKV_OK;
 }
 
-template <typename T>
-static int run_shared(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const SharedParams &s,
-                      const DecodeSharedParams &d, const SharedPlan &pl, int layout, cudaStream_t st) {
-    const bool hnd = layout == PKV_HND, prefix = pl.ctas > 0;
-    int launches = 1;
-    if (prefix) {
-        const dim3 grid(pl.ctas);
-        const int rc = pl.nb == 2 ? (hnd ? launch_prefix<T, PKV_HND, 2>(tq, tk, tv, s, grid, st)
-                                         : launch_prefix<T, PKV_NHD, 2>(tq, tk, tv, s, grid, st))
-                                  : (hnd ? launch_prefix<T, PKV_HND, 1>(tq, tk, tv, s, grid, st)
-                                         : launch_prefix<T, PKV_NHD, 1>(tq, tk, tv, s, grid, st));
+template <typename T, int MT>
+static int launch_own(const SharedMaps &m, const OwnParams &p, dim3 grid, cudaStream_t st) {
+    auto kern = shared_own_kernel<T, MT>;
+    constexpr int smem = static_cast<int>(OwnCfg<MT>::SMEM);
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return PKV_ERR_CUDA;
+    if (p.prefix.ctas > 0)
+        return launch_dependent(kern, grid, dim3(kOwnThreads), smem, st, m.own_q, m.own_k, m.own_v, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    kern<<<grid, kOwnThreads, smem, st>>>(m.own_q, m.own_k, m.own_v, p);
+    return PKV_OK;
+}
+
+template <typename T, int LAYOUT>
+static int run_shared(const SharedMaps &m, const SharedParams &s, const OwnParams &p, const SharedPlan &pl, cudaStream_t st) {
+    int launches = 2, rc = PKV_OK;
+    if (pl.ctas > 0) {
+        rc = pl.nb == 2 ? launch_prefix<T, LAYOUT, 2>(m, s, dim3(pl.ctas), st)
+                        : launch_prefix<T, LAYOUT, 1>(m, s, dim3(pl.ctas), st);
         if (rc != PKV_OK) return rc;
         ++launches;
     }
-    const dim3 grid(pl.own.n_split_max, d.Hkv, d.B);
-    const int rc = hnd ? launch_split_mt<T, PKV_HND, false, 3>(pl.own.MT, d, grid, st, prefix)
-                       : launch_split_mt<T, PKV_NHD, false, 3>(pl.own.MT, d, grid, st, prefix);
+    const dim3 grid(pl.n_split_max, p.prefix.Hkv, p.prefix.B);
+    rc = pl.MT == 1 ? launch_own<T, 1>(m, p, grid, st)
+                    : (pl.MT == 2 ? launch_own<T, 2>(m, p, grid, st) : launch_own<T, 4>(m, p, grid, st));
     if (rc != PKV_OK) return rc;
-    if (pl.own.n_split_max > 1) {
-        if (launch_dependent(shared_merge_kernel<T>, dim3(static_cast<unsigned>((pl.rows + 3) / 4)), dim3(128), 0, st,
-                             d) != cudaSuccess)
-            return PKV_ERR_CUDA;
-        ++launches;
-    }
+    const int64_t warps = (pl.rows + p.merge_rows - 1) / p.merge_rows;
+    if (launch_dependent(shared_merge_kernel<T>, dim3(static_cast<unsigned>((warps + 3) / 4)), dim3(128), 0, st, p) !=
+        cudaSuccess)
+        return PKV_ERR_CUDA;
     note_launches(launches);
     return launch_status();
 }
@@ -692,57 +681,57 @@ extern "C" int paged_decode_shared(const void *query, const void *k_cache, const
     s.bmm1_dev = bmm1_scale_dev;
     s.wait_ns = wait_limit_ns();
 
-    DecodeSharedParams d = {};
+    OwnParams d = {};
     d.prefix = w;
-    d.q = query;
-    d.k = k_cache;
-    d.v = v_cache;
-    d.page_stride = page_stride;
-    d.max_num_pages = max_num_pages;
     d.block_tables = block_tables;
     d.bt_stride = block_table_stride;
     d.seq_lens = seq_lens;
-    d.B = batch_size;
     d.max_seq_len = max_seq_len;
-    d.scale_log2 = bmm1_scale * kLog2e;
+    d.max_num_pages = max_num_pages;
+    d.scale_log2 = s.scale_log2;
     d.bmm1_dev = bmm1_scale_dev;
     d.bmm2_dev = bmm2_scale_dev;
     d.bmm2 = bmm2_scale;
-    d.window_left = -1;
     d.sinks = sinks;
-    d.Q = q_len_per_req;
-    d.Hqo = num_qo_heads;
-    d.Hkv = num_kv_heads;
-    d.group = w.group;
-    d.R = pl.own.R;
-    d.num_tokens = static_cast<int64_t>(batch_size) * q_len_per_req;
-    d.kv_extent = max_num_pages > 0 ? (max_num_pages - 1) * page_stride + page : 0;
-    d.ws_rows = static_cast<int64_t>(batch_size) * num_kv_heads * pl.own.n_split_max * pl.own.R;
+    d.R = pl.R;
     d.page_shift = s.page_shift;
-    d.chunk = pl.own.chunk;
-    d.n_split_max = pl.own.n_split_max;
+    d.chunk = pl.chunk;
+    d.n_split_max = pl.n_split_max;
     d.out = out;
     d.lse = lse;
     d.ws_o = reinterpret_cast<float *>(ws + pl.own_o);
     d.ws_lse = reinterpret_cast<float *>(ws + pl.own_lse);
+    d.ws_rows = static_cast<int64_t>(batch_size) * num_kv_heads * pl.n_split_max * pl.R;
+    // (a warp for a row until every SM has 28 of them, then one for up to 8)
+    const int64_t fill = (pl.rows + 28 * num_sms() - 1) / (28 * num_sms());
+    d.merge_rows = static_cast<int>(fill < 8 ? fill : 8);
     d.err = err_word;
+    d.wait_ns = s.wait_ns;
 
-    CUtensorMap tq, tk, tv;
+    SharedMaps m;
+    const CUtensorMapDataType t = dtype == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    // rows of queries in one box for each half of the head: (64 elements, the
+    // group's heads, whole tokens)
+    const uint64_t dims[3] = {kShD, static_cast<uint64_t>(num_qo_heads), static_cast<uint64_t>(batch_size) * q_len_per_req};
+    const uint64_t strides[2] = {kShD * 2, static_cast<uint64_t>(num_qo_heads) * kShD * 2};
+    const uint32_t heads = static_cast<uint32_t>(w.group);
+    const uint32_t block[3] = {64, heads, static_cast<uint32_t>(w.tok)}, own[3] = {64, heads, static_cast<uint32_t>(w.Q)};
+    const int64_t pages = max_num_pages > 0 ? max_num_pages : 1;
     if (pl.ctas > 0) {
-        const CUtensorMapDataType t = dtype == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-        // a block of rows in one box for each half of the head: (64 elements,
-        // the group's heads, whole tokens)
-        const uint64_t dims[3] = {kShD, static_cast<uint64_t>(num_qo_heads), static_cast<uint64_t>(d.num_tokens)};
-        const uint64_t strides[2] = {kShD * 2, static_cast<uint64_t>(num_qo_heads) * kShD * 2};
-        const uint32_t box[3] = {64, static_cast<uint32_t>(w.group), static_cast<uint32_t>(w.tok)};
-        const int rows = pf_box_rows(page_size, kShTile);
-        const int64_t pages = max_num_pages > 0 ? max_num_pages : 1;
-        if (!encode_tmap(&tq, query, t, 3, dims, strides, box) ||
-            !cache_tmap(&tk, k_cache, t, layout, kShD, page_size, num_kv_heads, page_stride, pages, rows) ||
-            !cache_tmap(&tv, v_cache, t, layout, kShD, page_size, num_kv_heads, page_stride, pages, rows))
+        const int box = pf_box_rows(page_size, kShTile);
+        if (!encode_tmap(&m.q, query, t, 3, dims, strides, block) ||
+            !cache_tmap(&m.k, k_cache, t, layout, kShD, page_size, num_kv_heads, page_stride, pages, box) ||
+            !cache_tmap(&m.v, v_cache, t, layout, kShD, page_size, num_kv_heads, page_stride, pages, box))
             return PKV_ERR_CUDA;
     }
+    const int box = pf_box_rows(page_size, kOwnTile);
+    if (!encode_tmap(&m.own_q, query, t, 3, dims, strides, own) ||
+        !own_tmap(&m.own_k, k_cache, t, layout, page_size, num_kv_heads, page_stride, pages, box) ||
+        !own_tmap(&m.own_v, v_cache, t, layout, page_size, num_kv_heads, page_stride, pages, box))
+        return PKV_ERR_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return dtype == PKV_BF16 ? run_shared<__nv_bfloat16>(tq, tk, tv, s, d, pl, layout, st)
-                             : run_shared<__half>(tq, tk, tv, s, d, pl, layout, st);
+    if (dtype == PKV_BF16)
+        return layout == PKV_HND ? run_shared<__nv_bfloat16, PKV_HND>(m, s, d, pl, st)
+                                 : run_shared<__nv_bfloat16, PKV_NHD>(m, s, d, pl, st);
+    return layout == PKV_HND ? run_shared<__half, PKV_HND>(m, s, d, pl, st) : run_shared<__half, PKV_NHD>(m, s, d, pl, st);
 }

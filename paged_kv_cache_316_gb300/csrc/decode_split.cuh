@@ -46,7 +46,6 @@
 #include <type_traits>
 
 #include "pkv_common.cuh"
-#include "shared_prefix.cuh"
 
 namespace pkv {
 
@@ -127,13 +126,6 @@ struct DecodeParams {
     int pages_cap, scales_cap;  // entries of the split's page and scale lists (shared memory)
 };
 
-// (EXT == 3) a request's own keys behind a shared prefix.
-struct DecodeSharedParams : DecodeParams {
-    PrefixWork prefix;
-};
-template <int EXT>
-using DecParams = typename std::conditional<EXT == 3, DecodeSharedParams, DecodeParams>::type;
-
 // Lowest visible key `lo` of a request and how its range [lo, L) is cut into
 // splits: from `first` = lo rounded down to a 64-key tile, split s covers
 // keys [max(lo, first + s * chunk), min(L, first + (s + 1) * chunk)).  An
@@ -196,85 +188,13 @@ __device__ __forceinline__ void store4(T *dst, float a, float b, float c, float 
     *reinterpret_cast<uint2 *>(dst) = v;
 }
 
-// A row's softmax while partial results join it, by one warp: maximum (base 2),
-// sum, four of the output's dimensions a lane.
-struct RowSum {
-    float M = -INFINITY, den = 0.f;
-    float4 acc = {0.f, 0.f, 0.f, 0.f};
-};
-// n partials, part i at index at(i) of (ws_o, ws_lse), eight at a time so that
-// their loads are in flight together.
-template <typename F>
-__device__ __forceinline__ void add_parts(RowSum &s, int n, F at, const float *ws_o, const float *ws_lse, int64_t extent,
-                                          int32_t *err) {
-    const int lane = threadIdx.x & 31;
-    for (int i0 = 0; i0 < n; i0 += 8) {
-        float x[8];
-        float4 v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            x[i] = -INFINITY;
-            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i0 + i < n) {
-                const int64_t row = at(i0 + i);
-                if (dbg_in(row, 1, extent, err)) {
-                    x[i] = ws_lse[row];
-                    v[i] = *reinterpret_cast<const float4 *>(ws_o + row * kDecD + lane * 4);
-                }
-            }
-        }
-        float top = s.M;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, x[i]);
-        const float base = top == -INFINITY ? 0.f : top, keep = fast_exp2(s.M - base);
-        s.M = top;
-        s.den *= keep;
-        s.acc = make_float4(s.acc.x * keep, s.acc.y * keep, s.acc.z * keep, s.acc.w * keep);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float w = fast_exp2(x[i] - base);  // (a part's NaN stays)
-            s.den += w;
-            s.acc.x += w * v[i].x;
-            s.acc.y += w * v[i].y;
-            s.acc.z += w * v[i].z;
-            s.acc.w += w * v[i].w;
-        }
-    }
-}
-// The sink, bmm2's scale, and the row written out.
-template <typename T>
-__device__ __forceinline__ void finish_row(const RowSum &s, const DecodeParams &p, int64_t row, int h, int d, float bmm2) {
-    float sc, lse_v, den = s.den, up = 1.f, M = s.M;
-    if (p.sinks) {
-        const float sink = p.sinks[h] * kLog2e;
-        M = fmaxf(M, sink);
-        if (M != -INFINITY) {
-            up = fast_exp2(s.M - M);
-            den = den * up + fast_exp2(sink - M);
-        }
-    }
-    if (den > 0.f) {
-        sc = bmm2 * up / den;
-        lse_v = (M + fast_log2(den)) * kLn2;
-    } else {
-        sc = den != den ? den : 0.f;  // a NaN among the visible keys; no key
-        lse_v = den != den ? den : -INFINITY;
-    }
-    if (!dbg_in(row * kDecD + d, 4, p.num_tokens * p.Hqo * kDecD, p.err)) return;
-    store4(static_cast<T *>(p.out) + row * kDecD + d, s.acc.x * sc, s.acc.y * sc, s.acc.z * sc, s.acc.w * sc);
-    if (p.lse && d == 0) p.lse[row] = lse_v;
-}
-
 // SW > 0 (an E4M3 cache and at most 8 SW query rows): the MMAs take the keys
 // as their 16-row side, S^T = K Q^T and O^T = V^T P^T (see the tile loop).
 // EXT: 0 all keys or a window; 1 a window and first tokens; 2 the same over
-// an E4M3 cache with a scale for each block of keys and head; 3 the requests'
-// own keys behind a shared prefix (decode_shared.cu): the grid runs beside the
-// one before it, whose end it awaits before it joins that one's partials to
-// its rows (keys in one split) or, having written its own, before its end.
+// an E4M3 cache with a scale for each block of keys and head.
 template <typename T, int MT, int LAYOUT, bool KV8, int SW = 0, int EXT = 0>
-__global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8, SW>::CTAS) decode_split_kernel(const DecParams<EXT> p) {
-    constexpr bool FIRST = EXT == 1 || EXT == 2, SCL = EXT == 2, SHARED = EXT == 3;
+__global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8, SW>::CTAS) decode_split_kernel(const DecodeParams p) {
+    constexpr bool FIRST = EXT >= 1, SCL = EXT == 2;
     static_assert(!SCL || KV8, "block scales: E4M3 cache");
     constexpr int kDecStages = DecCfg<MT, KV8, SW>::STAGES;
     constexpr int STAGE_BYTES = DecSmem<KV8>::STAGE;
@@ -300,7 +220,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8, SW>::CTAS) decode
 
     // launched as a dependent of the stream's previous kernel (enable_pdl):
     // wait for it before reading anything it may have written
-    if constexpr (!SHARED) pdl_wait();
+    pdl_wait();
     const int s = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int mt = warp % MT, kg = warp / MT;
@@ -336,10 +256,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8, SW>::CTAS) decode
     } else {
         decode_split_geometry(L, Q, p.window_left, p.chunk, lo, first, n_split);
     }
-    if (s >= n_split) {
-        if constexpr (SHARED) pdl_wait();
-        return;
-    }
+    if (s >= n_split) return;
     if (L < Q && s == 0 && kvh == 0 && tid == 0) set_err(p.err, PKV_DEV_ERR_QLEN);
     const int k_begin = FIRST ? s * p.chunk : max(lo, first + s * p.chunk);
     const int k_end = FIRST ? min(run.n, (s + 1) * p.chunk) : min(L, first + (s + 1) * p.chunk);
@@ -581,21 +498,6 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8, SW>::CTAS) decode
         const int i = (j >> p.block_shift) - (j0 >= run.n_first + run.gap ? first_block2 - n_blocks1 : first_block);
         return scale_s[min(max(i, 0), n_blocks - 1)];
     };
-    // (SHARED) the request's group, while the first tiles come
-    __shared__ PrefixGroup group_s;
-    __shared__ uint32_t per_s;
-    if constexpr (SHARED) {
-        if (warp == 0 && n_split == 1) {
-            PrefixGroup x;
-            bool bad;
-            const uint32_t W =
-                scan_prefixes(p.prefix, [=](int a, int e, uint32_t, uint32_t) { return a <= b && b < e; }, x, bad);
-            if (lane == 0) {
-                group_s = x;
-                per_s = prefix_steps_per_team(p.prefix, W);
-            }
-        }
-    }
     cp_async_wait<kDecStages - 1>();
     __syncthreads();
 
@@ -1110,9 +1012,6 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8, SW>::CTAS) decode
         comb_l[kg * ROWS + r1] = l1;
     }
     __syncthreads();
-    if constexpr (SHARED) {
-        if (n_split == 1) pdl_wait();  // the prefix's partials
-    }
 
     for (int idx = tid; idx < R * 32; idx += kDecThreads) {
         const int r = idx >> 5, d = (idx & 31) * 4;
@@ -1132,19 +1031,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8, SW>::CTAS) decode
             a3 += w * x.w;
         }
         const int t = r / p.group, i = r - t * p.group, h = kvh * p.group + i;
-        if (SHARED && n_split == 1) {
-            if constexpr (SHARED) {
-                const int token = static_cast<int>(qrow0) + t;
-                const PrefixParts parts = prefix_parts(p.prefix, group_s, per_s, token, h, kvh);
-                RowSum sum;
-                sum.M = M;
-                sum.den = lsum;
-                sum.acc = make_float4(a0, a1, a2, a3);
-                add_parts(sum, parts.n, [&](int j) { return parts.at(j); }, p.prefix.ws_o, p.prefix.ws_lse,
-                          p.prefix.parts, p.err);
-                finish_row<T>(sum, p, (qrow0 + t) * p.Hqo + h, h, d, bmm2);
-            }
-        } else if (n_split == 1) {
+        if (n_split == 1) {
             float sc_o, lse_v;
             if (p.sinks) {
                 const float sk = p.sinks[h] * kLog2e;
@@ -1176,7 +1063,6 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<MT, KV8, SW>::CTAS) decode
             }
         }
     }
-    if constexpr (SHARED) pdl_wait();  // whoever waits for this grid waits for the one before it too
 }
 
 // One warp per output row (b*Q + t, h): weights the split partials by
@@ -1252,8 +1138,7 @@ struct DecodePlan {
 };
 
 static int plan_decode(int B, int Q, int Hqo, int Hkv, int D, int max_seq_len, int page_size,
-                       int window_left, DecodePlan &pl, bool kv8 = false, int first_tokens = 0,
-                       int min_chunk = 4 * kDecTile) {
+                       int window_left, DecodePlan &pl, bool kv8 = false, int first_tokens = 0) {
     if (B < 0 || Q < 1 || Hqo < 1 || Hkv < 1 || max_seq_len < 0 || window_left < -1 || first_tokens < 0)
         return PKV_ERR_INVALID_ARG;
     if (Hqo % Hkv) return PKV_ERR_INVALID_ARG;
@@ -1285,7 +1170,7 @@ static int plan_decode(int B, int Q, int Hqo, int Hkv, int D, int max_seq_len, i
     if (window_left >= 0 && span_t > chunk && span_t <= chunk + chunk / 4 && span_t <= kDecMaxChunk)
         chunk = static_cast<int>((span_t + kDecTile - 1) / kDecTile * kDecTile);
     const int64_t want = 2LL * num_sms();
-    while (chunk > min_chunk &&
+    while (chunk > 4 * kDecTile &&
            static_cast<int64_t>(B) * Hkv * ((span + chunk - 1) / chunk) < want)
         chunk = (chunk / 2 + kDecTile - 1) / kDecTile * kDecTile;  // (tile multiples)
     pl.chunk = chunk;
@@ -1303,12 +1188,12 @@ static int plan_decode(int B, int Q, int Hqo, int Hkv, int D, int max_seq_len, i
 }
 
 template <typename T, int MT, int LAYOUT, bool KV8, int SW = 0, int EXT = 0>
-static int launch_split(const DecParams<EXT> &p, dim3 grid, cudaStream_t st, bool pdl) {
+static int launch_split(const DecodeParams &p, dim3 grid, cudaStream_t st, bool pdl) {
     constexpr int ROWS = DecCfg<MT, KV8, SW>::ROWS, NKG = 4 / MT;
     constexpr int kDecStages = DecCfg<MT, KV8, SW>::STAGES;
     const size_t smem = kDecStages * DecSmem<KV8>::STAGE + ROWS * kDecRowBytes +
                         kDecStages * kDecTile + 2 * NKG * ROWS * sizeof(float) +
-                        (EXT == 1 || EXT == 2 ? p.pages_cap : kDecMaxPages) * sizeof(int) +
+                        (EXT ? p.pages_cap : kDecMaxPages) * sizeof(int) +
                         (EXT == 2 ? p.scales_cap * sizeof(float2) : 0);
     auto kern = decode_split_kernel<T, MT, LAYOUT, KV8, SW, EXT>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1320,7 +1205,7 @@ static int launch_split(const DecParams<EXT> &p, dim3 grid, cudaStream_t st, boo
 }
 
 template <typename T, int LAYOUT, bool KV8, int EXT = 0>
-static int launch_split_mt(int MT, const DecParams<EXT> &p, dim3 grid, cudaStream_t st, bool pdl) {
+static int launch_split_mt(int MT, const DecodeParams &p, dim3 grid, cudaStream_t st, bool pdl) {
     if constexpr (KV8) {
         if (p.R <= 8) return launch_split<T, 1, LAYOUT, true, 1, EXT>(p, grid, st, pdl);  // swapped operands
         if constexpr (EXT > 0) {
