@@ -56,6 +56,7 @@ struct SharedParams {
     int64_t pt_stride;
     int page_shift;
     int64_t max_num_pages;
+    int hnd, ratio;  // ratio (WIDE): (page, head) is row page * ratio + head of the cache's map
     float scale_log2;
     const float *bmm1_dev;
     unsigned long long wait_ns;
@@ -77,12 +78,15 @@ struct PrefixWalk {
     }
 };
 
-template <typename T, int LAYOUT, int NB>
+template <typename T, int NB, bool WIDE>
 __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const SharedParams p) {
     using C = ShCfg<NB>;
     constexpr int ST = C::STAGES, SW = C::SOFTMAX, THREADS = C::THREADS;
+    // a tile in shared memory: WIDE, groups of 8 keys, 64 dimensions of each
+    // then the other 64; else 64 dimensions of all keys, then the other 64
+    constexpr uint32_t HALF = WIDE ? 1024 : kShTileBytes / 2, GROUP8 = WIDE ? 2048 : 1024;
     constexpr uint32_t O_COL = NB * 128;  // TMEM: S of block x at 128 x, O at O_COL + 128 x
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -201,22 +205,24 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
             bool ok = true;
             segments([&](int tile, int s0, int n, int seg) {
                 const int32_t *pt = p.prefix_tables + static_cast<int64_t>(at.x.g) * p.pt_stride;
-                auto lookup = [&](int t) {  // lane i < nbox: page of box i of step t
-                    const int key = (at.k + t) * kShTile + lane * RB;
-                    int page = oob;
-                    if (lane < nbox && key < at.x.P && dbg_in(key >> p.page_shift, 1, (w.max_prefix + S - 1) >> p.page_shift, w.err)) {
-                        page = pt[key >> p.page_shift];
-                        if (page < 0 || page >= p.max_num_pages) {
-                            if (is_k) set_err(w.err, PKV_DEV_ERR_PAGE);
-                            page = oob;
-                        }
-                    }
-                    return page;
+                // pages of 32 boxes at a time, a lane each, the next 32 on the way
+                const int key0 = at.k * kShTile, P = at.x.P, head = at.head;
+                auto lookup = [&](int j0) {
+                    const int key = key0 + (j0 + lane) * RB;
+                    const bool read = key < P && dbg_in(key >> p.page_shift, 1, (w.max_prefix + S - 1) >> p.page_shift, w.err);
+                    return read ? pt[key >> p.page_shift] : -1;
                 };
-                int next = lookup(0);
+                int pages = -1, pages_next = lookup(0);
                 for (int t = 0; t < n; ++t) {
-                    const int pg = next;
-                    if (t + 1 < n) next = lookup(t + 1);
+                    const int j0 = (t * nbox) & 31;
+                    if (j0 == 0) {
+                        pages = pages_next;
+                        if (pages < 0 || pages >= p.max_num_pages) {
+                            if (is_k && key0 + (t * nbox + lane) * RB < min(P, key0 + n * kShTile)) set_err(w.err, PKV_DEV_ERR_PAGE);
+                            pages = oob;
+                        }
+                        if (t * nbox + 32 < n * nbox) pages_next = lookup(t * nbox + 32);
+                    }
                     const int i = s0 + t, st = i % ST, us = i / ST;
                     if (leader && us > 0 && !mbar_wait(is_k ? b_kempty(st) : b_vempty(st), (us - 1) & 1, abort_flag, wlim)) {
                         give_up();
@@ -228,16 +234,20 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
                     if (leader) mbar_expect_tx(full, kShTileBytes);
 #pragma unroll 1
                     for (int b = 0; b < nbox; ++b) {
-                        const int page = __shfl_sync(0xffffffffu, pg, b);
+                        const int page = __shfl_sync(0xffffffffu, pages, j0 + b);
                         if (!leader) continue;
-                        const int slot = ((at.k + t) * kShTile + b * RB) & (S - 1);
+                        const int slot = (key0 + t * kShTile + b * RB) & (S - 1);
                         if (kDebugBounds) {
                             dbg_in(page, 1, oob + 1, w.err);
                             dbg_in(slot, RB, S, w.err);
                         }
-                        for (int c = 0; c < 2; ++c)
-                            tma_load_4d(base + st * kShTileBytes + c * (kShTileBytes / 2) + b * RB * 128, tm, full, 64 * c,
-                                        LAYOUT == PKV_HND ? slot : at.head, LAYOUT == PKV_HND ? at.head : slot, page);
+                        const uint32_t dst = base + st * kShTileBytes + b * RB * (WIDE ? 256 : 128);
+                        if constexpr (WIDE) {
+                            tma_load_5d(dst, tm, full, 0, 0, 0, slot >> 3, page * p.ratio + head);
+                        } else {
+                            for (int c = 0; c < 2; ++c)
+                                tma_load_4d(dst + c * HALF, tm, full, 64 * c, p.hnd ? slot : head, p.hnd ? head : slot, page);
+                        }
                     }
                     if (leader) issued = i + 1;
                     if (!is_k || t > 0) continue;
@@ -255,7 +265,7 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
                     for (int x = 0; x < NB; ++x)
                         for (int c = 0; c < 2; ++c)
                             tma_load_3d(q_s + x * kShTileBytes + c * (kShTileBytes / 2), &tm_q, b_qfull, 64 * c,
-                                        at.head * w.group, tok0 + x * w.tok);
+                                        head * w.group, tok0 + x * w.tok);
                     queries = seg + 1;
                 }
                 return true;
@@ -279,14 +289,14 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
             };
             constexpr uint32_t idesc_qk = umma_idesc(128, kShTile, IsBf16<T>::value, false);
             constexpr uint32_t idesc_pv = umma_idesc(128, kShD, IsBf16<T>::value, true);
-            const uint64_t qdesc = umma_sdesc_sw128(q_s, 16, 1024), kdesc = umma_sdesc_sw128(k_s, 16, 1024);
-            const uint64_t vdesc = umma_sdesc_sw128(v_s, kShTileBytes / 2, 1024);
+            const uint64_t qdesc = umma_sdesc_sw128(q_s, 16, 1024), kdesc = umma_sdesc_sw128(k_s, 16, GROUP8);
+            const uint64_t vdesc = umma_sdesc_sw128(v_s, HALF, GROUP8);
             auto qk = [&](int x, int i) {  // S_x = Q_x K(i)^T, 16 dimensions a step
                 const uint64_t qd = qdesc + ((x * kShTileBytes) >> 4), kd = kdesc + (((i % ST) * kShTileBytes) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < kShD / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * (kShTileBytes / 2) + (kk & 3) * 32;
-                    if (leader) umma_ss(tmem + x * 128, qd + (off >> 4), kd + (off >> 4), idesc_qk, kk > 0 ? 1u : 0u);
+                    const uint32_t dim = (kk & 3) * 32, qo = (kk >> 2) * (kShTileBytes / 2) + dim, ko = (kk >> 2) * HALF + dim;
+                    if (leader) umma_ss(tmem + x * 128, qd + (qo >> 4), kd + (ko >> 4), idesc_qk, kk > 0 ? 1u : 0u);
                 }
                 commit(b_sfull(x));
             };
@@ -296,7 +306,7 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
                 for (int kk = 0; kk < kShTile / 16; ++kk)
                     if (leader)
                         umma_ts(tmem + O_COL + x * 128, tmem + x * 128 + 32 * (kk / 2) + 8 * (kk % 2),
-                                vd + ((kk * 16 * 128) >> 4), idesc_pv, more || kk > 0 ? 1u : 0u);
+                                vd + ((kk * 2 * GROUP8) >> 4), idesc_pv, more || kk > 0 ? 1u : 0u);
             };
             bool ok = true;
             segments([&](int tile, int s0, int n, int seg) {
@@ -416,7 +426,7 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
                     uint8_t *vbase = v_gen + (i0 % ST) * kShTileBytes;
                     for (int q = r; q < (kShTile - past) * 16; q += 128) {
                         const int row = past + (q >> 4), c = q & 15;
-                        *reinterpret_cast<uint4 *>(vbase + (c >> 3) * (kShTileBytes / 2) + row * 128 + (c & 7) * 16) =
+                        *reinterpret_cast<uint4 *>(vbase + (c >> 3) * HALF + (row >> 3) * GROUP8 + (row & 7) * 128 + (c & 7) * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
                     }
                     fence_proxy_async_smem();
@@ -483,6 +493,27 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
         tc_fence_after();
         tmem_dealloc(tmem, C::TMEM);
     }
+}
+
+// K or V cache as a 5-D map (64 dimensions, 8 slots, the two halves of a head,
+// groups of 8 slots, (page, head)), whose box, `rows` slots of one head, lands
+// as WIDE tiles have it: one copy where cache_tmap's 64-dimension boxes take
+// two.  Boxes of 16 slots: the copy engine took 1714 to 2400 cycles for a tile
+// of K in 16 of those, about as long as a step's MMAs.  Where the page stride
+// is no multiple of the unit that makes (page, head) one index, or the index
+// passes 31 bits, wide_ratio says 0 and the kernel takes the narrow boxes.
+static int wide_ratio(int layout, int S, int heads, int64_t page_stride, int64_t pages) {
+    const int64_t unit = layout == PKV_HND ? static_cast<int64_t>(S) * kShD : kShD;
+    const int64_t r = page_stride / unit;
+    return page_stride % unit || (pages + 2) * r + heads >= (1LL << 31) ? 0 : static_cast<int>(r);
+}
+static bool wide_tmap(CUtensorMap *m, const void *base, CUtensorMapDataType t, int layout, int S, int heads, int ratio,
+                      int64_t pages, int rows) {
+    const uint64_t row = layout == PKV_HND ? 256 : 256ull * heads, unit = layout == PKV_HND ? 256ull * S : 256;
+    const uint64_t dims[5] = {64, 8, 2, static_cast<uint64_t>(S / 8), static_cast<uint64_t>(pages * ratio)};
+    const uint64_t strides[4] = {row, 128, 8 * row, unit};
+    const uint32_t box[5] = {64, 8, 2, static_cast<uint32_t>(rows / 8), 1};
+    return encode_tmap(m, base, t, 5, dims, strides, box);
 }
 
 struct SharedPlan {
@@ -556,9 +587,9 @@ struct SharedMaps {
     CUtensorMap own_q, own_k, own_v;  // the own keys': queries of a request, the caches
 };
 
-template <typename T, int LAYOUT, int NB>
+template <typename T, int NB, bool WIDE>
 static int launch_prefix(const SharedMaps &m, const SharedParams &p, dim3 grid, cudaStream_t st) {
-    auto kern = shared_prefix_kernel<T, LAYOUT, NB>;
+    auto kern = shared_prefix_kernel<T, NB, WIDE>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(ShCfg<NB>::SMEM)) !=
         cudaSuccess)
         return PKV_ERR_CUDA;
@@ -588,12 +619,13 @@ static int launch_own(const SharedMaps &m, const OwnParams &p, dim3 grid, cudaSt
     return PKV_OK;
 }
 
-template <typename T, int LAYOUT>
+template <typename T>
 static int run_shared(const SharedMaps &m, const SharedParams &s, const OwnParams &p, const SharedPlan &pl, cudaStream_t st) {
     int launches = 2, rc = PKV_OK;
     if (pl.ctas > 0) {
-        rc = pl.nb == 2 ? launch_prefix<T, LAYOUT, 2>(m, s, dim3(pl.ctas), st)
-                        : launch_prefix<T, LAYOUT, 1>(m, s, dim3(pl.ctas), st);
+        const dim3 grid(pl.ctas);
+        rc = pl.nb == 2 ? (s.ratio ? launch_prefix<T, 2, true>(m, s, grid, st) : launch_prefix<T, 2, false>(m, s, grid, st))
+                        : (s.ratio ? launch_prefix<T, 1, true>(m, s, grid, st) : launch_prefix<T, 1, false>(m, s, grid, st));
         if (rc != PKV_OK) return rc;
         ++launches;
     }
@@ -680,6 +712,8 @@ extern "C" int paged_decode_shared(const void *query, const void *k_cache, const
     s.scale_log2 = bmm1_scale * kLog2e;
     s.bmm1_dev = bmm1_scale_dev;
     s.wait_ns = wait_limit_ns();
+    s.hnd = layout == PKV_HND;
+    s.ratio = wide_ratio(layout, page_size, num_kv_heads, page_stride, max_num_pages);
 
     OwnParams d = {};
     d.prefix = w;
@@ -719,9 +753,11 @@ extern "C" int paged_decode_shared(const void *query, const void *k_cache, const
     const int64_t pages = max_num_pages > 0 ? max_num_pages : 1;
     if (pl.ctas > 0) {
         const int box = pf_box_rows(page_size, kShTile);
-        if (!encode_tmap(&m.q, query, t, 3, dims, strides, block) ||
-            !cache_tmap(&m.k, k_cache, t, layout, kShD, page_size, num_kv_heads, page_stride, pages, box) ||
-            !cache_tmap(&m.v, v_cache, t, layout, kShD, page_size, num_kv_heads, page_stride, pages, box))
+        auto cache = [&](CUtensorMap *x, const void *base) {
+            return s.ratio ? wide_tmap(x, base, t, layout, page_size, num_kv_heads, s.ratio, pages, box)
+                           : cache_tmap(x, base, t, layout, kShD, page_size, num_kv_heads, page_stride, pages, box);
+        };
+        if (!encode_tmap(&m.q, query, t, 3, dims, strides, block) || !cache(&m.k, k_cache) || !cache(&m.v, v_cache))
             return PKV_ERR_CUDA;
     }
     const int box = pf_box_rows(page_size, kOwnTile);
@@ -730,8 +766,5 @@ extern "C" int paged_decode_shared(const void *query, const void *k_cache, const
         !own_tmap(&m.own_v, v_cache, t, layout, page_size, num_kv_heads, page_stride, pages, box))
         return PKV_ERR_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dtype == PKV_BF16)
-        return layout == PKV_HND ? run_shared<__nv_bfloat16, PKV_HND>(m, s, d, pl, st)
-                                 : run_shared<__nv_bfloat16, PKV_NHD>(m, s, d, pl, st);
-    return layout == PKV_HND ? run_shared<__half, PKV_HND>(m, s, d, pl, st) : run_shared<__half, PKV_NHD>(m, s, d, pl, st);
+    return dtype == PKV_BF16 ? run_shared<__nv_bfloat16>(m, s, d, pl, st) : run_shared<__half>(m, s, d, pl, st);
 }
