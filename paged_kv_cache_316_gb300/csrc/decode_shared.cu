@@ -43,9 +43,9 @@ template <int NB>
 struct ShCfg {
     static constexpr int SOFTMAX = 4 * NB;                        // softmax warps
     static constexpr int THREADS = 32 * (SOFTMAX + 4);
-    static constexpr int STAGES = NB == 2 ? 2 : 3;                // of K and of V
+    static constexpr int KST = 3, VST = NB == 2 ? 2 : 3;          // ring stages of K and of V
     static constexpr uint32_t TMEM = NB == 2 ? 512 : 256;         // columns
-    static constexpr uint32_t SMEM = 1024 + (NB + 2 * STAGES) * kShTileBytes + 8 * (2 + 4 * STAGES + 3 * NB + 1);
+    static constexpr uint32_t SMEM = 1024 + (NB + KST + VST) * kShTileBytes + 8 * (3 + 2 * (KST + VST) + 3 * NB);
 };
 // Two blocks: registers as in the prefill kernel (launched with 384 x 168).
 constexpr int kShRegsLow = 104, kShRegsHigh = 200;
@@ -83,25 +83,25 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const SharedParams p) {
     using C = ShCfg<NB>;
-    constexpr int ST = C::STAGES, SW = C::SOFTMAX, THREADS = C::THREADS;
+    constexpr int KST = C::KST, VST = C::VST, SW = C::SOFTMAX, THREADS = C::THREADS;
     // a tile in shared memory: WIDE, groups of 8 keys, 64 dimensions of each
     // then the other 64; else 64 dimensions of all keys, then the other 64
     constexpr uint32_t HALF = WIDE ? 1024 : kShTileBytes / 2, GROUP8 = WIDE ? 2048 : 1024;
     constexpr uint32_t O_COL = NB * 128;  // TMEM: S of block x at 128 x, O at O_COL + 128 x
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const uint32_t q_s = smem_u32(smem), k_s = q_s + NB * kShTileBytes, v_s = k_s + ST * kShTileBytes;
-    uint8_t *v_gen = smem + (NB + ST) * kShTileBytes;
-    const uint32_t bar0 = v_s + ST * kShTileBytes;
+    const uint32_t q_s = smem_u32(smem), k_s = q_s + NB * kShTileBytes, v_s = k_s + KST * kShTileBytes;
+    uint8_t *v_gen = smem + (NB + KST) * kShTileBytes;
+    const uint32_t bar0 = v_s + VST * kShTileBytes;
     const uint32_t b_qfull = bar0, b_qempty = bar0 + 8;
     auto b_kfull = [&](int s) { return bar0 + 8u * (2 + s); };
-    auto b_kempty = [&](int s) { return bar0 + 8u * (2 + ST + s); };
-    auto b_vfull = [&](int s) { return bar0 + 8u * (2 + 2 * ST + s); };
-    auto b_vempty = [&](int s) { return bar0 + 8u * (2 + 3 * ST + s); };
-    auto b_sfull = [&](int x) { return bar0 + 8u * (2 + 4 * ST + x); };
-    auto b_pfull = [&](int x) { return bar0 + 8u * (2 + 4 * ST + NB + x); };
-    auto b_odone = [&](int x) { return bar0 + 8u * (2 + 4 * ST + 2 * NB + x); };
-    const uint32_t b_drain = bar0 + 8u * (2 + 4 * ST + 3 * NB);
+    auto b_kempty = [&](int s) { return bar0 + 8u * (2 + KST + s); };
+    auto b_vfull = [&](int s) { return bar0 + 8u * (2 + 2 * KST + s); };
+    auto b_vempty = [&](int s) { return bar0 + 8u * (2 + 2 * KST + VST + s); };
+    auto b_sfull = [&](int x) { return bar0 + 8u * (2 + 2 * (KST + VST) + x); };
+    auto b_pfull = [&](int x) { return bar0 + 8u * (2 + 2 * (KST + VST) + NB + x); };
+    auto b_odone = [&](int x) { return bar0 + 8u * (2 + 2 * (KST + VST) + 2 * NB + x); };
+    const uint32_t b_drain = bar0 + 8u * (2 + 2 * (KST + VST) + 3 * NB);
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_s, steps_s;
     __shared__ PrefixWalk walk_s[THREADS / 32];
@@ -157,9 +157,11 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
     if (tid == 0) {
         mbar_init(b_qfull, 1);
         mbar_init(b_qempty, 1);
-        for (int s = 0; s < ST; ++s) {
+        for (int s = 0; s < KST; ++s) {
             mbar_init(b_kfull(s), 1);
             mbar_init(b_kempty(s), 1);
+        }
+        for (int s = 0; s < VST; ++s) {
             mbar_init(b_vfull(s), 1);
             mbar_init(b_vempty(s), 1);
         }
@@ -187,13 +189,14 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
         set_err(w.err, PKV_DEV_ERR_TIMEOUT);
     };
     // Phases, counted over all of the CTA's steps i and segments: K / V stage of
-    // step i: i / ST; sfull / pfull of a block: i; Q and odone: the segment.
+    // step i: i / KST, i / VST; sfull / pfull of a block: i; Q and odone: the segment.
     // Every wait is for the newest phase that can be pending.
     if (warp >= SW) {
         if constexpr (NB == 2) reg_dealloc<kShRegsLow>();
         if (warp == SW || warp == SW + 2) {
             // ---- TMA: Q and K (warp SW), V (warp SW + 2)
             const bool is_k = warp == SW;
+            const int ST = is_k ? KST : VST;
             const bool leader = elect_one();
             const int leader_lane = __ffs(__ballot_sync(0xffffffffu, leader)) - 1;
             const CUtensorMap *tm = is_k ? &tm_k : &tm_v;
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
             const uint64_t qdesc = umma_sdesc_sw128(q_s, 16, 1024), kdesc = umma_sdesc_sw128(k_s, 16, GROUP8);
             const uint64_t vdesc = umma_sdesc_sw128(v_s, HALF, GROUP8);
             auto qk = [&](int x, int i) {  // S_x = Q_x K(i)^T, 16 dimensions a step
-                const uint64_t qd = qdesc + ((x * kShTileBytes) >> 4), kd = kdesc + (((i % ST) * kShTileBytes) >> 4);
+                const uint64_t qd = qdesc + ((x * kShTileBytes) >> 4), kd = kdesc + (((i % KST) * kShTileBytes) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < kShD / 16; ++kk) {
                     const uint32_t dim = (kk & 3) * 32, qo = (kk >> 2) * (kShTileBytes / 2) + dim, ko = (kk >> 2) * HALF + dim;
@@ -301,7 +304,7 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
                 commit(b_sfull(x));
             };
             auto pv = [&](int x, int i, bool more) {  // O_x (+)= P_x V(i), 16 keys a step
-                const uint64_t vd = vdesc + (((i % ST) * kShTileBytes) >> 4);
+                const uint64_t vd = vdesc + (((i % VST) * kShTileBytes) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < kShTile / 16; ++kk)
                     if (leader)
@@ -310,30 +313,37 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
             };
             bool ok = true;
             segments([&](int tile, int s0, int n, int seg) {
-                ok = mwait(b_qfull, seg & 1) && mwait(b_kfull(s0 % ST), (s0 / ST) & 1);
+                ok = mwait(b_qfull, seg & 1) && mwait(b_kfull(s0 % KST), (s0 / KST) & 1);
                 if (!ok) return false;
                 tc_fence_after();
                 // (S_x is free: the PV that read P_x from it was issued before)
                 for (int x = 0; x < NB; ++x) qk(x, s0);
-                commit(b_kempty(s0 % ST));
+                commit(b_kempty(s0 % KST));
                 if (n == 1) commit(b_qempty);
                 for (int t = 0; t < n; ++t) {
                     const int i = s0 + t;
                     const bool more = t + 1 < n;
-                    ok = mwait(b_vfull(i % ST), (i / ST) & 1) &&
-                         (!more || mwait(b_kfull((i + 1) % ST), ((i + 1) / ST) & 1));
+                    ok = mwait(b_vfull(i % VST), (i / VST) & 1);
                     if (!ok) return false;
                     for (int x = 0; x < NB; ++x) {
                         ok = mwait(b_pfull(x), i & 1);
                         if (!ok) return false;
                         tc_fence_after();
                         pv(x, i, t > 0);  // (a segment's first overwrites O_x, drained before its P came)
-                        if (!more) commit(b_odone(x));
-                        else qk(x, i + 1);
+                        if (x == NB - 1) commit(b_vempty(i % VST));
+                        if (!more) {
+                            commit(b_odone(x));
+                            continue;
+                        }
+                        if (x == 0) {
+                            ok = mwait(b_kfull((i + 1) % KST), ((i + 1) / KST) & 1);
+                            if (!ok) return false;
+                            tc_fence_after();
+                        }
+                        qk(x, i + 1);
                     }
-                    if (more) commit(b_kempty((i + 1) % ST));
+                    if (more) commit(b_kempty((i + 1) % KST));
                     if (t + 2 == n) commit(b_qempty);
-                    commit(b_vempty(i % ST));
                 }
                 return true;
             });
@@ -422,8 +432,8 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
                 // rows of V that are no key of the prefix may hold anything: zeroed by
                 // block A, so that P = 0 there cannot produce 0 * NaN
                 if (X == 0 && past < kShTile) {
-                    if (!wait_warp(b_vfull(i0 % ST), (i0 / ST) & 1)) return ok = false;
-                    uint8_t *vbase = v_gen + (i0 % ST) * kShTileBytes;
+                    if (!wait_warp(b_vfull(i0 % VST), (i0 / VST) & 1)) return ok = false;
+                    uint8_t *vbase = v_gen + (i0 % VST) * kShTileBytes;
                     for (int q = r; q < (kShTile - past) * 16; q += 128) {
                         const int row = past + (q >> 4), c = q & 15;
                         *reinterpret_cast<uint4 *>(vbase + (c >> 3) * HALF + (row >> 3) * GROUP8 + (row & 7) * 128 + (c & 7) * 16) =
