@@ -18,7 +18,7 @@
 // the softmax, one thread a row: scores read from TMEM once, running maximum
 // in base 2 that rises only where a tile's exceeds it by more than 2^8, P
 // written as 16-bit pairs over the consumed scores, the A operand of the PV
-// MMA.  Then a TMA warp for Q and K, the MMA warp, a TMA warp for V, and an
+// MMA, whose first half of the keys begins while the second's P is made.  Then a TMA warp for Q and K, the MMA warp, a TMA warp for V, and an
 // idle one.  With two blocks the MMAs alternate (QK_A QK_B, then PV_A(t)
 // QK_A(t+1) PV_B(t) QK_B(t+1)), so that the tensor core works for one block
 // while the softmax of the other runs.  The K / V ring runs on from one item
@@ -45,7 +45,7 @@ struct ShCfg {
     static constexpr int THREADS = 32 * (SOFTMAX + 4);
     static constexpr int KST = 3, VST = NB == 2 ? 2 : 3;          // ring stages of K and of V
     static constexpr uint32_t TMEM = NB == 2 ? 512 : 256;         // columns
-    static constexpr uint32_t SMEM = 1024 + (NB + KST + VST) * kShTileBytes + 8 * (3 + 2 * (KST + VST) + 3 * NB);
+    static constexpr uint32_t SMEM = 1024 + (NB + KST + VST) * kShTileBytes + 8 * (3 + 2 * (KST + VST) + 4 * NB);
 };
 // Two blocks: registers as in the prefill kernel (launched with 384 x 168).
 constexpr int kShRegsLow = 104, kShRegsHigh = 200;
@@ -99,9 +99,9 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
     auto b_vfull = [&](int s) { return bar0 + 8u * (2 + 2 * KST + s); };
     auto b_vempty = [&](int s) { return bar0 + 8u * (2 + 2 * KST + VST + s); };
     auto b_sfull = [&](int x) { return bar0 + 8u * (2 + 2 * (KST + VST) + x); };
-    auto b_pfull = [&](int x) { return bar0 + 8u * (2 + 2 * (KST + VST) + NB + x); };
-    auto b_odone = [&](int x) { return bar0 + 8u * (2 + 2 * (KST + VST) + 2 * NB + x); };
-    const uint32_t b_drain = bar0 + 8u * (2 + 2 * (KST + VST) + 3 * NB);
+    auto b_pfull = [&](int x, int half) { return bar0 + 8u * (2 + 2 * (KST + VST) + NB + 2 * x + half); };
+    auto b_odone = [&](int x) { return bar0 + 8u * (2 + 2 * (KST + VST) + 3 * NB + x); };
+    const uint32_t b_drain = bar0 + 8u * (2 + 2 * (KST + VST) + 4 * NB);
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_s, steps_s;
     __shared__ PrefixWalk walk_s[THREADS / 32];
@@ -167,7 +167,8 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
         }
         for (int x = 0; x < NB; ++x) {
             mbar_init(b_sfull(x), 1);
-            mbar_init(b_pfull(x), 128);
+            mbar_init(b_pfull(x, 0), 128);
+            mbar_init(b_pfull(x, 1), 128);
             mbar_init(b_odone(x), 1);
         }
         mbar_init(b_drain, 1);
@@ -303,10 +304,10 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
                 }
                 commit(b_sfull(x));
             };
-            auto pv = [&](int x, int i, bool more) {  // O_x (+)= P_x V(i), 16 keys a step
+            auto pv = [&](int x, int i, int half, bool more) {  // O_x (+)= P_x V(i) of 64 keys, 16 a step
                 const uint64_t vd = vdesc + (((i % VST) * kShTileBytes) >> 4);
 #pragma unroll
-                for (int kk = 0; kk < kShTile / 16; ++kk)
+                for (int kk = half * (kShTile / 32); kk < (half + 1) * (kShTile / 32); ++kk)
                     if (leader)
                         umma_ts(tmem + O_COL + x * 128, tmem + x * 128 + 32 * (kk / 2) + 8 * (kk % 2),
                                 vd + ((kk * 2 * GROUP8) >> 4), idesc_pv, more || kk > 0 ? 1u : 0u);
@@ -326,10 +327,12 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
                     ok = mwait(b_vfull(i % VST), (i / VST) & 1);
                     if (!ok) return false;
                     for (int x = 0; x < NB; ++x) {
-                        ok = mwait(b_pfull(x), i & 1);
-                        if (!ok) return false;
-                        tc_fence_after();
-                        pv(x, i, t > 0);  // (a segment's first overwrites O_x, drained before its P came)
+                        for (int half = 0; half < 2; ++half) {
+                            ok = mwait(b_pfull(x, half), i & 1);
+                            if (!ok) return false;
+                            tc_fence_after();
+                            pv(x, i, half, t > 0 || half > 0);  // (a segment's first overwrites O_x, drained before its P came)
+                        }
                         if (x == NB - 1) commit(b_vempty(i % VST));
                         if (!more) {
                             commit(b_odone(x));
@@ -411,24 +414,6 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
                     m = top;
                     l *= alpha;
                 }
-                const float base = m == -INFINITY ? 0.f : m;
-                const float2 shift = make_float2(-base, -base);
-                float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t pw[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float2 x = __ffma2_rn(
-                            make_float2(__uint_as_float(rs[i][2 * e]), __uint_as_float(rs[i][2 * e + 1])), mul, shift);
-                        const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
-                        if (e & 1) lb = __fadd2_rn(lb, make_float2(p0, p1));
-                        else la = __fadd2_rn(la, make_float2(p0, p1));
-                        pw[e] = pack2<T>(p0, p1);
-                    }
-                    tmem_st16(s_addr + 32 * i, pw);
-                }
-                l += (la.x + la.y) + (lb.x + lb.y);
                 // rows of V that are no key of the prefix may hold anything: zeroed by
                 // block A, so that P = 0 there cannot produce 0 * NaN
                 if (X == 0 && past < kShTile) {
@@ -453,9 +438,29 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
                         tmem_st32(o_addr + c * 32, ro);
                     }
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(b_pfull(X));
+                const float base = m == -INFINITY ? 0.f : m;
+                const float2 shift = make_float2(-base, -base);
+                float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t pw[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 x = __ffma2_rn(
+                            make_float2(__uint_as_float(rs[i][2 * e]), __uint_as_float(rs[i][2 * e + 1])), mul, shift);
+                        const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
+                        if (e & 1) lb = __fadd2_rn(lb, make_float2(p0, p1));
+                        else la = __fadd2_rn(la, make_float2(p0, p1));
+                        pw[e] = pack2<T>(p0, p1);
+                    }
+                    tmem_st16(s_addr + 32 * i, pw);
+                    if (i & 1) {  // half of the keys: their product may begin
+                        tmem_wait_st();
+                        tc_fence_before();
+                        mbar_arrive(b_pfull(X, i >> 1));
+                    }
+                }
+                l += (la.x + la.y) + (lb.x + lb.y);
             }
             if (!wait_warp(b_odone(X), seg & 1)) return ok = false;
             tc_fence_after();
