@@ -110,7 +110,36 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
 
     // the own keys' grid may start as soon as every CTA of this one has
     pdl_launch_dependents();
-    if (warp == 0) {
+    if (warp == SW + 1) {
+        tmem_alloc(smem_u32(&tmem_base_s), C::TMEM);
+        tmem_relinquish();
+        tc_fence_before();
+    } else if (warp == SW) {
+        if (lane == 0) {
+            prefetch_tmap(&tm_q);
+            prefetch_tmap(&tm_k);
+            prefetch_tmap(&tm_v);
+            mbar_init(b_qfull, 1);
+            mbar_init(b_qempty, 1);
+            for (int s = 0; s < KST; ++s) {
+                mbar_init(b_kfull(s), 1);
+                mbar_init(b_kempty(s), 1);
+            }
+            for (int s = 0; s < VST; ++s) {
+                mbar_init(b_vfull(s), 1);
+                mbar_init(b_vempty(s), 1);
+            }
+            for (int x = 0; x < NB; ++x) {
+                mbar_init(b_sfull(x), 1);
+                mbar_init(b_pfull(x, 0), 128);
+                mbar_init(b_pfull(x, 1), 128);
+                mbar_init(b_odone(x), 1);
+            }
+            mbar_init(b_drain, 1);
+            abort_s = 0;
+            fence_mbar_init();
+        }
+    } else if (warp == 0) {
         PrefixWalk at;
         bool bad;
         const uint32_t W = scan_prefixes(w, [](int, int, uint32_t, uint32_t) { return false; }, at.x, bad);
@@ -133,8 +162,13 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
         }
     }
     __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_s;
     const int steps = steps_s;
-    if (steps == 0) return;  // uniform over the CTA
+    if (steps == 0) {  // uniform over the CTA
+        if (warp == SW + 1) tmem_dealloc(tmem, C::TMEM);
+        return;
+    }
     PrefixWalk &at = walk_s[warp];
     const int member = static_cast<int>(blockIdx.x) % w.team;
     // f(the CTA's tile of the item, its first step counted over the CTA's
@@ -154,35 +188,6 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
         }
     };
 
-    if (tid == 0) {
-        mbar_init(b_qfull, 1);
-        mbar_init(b_qempty, 1);
-        for (int s = 0; s < KST; ++s) {
-            mbar_init(b_kfull(s), 1);
-            mbar_init(b_kempty(s), 1);
-        }
-        for (int s = 0; s < VST; ++s) {
-            mbar_init(b_vfull(s), 1);
-            mbar_init(b_vempty(s), 1);
-        }
-        for (int x = 0; x < NB; ++x) {
-            mbar_init(b_sfull(x), 1);
-            mbar_init(b_pfull(x, 0), 128);
-            mbar_init(b_pfull(x, 1), 128);
-            mbar_init(b_odone(x), 1);
-        }
-        mbar_init(b_drain, 1);
-        abort_s = 0;
-        fence_mbar_init();
-    }
-    if (warp == SW + 1) {
-        tmem_alloc(smem_u32(&tmem_base_s), C::TMEM);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = tmem_base_s;
     volatile int *abort_flag = &abort_s;
     const uint64_t wlim = p.wait_ns;
     auto give_up = [&]() {
@@ -202,7 +207,6 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
             const int leader_lane = __ffs(__ballot_sync(0xffffffffu, leader)) - 1;
             const CUtensorMap *tm = is_k ? &tm_k : &tm_v;
             const uint32_t base = is_k ? k_s : v_s;
-            if (leader) prefetch_tmap(tm);
             const int S = 1 << p.page_shift, RB = pf_box_rows(S, kShTile), nbox = kShTile / RB;
             const int oob = max(static_cast<int>(p.max_num_pages), 1);  // past the map: zero fill
             int issued = 0, queries = 0;  // (leader) steps, segments with copies issued
@@ -648,7 +652,7 @@ static int run_shared(const SharedMaps &m, const SharedParams &s, const OwnParam
     rc = pl.MT == 1 ? launch_own<T, 1>(m, p, grid, st)
                     : (pl.MT == 2 ? launch_own<T, 2>(m, p, grid, st) : launch_own<T, 4>(m, p, grid, st));
     if (rc != PKV_OK) return rc;
-    const int64_t warps = (pl.rows + p.merge_rows - 1) / p.merge_rows;
+    const int64_t warps = pl.rows / p.prefix.group * ((p.prefix.group + p.merge_rows - 1) / p.merge_rows);
     if (launch_dependent(shared_merge_kernel<T>, dim3(static_cast<unsigned>((warps + 3) / 4)), dim3(128), 0, st, p) !=
         cudaSuccess)
         return PKV_ERR_CUDA;
@@ -751,9 +755,9 @@ extern "C" int paged_decode_shared(const void *query, const void *k_cache, const
     d.ws_o = reinterpret_cast<float *>(ws + pl.own_o);
     d.ws_lse = reinterpret_cast<float *>(ws + pl.own_lse);
     d.ws_rows = static_cast<int64_t>(batch_size) * num_kv_heads * pl.n_split_max * pl.R;
-    // (a warp for a row until every SM has 28 of them, then one for up to 8)
+    // (a warp for a row until every SM has 28 of them)
     const int64_t fill = (pl.rows + 28 * num_sms() - 1) / (28 * num_sms());
-    d.merge_rows = static_cast<int>(fill < 8 ? fill : 8);
+    d.merge_rows = static_cast<int>(fill < w.group ? fill : w.group);
     d.err = err_word;
     d.wait_ns = s.wait_ns;
 
