@@ -142,14 +142,20 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
     } else if (warp == 0) {
         PrefixWalk at;
         bool bad;
-        const uint32_t W = scan_prefixes(w, [](int, int, uint32_t, uint32_t) { return false; }, at.x, bad);
-        const uint32_t per = prefix_steps_per_team(w, W), w0 = blockIdx.x / w.team * per;
+        const uint32_t team = blockIdx.x / w.team;
+        const uint32_t W = scan_prefixes(
+            w,
+            [&](uint32_t all, int, int, uint32_t first, uint32_t n) {
+                const uint32_t w0 = team * prefix_steps_per_team(w, all);
+                return w0 >= first && w0 - first < n;
+            },
+            at.x, bad);
+        const uint32_t per = prefix_steps_per_team(w, W), w0 = team * per;
         if (blockIdx.x == 0) {
             if (bad && lane == 0) set_err(w.err, PKV_DEV_ERR_BATCH);
             for (int g = lane; g < w.G && !bad; g += 32)
                 if (w.prefix_lens[g] < 0 || w.prefix_lens[g] > w.max_prefix) set_err(w.err, PKV_DEV_ERR_LEN);
         }
-        if (w0 < W) scan_prefixes(w, [=](int, int, uint32_t s, uint32_t n) { return w0 >= s && w0 - s < n; }, at.x, bad);
         if (lane == 0) {
             steps_s = w0 < W ? static_cast<int>(min(per, W - w0)) : 0;
             if (w0 < W) {
@@ -476,26 +482,23 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
                 row = at.k == 0 ? static_cast<int64_t>(token) * w.Hqo + at.head * w.group + h
                                 : w.rows + (static_cast<int64_t>(blockIdx.x) * NB + X) * 128 + r;
             const float inv = l > 0.f ? 1.f / l : (l != l ? l : 0.f);
-            int64_t quad[4];  // of the rows of this lane's four
-#pragma unroll
-            for (int i = 0; i < 4; ++i) quad[i] = __shfl_sync(0xffffffffu, row, (lane & ~3) + i);
+            // written from accumulator fragments: four lanes write 32 bytes of a row
 #pragma unroll 1
-            for (int c = 0; c < kShD / 32; ++c) {
+            for (int c = 0; c < 4; ++c) {  // rows 16 (c / 2) and on, columns 64 (c % 2) and on
                 uint32_t ro[32];
-                tmem_ld32(o_addr + c * 32, ro);
+                tmem_ld16x256(o_addr + (static_cast<uint32_t>(16 * (c >> 1)) << 16) + 64 * (c & 1), ro);
                 tmem_wait_ld_regs(ro);
 #pragma unroll
-                for (int h2 = 0; h2 < 2; ++h2) {  // four lanes trade pieces: a store writes 64 bytes of a row
-                    uint32_t v[4][4];
+                for (int f = 0; f < 2; ++f) {
+                    const int from = 16 * (c >> 1) + 8 * f + (lane >> 2);
+                    const int64_t to = __shfl_sync(0xffffffffu, row, from);
+                    const float mul = __shfl_sync(0xffffffffu, inv, from);
+                    if (to < 0 || !dbg_in(to, 1, w.parts, w.err)) continue;
+                    float *dst = w.ws_o + to * kShD + 64 * (c & 1) + 2 * (lane & 3);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        v[e >> 2][e & 3] = __float_as_uint(__uint_as_float(ro[16 * h2 + e]) * inv);
-                    transpose4(v);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (quad[i] >= 0 && dbg_in(quad[i], 1, w.parts, w.err))
-                            *reinterpret_cast<uint4 *>(w.ws_o + quad[i] * kShD + c * 32 + h2 * 16 + (lane & 3) * 4) =
-                                make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<float2 *>(dst + 8 * i) =
+                            make_float2(__uint_as_float(ro[4 * i + 2 * f]) * mul, __uint_as_float(ro[4 * i + 2 * f + 1]) * mul);
                 }
             }
             if (valid && dbg_in(row, 1, w.parts, w.err))

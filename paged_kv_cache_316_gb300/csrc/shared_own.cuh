@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const __grid_constant
     const int token = unit / w.Hkv, kvh = unit - token * w.Hkv, b = token / w.Q, t = token - b * w.Q;
     PrefixGroup x;
     bool bad;
-    const uint32_t W = scan_prefixes(w, [=](int lo, int hi, uint32_t, uint32_t) { return lo <= b && b < hi; }, x, bad);
+    const uint32_t W = scan_prefixes(w, [=](uint32_t, int lo, int hi, uint32_t, uint32_t) { return lo <= b && b < hi; }, x, bad);
     const int n_own = own_splits(static_cast<int>(min(p.seq_lens[b], static_cast<uint32_t>(p.max_seq_len))), p.chunk);
     const PrefixParts parts = prefix_parts(w, x, prefix_steps_per_team(w, W), token, kvh * w.group, kvh);
     const int64_t own0 = own_part(p, b, kvh, 0, t * w.group);

@@ -58,49 +58,59 @@ __device__ __forceinline__ void read_prefix_group(const PrefixWork &p, int g, Pr
 }
 
 // All groups, by one warp: returns W and, in `found`, the group for which
-// match(a, b, first step, steps) holds (g = -1: none).  Where group_indptr is
-// not in order no group has work (*bad).
+// match(W, a, b, first step, steps) holds (g = -1: none).  Where group_indptr
+// is not in order no group has work (*bad).  Up to 32 groups are read once,
+// more of them twice.
 template <typename F>
 __device__ __forceinline__ uint32_t scan_prefixes(const PrefixWork &p, F match, PrefixGroup &found, bool &bad) {
     const int lane = threadIdx.x & 31;
-    uint32_t carry = 0;
+    uint32_t W = 0;
     found.g = -1;
     bad = false;
-    for (int g0 = 0; g0 < p.G; g0 += 32) {
-        const int g = g0 + lane;
-        PrefixGroup x = {};
-        bool wrong = false;
-        if (g < p.G) {
-            read_prefix_group(p, g, x);
-            wrong = x.a < 0 || x.b < x.a || x.b > p.B || (g == 0 && x.a != 0);
-        }
-        if (__any_sync(0xffffffffu, wrong)) bad = true;
-        const uint32_t n = g < p.G && !bad ? static_cast<uint32_t>(x.items) * p.Hkv * x.nk : 0u;
-        uint32_t sum = n;
+    PrefixGroup x = {};
+    uint32_t n = 0, sum = 0;  // steps of this lane's group; of it and the lanes before
+    for (int pass = p.G <= 32 ? 1 : 0; pass < 2; ++pass) {
+        uint32_t carry = 0;
+        for (int g0 = 0; g0 < p.G; g0 += 32) {
+            const int g = g0 + lane;
+            bool wrong = false;
+            if (g < p.G) {
+                read_prefix_group(p, g, x);
+                wrong = x.a < 0 || x.b < x.a || x.b > p.B || (g == 0 && x.a != 0);
+            }
+            if (__any_sync(0xffffffffu, wrong)) bad = true;
+            if (bad) break;
+            sum = n = g < p.G ? static_cast<uint32_t>(x.items) * p.Hkv * x.nk : 0u;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += y;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += y;
+            }
+            const uint32_t all = __shfl_sync(0xffffffffu, sum, 31);
+            if (p.G <= 32) W = all;
+            if (pass == 1) {
+                const unsigned m = __ballot_sync(0xffffffffu, g < p.G && match(W, x.a, x.b, carry + sum - n, n));
+                if (m && found.g < 0) {
+                    const int j = __ffs(m) - 1;
+                    found.g = g0 + j;
+                    found.a = __shfl_sync(0xffffffffu, x.a, j);
+                    found.b = __shfl_sync(0xffffffffu, x.b, j);
+                    found.P = __shfl_sync(0xffffffffu, x.P, j);
+                    found.nk = __shfl_sync(0xffffffffu, x.nk, j);
+                    found.tiles = __shfl_sync(0xffffffffu, x.tiles, j);
+                    found.items = __shfl_sync(0xffffffffu, x.items, j);
+                    found.base = carry + __shfl_sync(0xffffffffu, sum - n, j);
+                }
+            }
+            carry += all;
         }
-        const unsigned m = __ballot_sync(0xffffffffu, g < p.G && match(x.a, x.b, carry + sum - n, n));
-        if (m && found.g < 0) {
-            const int j = __ffs(m) - 1;
-            found.g = g0 + j;
-            found.a = __shfl_sync(0xffffffffu, x.a, j);
-            found.b = __shfl_sync(0xffffffffu, x.b, j);
-            found.P = __shfl_sync(0xffffffffu, x.P, j);
-            found.nk = __shfl_sync(0xffffffffu, x.nk, j);
-            found.tiles = __shfl_sync(0xffffffffu, x.tiles, j);
-            found.items = __shfl_sync(0xffffffffu, x.items, j);
-            found.base = carry + __shfl_sync(0xffffffffu, sum - n, j);
+        if (bad) {
+            found.g = -1;
+            return 0;
         }
-        carry += __shfl_sync(0xffffffffu, sum, 31);
+        W = carry;
     }
-    if (bad) {
-        found.g = -1;
-        return 0;
-    }
-    return carry;
+    return W;
 }
 
 // Steps of a team: all share the work evenly, but none takes fewer than
