@@ -8,6 +8,7 @@ library has not been built, every call raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 import os
@@ -422,37 +423,53 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling=None, fac
 
 
 def _token_rows(t, name: str):
-    """(heads, head_dim, elements from token to token) of [tokens, heads,
-    head_dim] whose heads are contiguous."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or (shape[2] > 1 and stride[2] != 1) or (shape[1] > 1 and stride[1] != shape[2]):
-        raise PagedKVError(f"{name} must be [tokens, heads, head_dim] with contiguous heads")
-    return shape[1], shape[2], stride[0] if shape[0] > 1 else max(stride[0], shape[1] * shape[2])
+    """(tokens, heads, head_dim, elements from token to token) of [tokens,
+    heads, head_dim] whose heads are contiguous."""
+    shape = t.shape
+    if len(shape) == 3:
+        n, H, D = shape
+        if t.is_contiguous():
+            return n, H, D, H * D
+        stride = t.stride()
+        if (D == 1 or stride[2] == 1) and (H == 1 or stride[1] == D):
+            return n, H, D, stride[0] if n > 1 else max(stride[0], H * D)
+    raise PagedKVError(f"{name} must be [tokens, heads, head_dim] with contiguous heads")
+
+
+def _int32_of(t, n: int, name: str):
+    if t.dtype != torch.int32 or t.numel() < n or not t.is_contiguous():
+        raise PagedKVError(f"{name} must be contiguous int32 with >= {n} entries")
+    return t.data_ptr()
 
 
 def _rotary_args(query, key, positions, frequencies, query_weight, key_weight, query_out):
     """The checks that paged_rotary and paged_append_rotary share: (tokens, q
-    heads, kv heads, head_dim, strides, rotary_dim, query_out, dtype)."""
-    Hq, D, qs = _token_rows(query, "query")
-    Hkv, Dk, ks = _token_rows(key, "key")
-    n = query.shape[0]
-    if key.shape[0] != n or Dk != D:
+    heads, kv heads, head_dim, strides, rotary_dim, query_out, dtype, the
+    weights' addresses)."""
+    n, Hq, D, qs = _token_rows(query, "query")
+    nk, Hkv, Dk, ks = _token_rows(key, "key")
+    if nk != n or Dk != D:
         raise PagedKVError("query and key have the same tokens and head_dim")
+    kind = query.dtype
     dtype = _dtype_code(query)
-    if dtype > BF16 or key.dtype != query.dtype:
+    if dtype > BF16 or key.dtype != kind:
         raise PagedKVError("query and key are both fp16 or both bf16")
-    if positions.dtype != torch.int32 or positions.numel() < n or not positions.is_contiguous():
-        raise PagedKVError(f"positions must be contiguous int32 with >= {n} entries")
     if frequencies.dtype != torch.float64 or frequencies.dim() != 1 or not frequencies.is_contiguous():
         raise PagedKVError("frequencies must be contiguous float64 [rotary_dim // 2]")
-    for w in (query_weight, key_weight):
-        if w is not None and (w.dtype != query.dtype or w.numel() != D or not w.is_contiguous()):
+    qw = kw = None
+    if query_weight is not None:
+        if query_weight.dtype != kind or query_weight.numel() != D or not query_weight.is_contiguous():
             raise PagedKVError(f"norm weights must be contiguous [{D}] of the query's type")
+        qw = query_weight.data_ptr()
+    if key_weight is not None:
+        if key_weight.dtype != kind or key_weight.numel() != D or not key_weight.is_contiguous():
+            raise PagedKVError(f"norm weights must be contiguous [{D}] of the query's type")
+        kw = key_weight.data_ptr()
     if query_out is None:
-        query_out = torch.empty((n, Hq, D), dtype=query.dtype, device=query.device)
-    elif query_out.shape != query.shape or query_out.dtype != query.dtype or not query_out.is_contiguous():
+        query_out = torch.empty((n, Hq, D), dtype=kind, device=query.device)
+    elif query_out.shape != query.shape or query_out.dtype != kind or not query_out.is_contiguous():
         raise PagedKVError("query_out must be a contiguous tensor of the query's shape and dtype")
-    return n, Hq, Hkv, D, qs, ks, 2 * frequencies.numel(), query_out, dtype
+    return n, Hq, Hkv, D, qs, ks, 2 * frequencies.shape[0], query_out, dtype, qw, kw
 
 
 def paged_rotary(query, key, positions, frequencies, rotary_start: int = 0, interleaved: bool = False,
@@ -466,17 +483,17 @@ def paged_rotary(query, key, positions, frequencies, rotary_start: int = 0, inte
     (float64 radians a position) and magnitude: see rotary_frequencies.
     Tokens may be slices of a fused projection's rows; an output may be its
     own contiguous input.  Returns (query_out, key_out)."""
-    n, Hq, Hkv, D, qs, ks, rd, query_out, dtype = _rotary_args(query, key, positions, frequencies, query_weight,
-                                                               key_weight, query_out)
+    n, Hq, Hkv, D, qs, ks, rd, query_out, dtype, qw, kw = _rotary_args(query, key, positions, frequencies,
+                                                                       query_weight, key_weight, query_out)
+    at = _int32_of(positions, n, "positions")
     if key_out is None:
         key_out = torch.empty((n, Hkv, D), dtype=key.dtype, device=key.device)
     elif key_out.shape != key.shape or key_out.dtype != key.dtype or not key_out.is_contiguous():
         raise PagedKVError("key_out must be a contiguous tensor of the key's shape and dtype")
     device = _same_device(query, key, positions, frequencies, query_weight, key_weight, query_out, key_out)
     status = load_library().paged_rotary(
-        _addr(query), _addr(key), qs, ks, n, _addr(positions), _addr(frequencies), rd, rotary_start,
-        1 if interleaved else 0, magnitude, None if query_weight is None else _addr(query_weight),
-        None if key_weight is None else _addr(key_weight), eps, Hq, Hkv, D, dtype, _addr(query_out), _addr(key_out),
+        query.data_ptr(), key.data_ptr(), qs, ks, n, at, frequencies.data_ptr(), rd, rotary_start,
+        1 if interleaved else 0, magnitude, qw, kw, eps, Hq, Hkv, D, dtype, query_out.data_ptr(), key_out.data_ptr(),
         _stream_on(stream, device))
     if status:
         _check(status)
@@ -494,34 +511,28 @@ def paged_append_rotary(query, key, value, batch_indices, positions, paged_kv_ca
     their requests."""
     layout = _layout_code(kv_layout)
     kp, vp, stride, P, H, S, D, base = split_cache(paged_kv_cache, layout)
-    n, Hq, Hkv, Dq, qs, ks, rd, query_out, dtype = _rotary_args(query, key, positions, frequencies, query_weight,
-                                                                key_weight, query_out)
-    Hv, Dv, vs = _token_rows(value, "value")
-    if Hkv != H or Dq != D or Hv != H or Dv != D or value.shape[0] != n:
+    n, Hq, Hkv, Dq, qs, ks, rd, query_out, dtype, qw, kw = _rotary_args(query, key, positions, frequencies,
+                                                                        query_weight, key_weight, query_out)
+    nv, Hv, Dv, vs = _token_rows(value, "value")
+    if Hkv != H or Dq != D or Hv != H or Dv != D or nv != n:
         raise PagedKVError(f"key/value must both be [{n}, {H}, {D}], query heads {D} wide")
-    if base.dtype != query.dtype or value.dtype != query.dtype:
+    kind = query.dtype
+    if base.dtype != kind or value.dtype != kind:
         raise PagedKVError("query, key, value and the cache hold the same 16-bit type")
-    if batch_indices.dtype != torch.int32 or batch_indices.numel() < n or not batch_indices.is_contiguous():
-        raise PagedKVError(f"batch_indices must be contiguous int32 with >= {n} entries")
-    rp = None
-    if rotary_positions is not None:
-        if rotary_positions.dtype != torch.int32 or rotary_positions.numel() < n or not rotary_positions.is_contiguous():
-            raise PagedKVError(f"rotary_positions must be contiguous int32 with >= {n} entries")
-        rp = _addr(rotary_positions)
+    at, requests = _int32_of(positions, n, "positions"), _int32_of(batch_indices, n, "batch_indices")
+    turn = None if rotary_positions is None else _int32_of(rotary_positions, n, "rotary_positions")
     B = kv_last_page_len.shape[0]
-    for t in (kv_indices, kv_indptr, kv_last_page_len):
-        if t.dtype != torch.int32 or not t.is_contiguous():
-            raise PagedKVError("kv_indices/kv_indptr/kv_last_page_len must be contiguous int32")
+    indices, last = _int32_of(kv_indices, 0, "kv_indices"), _int32_of(kv_last_page_len, 0, "kv_last_page_len")
+    indptr = _int32_of(kv_indptr, 0, "kv_indptr")
     if kv_indptr.numel() != B + 1:
         raise PagedKVError(f"kv_indptr must have {B + 1} entries")
     device = _same_device(query, key, value, base, batch_indices, positions, rotary_positions, kv_indices, kv_indptr,
                           kv_last_page_len, frequencies, query_weight, key_weight, query_out, err_word)
     status = load_library().paged_append_rotary(
-        _addr(query), _addr(key), _addr(value), qs, ks, vs, n, _addr(batch_indices), _addr(positions), rp, kp, vp,
-        stride, P, _addr(kv_indices), _addr(kv_indptr), _addr(kv_last_page_len), B, _addr(frequencies), rd,
-        rotary_start, 1 if interleaved else 0, magnitude, None if query_weight is None else _addr(query_weight),
-        None if key_weight is None else _addr(key_weight), eps, Hq, H, D, S, layout, dtype, _addr(query_out),
-        None if err_word is None else _addr(err_word), _stream_on(stream, device))
+        query.data_ptr(), key.data_ptr(), value.data_ptr(), qs, ks, vs, n, requests, at, turn, kp, vp, stride, P,
+        indices, indptr, last, B, frequencies.data_ptr(), rd, rotary_start, 1 if interleaved else 0, magnitude, qw, kw,
+        eps, Hq, H, D, S, layout, dtype, query_out.data_ptr(), None if err_word is None else err_word.data_ptr(),
+        _stream_on(stream, device))
     if status:
         _check(status)
     return query_out
@@ -746,6 +757,17 @@ def paged_decode_shared_workspace_size(batch_size, q_len_per_req, num_qo_heads, 
         page_size))
 
 
+def _page_table(t, n: int, longest: int, page_size: int) -> int:
+    """The row stride of a table of n rows of pages, for sequences of up to
+    `longest` tokens."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or t.dtype != torch.int32 or shape[0] < n or (shape[1] > 1 and stride[1] != 1):
+        raise PagedKVError("page tables must be int32 [rows, pages] with unit column stride")
+    if n and shape[1] * page_size < longest:
+        raise PagedKVError("a page table has fewer columns than its longest sequence needs")
+    return stride[0]
+
+
 def paged_decode_shared(query, kv_cache, workspace, prefix_tables, prefix_lens, group_indptr, max_prefix_len: int,
                         block_tables, seq_lens, max_seq_len: int, bmm1_scale: float = 1.0, bmm2_scale: float = 1.0,
                         sinks=None, kv_layout="HND", q_len_per_req: int = 1, out=None, lse=None, err_word=None,
@@ -774,14 +796,11 @@ def paged_decode_shared(query, kv_cache, workspace, prefix_tables, prefix_lens, 
     if rows < B * q_len_per_req:
         raise PagedKVError(f"query has {rows} rows; the requests need {B * q_len_per_req}")
     G = prefix_lens.shape[0]
-    for t, n in ((prefix_lens, G), (group_indptr, G + 1)):
-        if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-            raise PagedKVError("prefix_lens [groups] and group_indptr [groups + 1] must be contiguous int32")
-    for t, n, longest in ((prefix_tables, G, max_prefix_len), (block_tables, B, max_seq_len)):
-        if t.dim() != 2 or t.dtype != torch.int32 or t.shape[0] < n or (t.shape[1] > 1 and t.stride(1) != 1):
-            raise PagedKVError("page tables must be int32 [rows, pages] with unit column stride")
-        if n and t.shape[1] * S < longest:
-            raise PagedKVError("a page table has fewer columns than its longest sequence needs")
+    if prefix_lens.dtype != torch.int32 or prefix_lens.dim() != 1 or not prefix_lens.is_contiguous() or \
+            group_indptr.dtype != torch.int32 or group_indptr.shape != (G + 1,) or not group_indptr.is_contiguous():
+        raise PagedKVError("prefix_lens [groups] and group_indptr [groups + 1] must be contiguous int32")
+    prefix_stride = _page_table(prefix_tables, G, max_prefix_len, S)
+    table_stride = _page_table(block_tables, B, max_seq_len, S)
     if out is None:
         out = torch.empty_like(query)
     elif out.shape != shape or out.dtype != query.dtype or not out.is_contiguous():
@@ -798,11 +817,12 @@ def paged_decode_shared(query, kv_cache, workspace, prefix_tables, prefix_lens, 
     device = _same_device(query, base, workspace, prefix_tables, prefix_lens, group_indptr, block_tables, seq_lens,
                           sinks, out, lse, err_word)
     status = load_library().paged_decode_shared(
-        _addr(query), kp, vp, stride, P, _addr(workspace), workspace.nbytes, _addr(prefix_tables),
-        prefix_tables.stride(0), _addr(prefix_lens), _addr(group_indptr), G, max_prefix_len, _addr(block_tables),
-        block_tables.stride(0), _addr(seq_lens), B, max_seq_len, s1, s2, s1_dev, s2_dev,
-        None if sinks is None else _addr(sinks), q_len_per_req, Hqo, Hkv, D, S, layout, dtype, _addr(out),
-        None if lse is None else _addr(lse), None if err_word is None else _addr(err_word), _stream_on(stream, device))
+        query.data_ptr(), kp, vp, stride, P, workspace.data_ptr(), workspace.nbytes, prefix_tables.data_ptr(),
+        prefix_stride, prefix_lens.data_ptr(), group_indptr.data_ptr(), G, max_prefix_len, block_tables.data_ptr(),
+        table_stride, seq_lens.data_ptr(), B, max_seq_len, s1, s2, s1_dev, s2_dev,
+        None if sinks is None else sinks.data_ptr(), q_len_per_req, Hqo, Hkv, D, S, layout, dtype, out.data_ptr(),
+        None if lse is None else lse.data_ptr(), None if err_word is None else err_word.data_ptr(),
+        _stream_on(stream, device))
     if status:
         _check(status)
     return out
@@ -813,31 +833,36 @@ def paged_merge_states(states, out=None, lse=None, stream=None):
     of up to 16 (out [rows, heads, head_dim], lse float32 [rows, heads]) pairs
     as paged_decode and paged_prefill give them, over parts that share no key.
     out / lse may be those of one of the parts.  Returns (out, lse)."""
-    states = list(states)
-    if not states:
+    parts = list(states)
+    n = len(parts)
+    if not n:
         raise PagedKVError("no states to merge")
-    first = states[0][0]
-    shape = first.shape
+    first = parts[0][0]
+    shape, kind, device = first.shape, first.dtype, first.device
     dtype = _dtype_code(first)
-    if first.dim() != 3 or dtype > BF16:
+    if len(shape) != 3 or dtype > BF16:
         raise PagedKVError("a state's output is [rows, heads, head_dim] in fp16 or bf16")
+    rows = shape[:2]
     if out is None:
-        out = torch.empty(shape, dtype=first.dtype, device=first.device)
+        out = torch.empty(shape, dtype=kind, device=device)
     if lse is None:
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=first.device)
-    tensors = []
-    for o, l in states + [(out, lse)]:
-        if o.shape != shape or o.dtype != first.dtype or not o.is_contiguous():
+        lse = torch.empty(rows, dtype=torch.float32, device=device)
+    parts.append((out, lse))
+    here = torch.cuda.current_device() if first.is_cuda else -2
+    outs, lses = [], []
+    for o, l in parts:
+        if o.shape != shape or o.dtype != kind or not o.is_contiguous():
             raise PagedKVError("outputs must be contiguous tensors of the same shape and type")
-        if l.shape != shape[:2] or l.dtype != torch.float32 or not l.is_contiguous():
-            raise PagedKVError(f"log-sum-exps must be contiguous float32 {list(shape[:2])}")
-        tensors += (o, l)
-    device = _same_device(*tensors)
-    n = len(states)
-    pointers = (_c_p * (2 * n))(*[_addr(o) for o, _ in states], *[_addr(l) for _, l in states])
-    at = ctypes.addressof(pointers)
-    status = load_library().paged_merge_states(at, at + n * ctypes.sizeof(_c_p), n, shape[0] * shape[1], shape[2],
-                                               dtype, _addr(out), _addr(lse), _stream_on(stream, device))
+        if l.shape != rows or l.dtype != torch.float32 or not l.is_contiguous():
+            raise PagedKVError(f"log-sum-exps must be contiguous float32 {list(rows)}")
+        if o.get_device() != here or l.get_device() != here:
+            raise PagedKVError("tensor arguments must live on the current CUDA device")
+        outs.append(o.data_ptr())
+        lses.append(l.data_ptr())
+    pointers = array.array("Q", outs + lses)  # [outputs, out, log-sum-exps, lse]
+    at = pointers.buffer_info()[0]
+    status = load_library().paged_merge_states(at, at + 8 * (n + 1), n, shape[0] * shape[1], shape[2], dtype, outs[n],
+                                               lses[n], _stream_on(stream, here))
     if status:
         _check(status)
     return out, lse

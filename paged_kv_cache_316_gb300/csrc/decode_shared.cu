@@ -29,6 +29,8 @@
 // once at the end; scores, maxima, sums, O, the partials and the LSE are fp32.
 #include <math.h>
 
+#include <atomic>
+
 #include "attn_tile.cuh"
 #include "shared_own.cuh"
 #include "shared_prefix.cuh"
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
             const int leader_lane = __ffs(__ballot_sync(0xffffffffu, leader)) - 1;
             const CUtensorMap *tm = is_k ? &tm_k : &tm_v;
             const uint32_t base = is_k ? k_s : v_s;
-            const int S = 1 << p.page_shift, RB = pf_box_rows(S, kShTile), nbox = kShTile / RB;
+            const int S = 1 << p.page_shift, RB = pf_box_rows(S, WIDE ? kOwnTile : kShTile), nbox = kShTile / RB;
             const int oob = max(static_cast<int>(p.max_num_pages), 1);  // past the map: zero fill
             int issued = 0, queries = 0;  // (leader) steps, segments with copies issued
             bool ok = true;
@@ -606,19 +608,31 @@ static int plan_shared(int B, int Q, int Hqo, int Hkv, int D, int G, int max_pre
 
 struct SharedMaps {
     CUtensorMap q, k, v;              // the prefix kernel's: queries of a block of rows, the caches
-    CUtensorMap own_q, own_k, own_v;  // the own keys': queries of a request, the caches
+    CUtensorMap own_q, own_k, own_v;  // the own keys': queries of a request, the caches (k and v where they are wide)
 };
+
+// The kernel's dynamic shared memory, asked for once per device (bit d of
+// `set`: done on device d): a host call less in every later launch.
+template <typename K>
+static bool allow_smem(K kern, int bytes, std::atomic<unsigned long long> &set) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if (set.load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    set.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
 
 template <typename T, int NB, bool WIDE>
 static int launch_prefix(const SharedMaps &m, const SharedParams &p, dim3 grid, cudaStream_t st) {
     auto kern = shared_prefix_kernel<T, NB, WIDE>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(ShCfg<NB>::SMEM)) !=
-        cudaSuccess)
-        return PKV_ERR_CUDA;
+    static std::atomic<unsigned long long> set{0};
+    if (!allow_smem(kern, static_cast<int>(ShCfg<NB>::SMEM), set)) return PKV_ERR_CUDA;
     if constexpr (NB == 2) {
         // the register split draws on what the CTA is launched with: refuse to
         // launch if the compiled kernel has fewer (setmaxnreg.inc would wait forever)
-        static int ok = -1;
+        static std::atomic<int> ok{-1};
         if (ok < 0) {
             cudaFuncAttributes fa;
             if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return PKV_ERR_CUDA;
@@ -634,10 +648,12 @@ template <typename T, int MT>
 static int launch_own(const SharedMaps &m, const OwnParams &p, dim3 grid, cudaStream_t st) {
     auto kern = shared_own_kernel<T, MT>;
     constexpr int smem = static_cast<int>(OwnCfg<MT>::SMEM);
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return PKV_ERR_CUDA;
+    static std::atomic<unsigned long long> set{0};
+    if (!allow_smem(kern, smem, set)) return PKV_ERR_CUDA;
+    const CUtensorMap &k = p.ratio ? m.k : m.own_k, &v = p.ratio ? m.v : m.own_v;
     if (p.prefix.ctas > 0)
-        return launch_dependent(kern, grid, dim3(kOwnThreads), smem, st, m.own_q, m.own_k, m.own_v, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
-    kern<<<grid, kOwnThreads, smem, st>>>(m.own_q, m.own_k, m.own_v, p);
+        return launch_dependent(kern, grid, dim3(kOwnThreads), smem, st, m.own_q, k, v, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    kern<<<grid, kOwnThreads, smem, st>>>(m.own_q, k, v, p);
     return PKV_OK;
 }
 
@@ -751,6 +767,7 @@ extern "C" int paged_decode_shared(const void *query, const void *k_cache, const
     d.sinks = sinks;
     d.R = pl.R;
     d.page_shift = s.page_shift;
+    d.ratio = s.ratio;
     d.chunk = pl.chunk;
     d.n_split_max = pl.n_split_max;
     d.out = out;
@@ -773,20 +790,23 @@ extern "C" int paged_decode_shared(const void *query, const void *k_cache, const
     const uint32_t heads = static_cast<uint32_t>(w.group);
     const uint32_t block[3] = {64, heads, static_cast<uint32_t>(w.tok)}, own[3] = {64, heads, static_cast<uint32_t>(w.Q)};
     const int64_t pages = max_num_pages > 0 ? max_num_pages : 1;
-    if (pl.ctas > 0) {
-        const int box = pf_box_rows(page_size, kShTile);
-        auto cache = [&](CUtensorMap *x, const void *base) {
-            return s.ratio ? wide_tmap(x, base, t, layout, page_size, num_kv_heads, s.ratio, pages, box)
-                           : cache_tmap(x, base, t, layout, kShD, page_size, num_kv_heads, page_stride, pages, box);
-        };
-        if (!encode_tmap(&m.q, query, t, 3, dims, strides, block) || !cache(&m.k, k_cache) || !cache(&m.v, v_cache))
+    const int box = pf_box_rows(page_size, kOwnTile);
+    if ((pl.ctas > 0 && !encode_tmap(&m.q, query, t, 3, dims, strides, block)) ||
+        !encode_tmap(&m.own_q, query, t, 3, dims, strides, own))
+        return PKV_ERR_CUDA;
+    if (s.ratio) {  // the same boxes for both kernels
+        if (!wide_tmap(&m.k, k_cache, t, layout, page_size, num_kv_heads, s.ratio, pages, box) ||
+            !wide_tmap(&m.v, v_cache, t, layout, page_size, num_kv_heads, s.ratio, pages, box))
+            return PKV_ERR_CUDA;
+    } else {
+        const int box_p = pf_box_rows(page_size, kShTile);
+        if ((pl.ctas > 0 &&
+             (!cache_tmap(&m.k, k_cache, t, layout, kShD, page_size, num_kv_heads, page_stride, pages, box_p) ||
+              !cache_tmap(&m.v, v_cache, t, layout, kShD, page_size, num_kv_heads, page_stride, pages, box_p))) ||
+            !own_tmap(&m.own_k, k_cache, t, layout, page_size, num_kv_heads, page_stride, pages, box) ||
+            !own_tmap(&m.own_v, v_cache, t, layout, page_size, num_kv_heads, page_stride, pages, box))
             return PKV_ERR_CUDA;
     }
-    const int box = pf_box_rows(page_size, kOwnTile);
-    if (!encode_tmap(&m.own_q, query, t, 3, dims, strides, own) ||
-        !own_tmap(&m.own_k, k_cache, t, layout, page_size, num_kv_heads, page_stride, pages, box) ||
-        !own_tmap(&m.own_v, v_cache, t, layout, page_size, num_kv_heads, page_stride, pages, box))
-        return PKV_ERR_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     return dtype == PKV_BF16 ? run_shared<__nv_bfloat16>(m, s, d, pl, st) : run_shared<__half>(m, s, d, pl, st);
 }

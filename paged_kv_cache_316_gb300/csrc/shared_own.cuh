@@ -52,6 +52,7 @@ struct OwnParams {
     float bmm2;
     const float *sinks;
     int R, page_shift, chunk, n_split_max;
+    int ratio;  // see SharedParams
     void *out;
     float *lse;
     int merge_rows;  // most rows of a warp of the merge kernel
@@ -62,7 +63,8 @@ struct OwnParams {
     unsigned long long wait_ns;
 };
 
-// K or V cache as a 5-D map (64 dimensions, slots, the two halves of a head,
+// K or V cache, where the prefix kernel's wide map is not possible, as a 5-D
+// map (64 dimensions, slots, the two halves of a head,
 // heads, pages) whose box is `rows` slots of one head: 64 dimensions of each,
 // then the other 64.
 inline bool own_tmap(CUtensorMap *m, const void *base, CUtensorMapDataType t, int layout, int page_size, int heads,
@@ -290,8 +292,13 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
                             dbg_in(slot, RB, S, p.err);
                         }
                         const uint32_t dst = ring + st * STAGE + j * RB * 256;
-                        tma_load_5d(dst, &tm_k, b_full(st), 0, slot, 0, kvh, page);
-                        tma_load_5d(dst + kOwnBytes, &tm_v, b_full(st), 0, slot, 0, kvh, page);
+                        if (p.ratio) {  // (the prefix's maps: groups of 8 slots, (page, head))
+                            tma_load_5d(dst, &tm_k, b_full(st), 0, 0, 0, slot >> 3, page * p.ratio + kvh);
+                            tma_load_5d(dst + kOwnBytes, &tm_v, b_full(st), 0, 0, 0, slot >> 3, page * p.ratio + kvh);
+                        } else {
+                            tma_load_5d(dst, &tm_k, b_full(st), 0, slot, 0, kvh, page);
+                            tma_load_5d(dst + kOwnBytes, &tm_v, b_full(st), 0, slot, 0, kvh, page);
+                        }
                     }
                 }
                 if (t == 0) {  // the item's queries, as soon as the ones before are read
@@ -341,8 +348,9 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
         auto wait_warp = [&](uint32_t bar, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, wlim));
         };
-        // 16 bytes `ch` of key `row` of a tile: boxes of RB rows, 64 dimensions then 64
-        const int box_shift = min(p.page_shift, 6), box_low = (1 << box_shift) - 1;
+        // 16 bytes `ch` of key `row` of a tile: 2^box_shift keys (a box's, or 8),
+        // 64 dimensions of each, then the other 64
+        const int box_shift = p.ratio ? 3 : min(p.page_shift, 6), box_low = (1 << box_shift) - 1;
         auto at = [&](int row, int ch) {
             return static_cast<uint32_t>(((row & ~box_low) << 8) + (ch >> 3 << (box_shift + 7)) + ((row & box_low) << 7) +
                                          (((ch & 7) ^ (row & 7)) << 4));
