@@ -4,11 +4,12 @@ Argument marshalling only: every function derives sizes and strides from
 torch tensor shapes, passes device pointers and the current CUDA stream to
 the C entry point of the same name, and raises on a non-zero status.  No
 step of the computation happens here, and there is no CPU fallback: when the
-library has not been built, every call raises.
+library has not been built, every call raises.  The calls around attention
+over shared prefixes, which a small batch makes for a few microseconds of GPU
+work, do their marshalling in C++ (csrc/calls.cpp, _calls.so).
 """
 from __future__ import annotations
 
-import array
 import ctypes
 import math
 import os
@@ -21,6 +22,7 @@ F16, BF16, E4M3, F16_E4M3, BF16_E4M3 = 0, 1, 2, 3, 4
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libpagedkv.so"
 _lib = None
+_calls = None  # _calls.so, with the addresses of _lib's entry points
 
 _c_p = ctypes.c_void_p
 _i32 = ctypes.c_int32
@@ -100,7 +102,7 @@ def load_library(path: str | None = None):
     With `path`, load that build of the library instead and route every later
     call to it (e.g. the range-checking libpagedkv_debug.so; passing
     library_path() switches back)."""
-    global _lib
+    global _lib, _calls
     if _lib is None or path is not None:
         path = path or library_path()
         if not os.path.exists(path):
@@ -112,7 +114,16 @@ def load_library(path: str | None = None):
             fn = getattr(lib, name)
             fn.argtypes = args
             fn.restype = res
+        try:
+            from . import _calls as calls
+        except ImportError as e:
+            raise PagedKVError("_calls.so is not built for this interpreter and torch: run "
+                               f"`python -m paged_kv_cache_316_gb300.build` first ({e})") from None
         _lib = lib
+        calls.use(PagedKVError, _check, *(ctypes.cast(getattr(lib, f), _c_p).value for f in
+                                          ("paged_rotary", "paged_append_rotary", "paged_decode_shared",
+                                           "paged_merge_states")))
+        _calls = calls
     return _lib
 
 
@@ -422,54 +433,16 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling=None, fac
     return f.to(device), magnitude
 
 
-def _token_rows(t, name: str):
-    """(tokens, heads, head_dim, elements from token to token) of [tokens,
-    heads, head_dim] whose heads are contiguous."""
-    shape = t.shape
-    if len(shape) == 3:
-        n, H, D = shape
-        if t.is_contiguous():
-            return n, H, D, H * D
-        stride = t.stride()
-        if (D == 1 or stride[2] == 1) and (H == 1 or stride[1] == D):
-            return n, H, D, stride[0] if n > 1 else max(stride[0], H * D)
-    raise PagedKVError(f"{name} must be [tokens, heads, head_dim] with contiguous heads")
+def _native():
+    """_calls.so, once the library is loaded."""
+    if _calls is None:
+        load_library()
+    return _calls
 
 
-def _int32_of(t, n: int, name: str):
-    if t.dtype != torch.int32 or t.numel() < n or not t.is_contiguous():
-        raise PagedKVError(f"{name} must be contiguous int32 with >= {n} entries")
-    return t.data_ptr()
-
-
-def _rotary_args(query, key, positions, frequencies, query_weight, key_weight, query_out):
-    """The checks that paged_rotary and paged_append_rotary share: (tokens, q
-    heads, kv heads, head_dim, strides, rotary_dim, query_out, dtype, the
-    weights' addresses)."""
-    n, Hq, D, qs = _token_rows(query, "query")
-    nk, Hkv, Dk, ks = _token_rows(key, "key")
-    if nk != n or Dk != D:
-        raise PagedKVError("query and key have the same tokens and head_dim")
-    kind = query.dtype
-    dtype = _dtype_code(query)
-    if dtype > BF16 or key.dtype != kind:
-        raise PagedKVError("query and key are both fp16 or both bf16")
-    if frequencies.dtype != torch.float64 or frequencies.dim() != 1 or not frequencies.is_contiguous():
-        raise PagedKVError("frequencies must be contiguous float64 [rotary_dim // 2]")
-    qw = kw = None
-    if query_weight is not None:
-        if query_weight.dtype != kind or query_weight.numel() != D or not query_weight.is_contiguous():
-            raise PagedKVError(f"norm weights must be contiguous [{D}] of the query's type")
-        qw = query_weight.data_ptr()
-    if key_weight is not None:
-        if key_weight.dtype != kind or key_weight.numel() != D or not key_weight.is_contiguous():
-            raise PagedKVError(f"norm weights must be contiguous [{D}] of the query's type")
-        kw = key_weight.data_ptr()
-    if query_out is None:
-        query_out = torch.empty((n, Hq, D), dtype=kind, device=query.device)
-    elif query_out.shape != query.shape or query_out.dtype != kind or not query_out.is_contiguous():
-        raise PagedKVError("query_out must be a contiguous tensor of the query's shape and dtype")
-    return n, Hq, Hkv, D, qs, ks, 2 * frequencies.shape[0], query_out, dtype, qw, kw
+def _stream_arg(stream):
+    """None, for the current stream, or a stream's handle."""
+    return None if stream is None else _stream(stream)
 
 
 def paged_rotary(query, key, positions, frequencies, rotary_start: int = 0, interleaved: bool = False,
@@ -483,21 +456,8 @@ def paged_rotary(query, key, positions, frequencies, rotary_start: int = 0, inte
     (float64 radians a position) and magnitude: see rotary_frequencies.
     Tokens may be slices of a fused projection's rows; an output may be its
     own contiguous input.  Returns (query_out, key_out)."""
-    n, Hq, Hkv, D, qs, ks, rd, query_out, dtype, qw, kw = _rotary_args(query, key, positions, frequencies,
-                                                                       query_weight, key_weight, query_out)
-    at = _int32_of(positions, n, "positions")
-    if key_out is None:
-        key_out = torch.empty((n, Hkv, D), dtype=key.dtype, device=key.device)
-    elif key_out.shape != key.shape or key_out.dtype != key.dtype or not key_out.is_contiguous():
-        raise PagedKVError("key_out must be a contiguous tensor of the key's shape and dtype")
-    device = _same_device(query, key, positions, frequencies, query_weight, key_weight, query_out, key_out)
-    status = load_library().paged_rotary(
-        query.data_ptr(), key.data_ptr(), qs, ks, n, at, frequencies.data_ptr(), rd, rotary_start,
-        1 if interleaved else 0, magnitude, qw, kw, eps, Hq, Hkv, D, dtype, query_out.data_ptr(), key_out.data_ptr(),
-        _stream_on(stream, device))
-    if status:
-        _check(status)
-    return query_out, key_out
+    return (_calls or _native()).rotary(query, key, positions, frequencies, rotary_start, interleaved, magnitude,
+                                        query_weight, key_weight, eps, query_out, key_out, _stream_arg(stream))
 
 
 def paged_append_rotary(query, key, value, batch_indices, positions, paged_kv_cache, kv_indices, kv_indptr,
@@ -509,33 +469,10 @@ def paged_append_rotary(query, key, value, batch_indices, positions, paged_kv_ca
     returned, keys and values to their pages.  rotary_positions (int32): other
     positions for the rotation than `positions`, which place the tokens in
     their requests."""
-    layout = _layout_code(kv_layout)
-    kp, vp, stride, P, H, S, D, base = split_cache(paged_kv_cache, layout)
-    n, Hq, Hkv, Dq, qs, ks, rd, query_out, dtype, qw, kw = _rotary_args(query, key, positions, frequencies,
-                                                                        query_weight, key_weight, query_out)
-    nv, Hv, Dv, vs = _token_rows(value, "value")
-    if Hkv != H or Dq != D or Hv != H or Dv != D or nv != n:
-        raise PagedKVError(f"key/value must both be [{n}, {H}, {D}], query heads {D} wide")
-    kind = query.dtype
-    if base.dtype != kind or value.dtype != kind:
-        raise PagedKVError("query, key, value and the cache hold the same 16-bit type")
-    at, requests = _int32_of(positions, n, "positions"), _int32_of(batch_indices, n, "batch_indices")
-    turn = None if rotary_positions is None else _int32_of(rotary_positions, n, "rotary_positions")
-    B = kv_last_page_len.shape[0]
-    indices, last = _int32_of(kv_indices, 0, "kv_indices"), _int32_of(kv_last_page_len, 0, "kv_last_page_len")
-    indptr = _int32_of(kv_indptr, 0, "kv_indptr")
-    if kv_indptr.numel() != B + 1:
-        raise PagedKVError(f"kv_indptr must have {B + 1} entries")
-    device = _same_device(query, key, value, base, batch_indices, positions, rotary_positions, kv_indices, kv_indptr,
-                          kv_last_page_len, frequencies, query_weight, key_weight, query_out, err_word)
-    status = load_library().paged_append_rotary(
-        query.data_ptr(), key.data_ptr(), value.data_ptr(), qs, ks, vs, n, requests, at, turn, kp, vp, stride, P,
-        indices, indptr, last, B, frequencies.data_ptr(), rd, rotary_start, 1 if interleaved else 0, magnitude, qw, kw,
-        eps, Hq, H, D, S, layout, dtype, query_out.data_ptr(), None if err_word is None else err_word.data_ptr(),
-        _stream_on(stream, device))
-    if status:
-        _check(status)
-    return query_out
+    return (_calls or _native()).append_rotary(query, key, value, batch_indices, positions, paged_kv_cache, kv_indices,
+                                               kv_indptr, kv_last_page_len, frequencies, kv_layout, rotary_start,
+                                               interleaved, magnitude, query_weight, key_weight, eps, rotary_positions,
+                                               query_out, err_word, _stream_arg(stream))
 
 
 # ---- decode -------------------------------------------------------------------------------
@@ -757,17 +694,6 @@ def paged_decode_shared_workspace_size(batch_size, q_len_per_req, num_qo_heads, 
         page_size))
 
 
-def _page_table(t, n: int, longest: int, page_size: int) -> int:
-    """The row stride of a table of n rows of pages, for sequences of up to
-    `longest` tokens."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 2 or t.dtype != torch.int32 or shape[0] < n or (shape[1] > 1 and stride[1] != 1):
-        raise PagedKVError("page tables must be int32 [rows, pages] with unit column stride")
-    if n and shape[1] * page_size < longest:
-        raise PagedKVError("a page table has fewer columns than its longest sequence needs")
-    return stride[0]
-
-
 def paged_decode_shared(query, kv_cache, workspace, prefix_tables, prefix_lens, group_indptr, max_prefix_len: int,
                         block_tables, seq_lens, max_seq_len: int, bmm1_scale: float = 1.0, bmm2_scale: float = 1.0,
                         sinks=None, kv_layout="HND", q_len_per_req: int = 1, out=None, lse=None, err_word=None,
@@ -781,51 +707,15 @@ def paged_decode_shared(query, kv_cache, workspace, prefix_tables, prefix_lens, 
     of their own and end with the q_len_per_req newest tokens.  query and out
     [batch_size * q_len_per_req, heads, 128] and the cache are fp16 or bf16;
     scales may be one-element float32 device tensors."""
-    layout = _layout_code(kv_layout)
-    kp, vp, stride, P, Hkv, S, D, base = split_cache(kv_cache, layout)
-    shape = query.shape
-    rows, Hqo, Dq = shape
-    dtype = _dtype_code(query)
-    if Dq != D or not query.is_contiguous():
-        raise PagedKVError(f"query must be contiguous [rows, num_qo_heads, {D}]")
-    if dtype > BF16 or base.dtype != query.dtype:
-        raise PagedKVError("query and cache are both fp16 or both bf16")
-    if seq_lens.dim() != 1 or seq_lens.element_size() != 4 or not seq_lens.is_contiguous():
-        raise PagedKVError("seq_lens must be a contiguous 1-D tensor of 32-bit lengths")
-    B = seq_lens.shape[0]
-    if rows < B * q_len_per_req:
-        raise PagedKVError(f"query has {rows} rows; the requests need {B * q_len_per_req}")
-    G = prefix_lens.shape[0]
-    if prefix_lens.dtype != torch.int32 or prefix_lens.dim() != 1 or not prefix_lens.is_contiguous() or \
-            group_indptr.dtype != torch.int32 or group_indptr.shape != (G + 1,) or not group_indptr.is_contiguous():
-        raise PagedKVError("prefix_lens [groups] and group_indptr [groups + 1] must be contiguous int32")
-    prefix_stride = _page_table(prefix_tables, G, max_prefix_len, S)
-    table_stride = _page_table(block_tables, B, max_seq_len, S)
-    if out is None:
-        out = torch.empty_like(query)
-    elif out.shape != shape or out.dtype != query.dtype or not out.is_contiguous():
-        raise PagedKVError("out must be a contiguous tensor of the query's shape and dtype")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != shape[:2] or not lse.is_contiguous()):
-        raise PagedKVError(f"lse must be a contiguous float32 [{rows}, {Hqo}] tensor")
-    if sinks is not None and (sinks.dtype != torch.float32 or sinks.numel() != Hqo or not sinks.is_contiguous()):
-        raise PagedKVError(f"sinks must be contiguous float32 [{Hqo}]")
     s1, s2, s1_dev, s2_dev = bmm1_scale, bmm2_scale, None, None
     if type(s1) is not float:
         s1, s1_dev = _scale_arg(s1, query.device)
     if type(s2) is not float:
         s2, s2_dev = _scale_arg(s2, query.device)
-    device = _same_device(query, base, workspace, prefix_tables, prefix_lens, group_indptr, block_tables, seq_lens,
-                          sinks, out, lse, err_word)
-    status = load_library().paged_decode_shared(
-        query.data_ptr(), kp, vp, stride, P, workspace.data_ptr(), workspace.nbytes, prefix_tables.data_ptr(),
-        prefix_stride, prefix_lens.data_ptr(), group_indptr.data_ptr(), G, max_prefix_len, block_tables.data_ptr(),
-        table_stride, seq_lens.data_ptr(), B, max_seq_len, s1, s2, s1_dev, s2_dev,
-        None if sinks is None else sinks.data_ptr(), q_len_per_req, Hqo, Hkv, D, S, layout, dtype, out.data_ptr(),
-        None if lse is None else lse.data_ptr(), None if err_word is None else err_word.data_ptr(),
-        _stream_on(stream, device))
-    if status:
-        _check(status)
-    return out
+    return (_calls or _native()).decode_shared(query, kv_cache, workspace, prefix_tables, prefix_lens, group_indptr,
+                                               max_prefix_len, block_tables, seq_lens, max_seq_len, s1, s2, s1_dev,
+                                               s2_dev, sinks, kv_layout, q_len_per_req, out, lse, err_word,
+                                               _stream_arg(stream))
 
 
 def paged_merge_states(states, out=None, lse=None, stream=None):
@@ -833,39 +723,7 @@ def paged_merge_states(states, out=None, lse=None, stream=None):
     of up to 16 (out [rows, heads, head_dim], lse float32 [rows, heads]) pairs
     as paged_decode and paged_prefill give them, over parts that share no key.
     out / lse may be those of one of the parts.  Returns (out, lse)."""
-    parts = list(states)
-    n = len(parts)
-    if not n:
-        raise PagedKVError("no states to merge")
-    first = parts[0][0]
-    shape, kind, device = first.shape, first.dtype, first.device
-    dtype = _dtype_code(first)
-    if len(shape) != 3 or dtype > BF16:
-        raise PagedKVError("a state's output is [rows, heads, head_dim] in fp16 or bf16")
-    rows = shape[:2]
-    if out is None:
-        out = torch.empty(shape, dtype=kind, device=device)
-    if lse is None:
-        lse = torch.empty(rows, dtype=torch.float32, device=device)
-    parts.append((out, lse))
-    here = torch.cuda.current_device() if first.is_cuda else -2
-    outs, lses = [], []
-    for o, l in parts:
-        if o.shape != shape or o.dtype != kind or not o.is_contiguous():
-            raise PagedKVError("outputs must be contiguous tensors of the same shape and type")
-        if l.shape != rows or l.dtype != torch.float32 or not l.is_contiguous():
-            raise PagedKVError(f"log-sum-exps must be contiguous float32 {list(rows)}")
-        if o.get_device() != here or l.get_device() != here:
-            raise PagedKVError("tensor arguments must live on the current CUDA device")
-        outs.append(o.data_ptr())
-        lses.append(l.data_ptr())
-    pointers = array.array("Q", outs + lses)  # [outputs, out, log-sum-exps, lse]
-    at = pointers.buffer_info()[0]
-    status = load_library().paged_merge_states(at, at + 8 * (n + 1), n, shape[0] * shape[1], shape[2], dtype, outs[n],
-                                               lses[n], _stream_on(stream, here))
-    if status:
-        _check(status)
-    return out, lse
+    return (_calls or _native()).merge_states(states, out, lse, _stream_arg(stream))
 
 
 # ---- prefill ---------------------------------------------------------------------------------

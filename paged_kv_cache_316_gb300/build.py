@@ -9,6 +9,9 @@ and no libcuda at link time).  The debug variant, libpagedkv_debug.so
 (objects in _build/debug/), is the same source compiled with
 -DPKV_DEBUG_BOUNDS=1: every offset the kernels derive is range-checked
 before use (the PKV_DEV_ERR_BOUNDS bit of the error word).
+
+_calls.so, the part of the Python binding that is C++ (csrc/calls.cpp), is
+compiled beside them with g++ against the installed torch's headers.
 """
 from __future__ import annotations
 
@@ -17,6 +20,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -24,6 +28,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpagedkv.so")
 LIB_DEBUG = os.path.join(HERE, "libpagedkv_debug.so")
+LIB_CALLS = os.path.join(HERE, "_calls.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -94,19 +99,51 @@ def _finish(objs, lib, procs, force: bool, ptxas_verbose: bool, quiet: bool) -> 
     return lib
 
 
+def _start_calls(force: bool):
+    """Start the compilation of _calls.so if it is stale; returns the jobs of
+    _finish."""
+    src = os.path.join(CSRC, "calls.cpp")
+    if not (force or _stale(LIB_CALLS, [src, os.path.join(INCLUDE, "pagedkv.h")])):
+        return []
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    lib = os.path.join(root, "lib")
+    tmp = LIB_CALLS + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-I", os.path.join(root, "include"), "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), src, "-o", tmp, "-L", lib,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
+    return [(src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True), tmp)]
+
+
+def _finish_calls(jobs):
+    for src, pr, tmp in jobs:
+        out, _ = pr.communicate()
+        if pr.returncode != 0:
+            raise RuntimeError(f"g++ failed:\n--- {src}\n{out}")
+        os.replace(tmp, LIB_CALLS)
+
+
 def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True,
           debug_bounds: bool = False) -> str:
     """Build one variant: libpagedkv.so, or with debug_bounds the range-checking
     libpagedkv_debug.so (-DPKV_DEBUG_BOUNDS=1); returns its path."""
+    calls = _start_calls(force)
     objs, lib, procs = _start(debug_bounds, force, ptxas_verbose)
-    return _finish(objs, lib, procs, force, ptxas_verbose, quiet)
+    lib = _finish(objs, lib, procs, force, ptxas_verbose, quiet)
+    _finish_calls(calls)
+    return lib
 
 
 def build_all(force: bool = False, quiet: bool = True):
     """Build both variants, all translation units compiled in parallel;
     returns (release library, debug library)."""
+    calls = _start_calls(force)
     jobs = [_start(d, force, False) for d in (False, True)]
-    return tuple(_finish(*j, force, False, quiet) for j in jobs)
+    libs = tuple(_finish(*j, force, False, quiet) for j in jobs)
+    _finish_calls(calls)
+    return libs
 
 
 def main():
