@@ -145,16 +145,19 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
         PrefixWalk at;
         bool bad;
         const uint32_t team = blockIdx.x / w.team;
-        const uint32_t W = scan_prefixes(
+        uint32_t W = 0, per = 1, w0 = 0;
+        scan_prefixes(
             w,
-            [&](uint32_t all, int, int, uint32_t first, uint32_t n) {
-                const uint32_t w0 = team * prefix_steps_per_team(w, all);
-                return w0 >= first && w0 - first < n;
+            [&](uint32_t all) {
+                W = all;
+                per = prefix_steps_per_team(w, all);
+                w0 = team * per;
             },
-            at.x, bad);
-        const uint32_t per = prefix_steps_per_team(w, W), w0 = team * per;
+            [&](int, int, uint32_t first, uint32_t n) { return w0 >= first && w0 - first < n; }, at.x, bad);
+        if (bad) W = 0;
         if (blockIdx.x == 0) {
             if (bad && lane == 0) set_err(w.err, PKV_DEV_ERR_BATCH);
+            if (lane == 0) *w.per = per;
             for (int g = lane; g < w.G && !bad; g += 32)
                 if (w.prefix_lens[g] < 0 || w.prefix_lens[g] > w.max_prefix) set_err(w.err, PKV_DEV_ERR_LEN);
         }
@@ -544,7 +547,8 @@ struct SharedPlan {
     int R, MT, chunk, n_split_max;  // own keys: rows of an item, tiles of 16 of them, keys and splits
     int nb, tok, team, ctas;
     int64_t rows, parts;
-    size_t prefix_o, prefix_lse, own_o, own_lse, bytes;  // offsets in the workspace
+    int64_t all;         // partial rows: the prefix's, then the own keys'
+    size_t lse, per, bytes;  // offsets in the workspace
 };
 
 static int plan_shared(int B, int Q, int Hqo, int Hkv, int D, int G, int max_prefix, int max_seq_len, int page_size,
@@ -592,17 +596,11 @@ static int plan_shared(int B, int Q, int Hqo, int Hkv, int D, int G, int max_pre
     const int64_t most = tiles * Hkv * nk;  // (a CTA takes one step at least; a team is for more than that)
     pl.ctas = G > 0 && nk > 0 ? static_cast<int>((most < sms ? most : sms) / pl.team * pl.team) : 0;
     pl.parts = pl.ctas > 0 ? pl.rows + static_cast<int64_t>(pl.ctas) * pl.nb * 128 : 0;
-    const size_t slots = static_cast<size_t>(B) * Hkv * pl.n_split_max * pl.R;
-    size_t at = 0;
-    pl.prefix_o = at;
-    at += round_up(pl.parts * kShD * sizeof(float), 256);
-    pl.prefix_lse = at;
-    at += round_up(pl.parts * sizeof(float), 256);
-    pl.own_o = at;
-    at += round_up(slots * kShD * sizeof(float), 256);
-    pl.own_lse = at;
-    at += round_up(slots * sizeof(float), 256);
-    pl.bytes = at;
+    pl.all = pl.parts + static_cast<int64_t>(B) * Hkv * pl.n_split_max * pl.R;
+    if (pl.all > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
+    pl.lse = static_cast<size_t>(pl.all) * kShD * sizeof(float);
+    pl.per = pl.lse + round_up(static_cast<size_t>(pl.all) * sizeof(float), 256);
+    pl.bytes = pl.all > 0 ? pl.per + 256 : 0;
     return PKV_OK;
 }
 
@@ -726,6 +724,8 @@ extern "C" int paged_decode_shared(const void *query, const void *k_cache, const
     PrefixWork &w = s.w;
     w.group_indptr = group_indptr;
     w.prefix_lens = prefix_lens;
+    w.seq_lens = seq_lens;
+    w.max_seq_len = max_seq_len;
     w.G = pl.ctas > 0 ? num_groups : 0;
     w.B = batch_size;
     w.Q = q_len_per_req;
@@ -737,11 +737,13 @@ extern "C" int paged_decode_shared(const void *query, const void *k_cache, const
     w.max_prefix = max_prefix_len;
     w.team = pl.team;
     w.ctas = pl.ctas;
-    w.full = num_sms() / pl.team;
-    w.rows = pl.rows;
-    w.parts = pl.parts;
-    w.ws_o = reinterpret_cast<float *>(ws + pl.prefix_o);
-    w.ws_lse = reinterpret_cast<float *>(ws + pl.prefix_lse);
+    w.sms = num_sms();
+    w.rows = static_cast<uint32_t>(pl.rows);
+    w.parts = static_cast<uint32_t>(pl.parts);
+    w.all = static_cast<uint32_t>(pl.all);
+    w.ws_o = reinterpret_cast<float *>(ws);
+    w.ws_lse = reinterpret_cast<float *>(ws + pl.lse);
+    w.per = reinterpret_cast<uint32_t *>(ws + pl.per);
     w.err = err_word;
     s.prefix_tables = prefix_tables;
     s.pt_stride = prefix_table_stride;
@@ -757,8 +759,6 @@ extern "C" int paged_decode_shared(const void *query, const void *k_cache, const
     d.prefix = w;
     d.block_tables = block_tables;
     d.bt_stride = block_table_stride;
-    d.seq_lens = seq_lens;
-    d.max_seq_len = max_seq_len;
     d.max_num_pages = max_num_pages;
     d.scale_log2 = s.scale_log2;
     d.bmm1_dev = bmm1_scale_dev;
@@ -772,9 +772,6 @@ extern "C" int paged_decode_shared(const void *query, const void *k_cache, const
     d.n_split_max = pl.n_split_max;
     d.out = out;
     d.lse = lse;
-    d.ws_o = reinterpret_cast<float *>(ws + pl.own_o);
-    d.ws_lse = reinterpret_cast<float *>(ws + pl.own_lse);
-    d.ws_rows = static_cast<int64_t>(batch_size) * num_kv_heads * pl.n_split_max * pl.R;
     // (a warp for a row until every SM has 28 of them)
     const int64_t fill = (pl.rows + 28 * num_sms() - 1) / (28 * num_sms());
     d.merge_rows = static_cast<int>(fill < w.group ? fill : w.group);

@@ -44,8 +44,6 @@ struct OwnParams {
     PrefixWork prefix;
     const int32_t *block_tables;
     int64_t bt_stride;
-    const uint32_t *seq_lens;
-    int max_seq_len;
     int64_t max_num_pages;
     float scale_log2;
     const float *bmm1_dev, *bmm2_dev;
@@ -56,9 +54,6 @@ struct OwnParams {
     void *out;
     float *lse;
     int merge_rows;  // most rows of a warp of the merge kernel
-    float *ws_o;    // [B][Hkv][n_split_max][R][128]
-    float *ws_lse;  // [B][Hkv][n_split_max][R], base 2
-    int64_t ws_rows;
     int32_t *err;
     unsigned long long wait_ns;
 };
@@ -77,8 +72,9 @@ inline bool own_tmap(CUtensorMap *m, const void *base, CUtensorMapDataType t, in
 }
 
 __host__ __device__ inline int own_splits(int L, int chunk) { return L <= 0 ? 1 : (L + chunk - 1) / chunk; }
-__device__ __forceinline__ int64_t own_part(const OwnParams &p, int b, int kvh, int s, int r) {
-    return ((static_cast<int64_t>(b) * p.prefix.Hkv + kvh) * p.n_split_max + s) * p.R + r;
+// Where row r of an item goes: [B][Hkv][n_split_max][R] behind the prefix's partials.
+__device__ __forceinline__ uint32_t own_part(const OwnParams &p, int b, int kvh, int s, int r) {
+    return p.prefix.parts + ((static_cast<uint32_t>(b) * p.prefix.Hkv + kvh) * p.n_split_max + s) * p.R + r;
 }
 
 // The rest of a row once its maximum M (base 2) and sum den are known: what the
@@ -195,14 +191,14 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, wlim));
         };
         int s = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
-        uint32_t L_in = p.seq_lens[b];
+        uint32_t L_in = p.prefix.seq_lens[b];
         int i = 0, items = 0;       // tiles put into the ring, items with queries
         int asked = 0, heard = 0;   // CTAs asked for, answers read
         bool more = true, ok = true;
         while (more && ok) {
-            const int L = static_cast<int>(min(L_in, static_cast<uint32_t>(p.max_seq_len)));
+            const int L = static_cast<int>(min(L_in, static_cast<uint32_t>(p.prefix.max_seq_len)));
             if (s == 0 && kvh == 0 && lane == 0) {
-                if (L_in > static_cast<uint32_t>(p.max_seq_len)) set_err(p.err, PKV_DEV_ERR_LEN);
+                if (L_in > static_cast<uint32_t>(p.prefix.max_seq_len)) set_err(p.err, PKV_DEV_ERR_LEN);
                 if (L < w.Q) set_err(p.err, PKV_DEV_ERR_QLEN);
             }
             const int n_split = own_splits(L, p.chunk);
@@ -212,7 +208,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
             // pages of 32 boxes at a time, a lane each (-1: no key), the next 32 on the way
             auto lookup = [&](int j0) {
                 const int key = k0 + (j0 + lane) * RB;
-                const bool read = key < k1 && dbg_in(key >> p.page_shift, 1, (p.max_seq_len + S - 1) >> p.page_shift, p.err);
+                const bool read = key < k1 && dbg_in(key >> p.page_shift, 1, (p.prefix.max_seq_len + S - 1) >> p.page_shift, p.err);
                 return read ? bt[key >> p.page_shift] : -1;
             };
             int pages = -1, pages_next = n > 0 ? lookup(0) : -1;
@@ -231,7 +227,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
                 more = cta_answer(answer, ns, nkvh, nb);
                 fence_proxy_async_smem();  // (before the next answer overwrites this one)
                 __syncwarp();
-                if (more) nL = p.seq_lens[nb];
+                if (more) nL = p.prefix.seq_lens[nb];
                 return true;
             };
             for (int t = 0; t < n && ok; ++t, ++i) {
@@ -525,16 +521,16 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
 #pragma unroll
                 for (int f = 0; f < 2; ++f) {
                     const int r = 16 * mt + g + 8 * f;
-                    const int64_t row = own_part(p, b, kvh, s, r);
-                    if (r >= p.R || !dbg_in(row, 1, p.ws_rows, p.err)) continue;
+                    const uint32_t row = own_part(p, b, kvh, s, r);
+                    if (r >= p.R || !dbg_in(row, 1, w.all, p.err)) continue;
                     const float den = (red_l[r] + red_l[ROWS + r]) + (red_l[2 * ROWS + r] + red_l[3 * ROWS + r]);
                     const float inv = den > 0.f ? 1.f / den : (den != den ? den : 0.f);
 #pragma unroll
                     for (int n = 0; n < 4; ++n)
-                        *reinterpret_cast<float2 *>(p.ws_o + row * 128 + d + 8 * n) =
+                        *reinterpret_cast<float2 *>(w.ws_o + static_cast<size_t>(row) * 128 + d + 8 * n) =
                             make_float2(o[mt][n][2 * f] * inv, o[mt][n][2 * f + 1] * inv);
                     if (warp == 0 && c == 0)
-                        p.ws_lse[row] = den > 0.f ? m[mt][f] + fast_log2(den) : (den != den ? den : -INFINITY);
+                        w.ws_lse[row] = den > 0.f ? m[mt][f] + fast_log2(den) : (den != den ? den : -INFINITY);
                 }
         }
     }
@@ -543,61 +539,74 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
 
 // A warp for up to `merge_rows` query heads of one token and kv head in turn:
 // the partials of its request's own keys and of its group's prefix, and the
-// sink.  Their rows lie one behind the other in every partial, so that where
-// they are is worked out once, while the kernels before still run.  (A warp to
-// a row with the divisions of its own: 13 us against 6 for 16,384 rows.)
+// sink.  Their rows lie one behind the other in every partial: where they are
+// is worked out once, a partial to a lane, and a lane takes one partial's LSE
+// and weight of a row too.  (A warp to a row, everything worked out by all of
+// its lanes: 23 us for 16,384 rows of 5 partials, bound by instructions.)
 template <typename T>
 __global__ void __launch_bounds__(128) shared_merge_kernel(const __grid_constant__ OwnParams p) {
     const PrefixWork &w = p.prefix;
     const int lane = threadIdx.x & 31, subs = (w.group + p.merge_rows - 1) / p.merge_rows;
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    const uint32_t at = blockIdx.x * 4 + (threadIdx.x >> 5);
     if (at >= w.rows / w.group * subs) return pdl_wait();  // (rows / group: tokens * Hkv)
-    const uint32_t unit = static_cast<uint32_t>(at / subs);
-    const int i_first = static_cast<int>(at - static_cast<int64_t>(unit) * subs) * p.merge_rows;
-    const int i_end = min(i_first + p.merge_rows, w.group);
+    const uint32_t unit = at / subs;
+    const int i_first = static_cast<int>(at - unit * subs) * p.merge_rows, i_end = min(i_first + p.merge_rows, w.group);
     const int token = unit / w.Hkv, kvh = unit - token * w.Hkv, b = token / w.Q, t = token - b * w.Q;
+    const int n_own = own_splits(static_cast<int>(min(w.seq_lens[b], static_cast<uint32_t>(w.max_seq_len))), p.chunk);
     PrefixGroup x;
     bool bad;
-    const uint32_t W = scan_prefixes(w, [=](uint32_t, int lo, int hi, uint32_t, uint32_t) { return lo <= b && b < hi; }, x, bad);
-    const int n_own = own_splits(static_cast<int>(min(p.seq_lens[b], static_cast<uint32_t>(p.max_seq_len))), p.chunk);
-    const PrefixParts parts = prefix_parts(w, x, prefix_steps_per_team(w, W), token, kvh * w.group, kvh);
-    const int64_t own0 = own_part(p, b, kvh, 0, t * w.group);
-    const int n = n_own + parts.n;
+    scan_prefixes(w, [](uint32_t) {}, [=](int lo, int hi, uint32_t, uint32_t) { return lo <= b && b < hi; }, x, bad);
+    const uint32_t own0 = own_part(p, b, kvh, 0, t * w.group);
     pdl_wait();
+    const PrefixParts parts = prefix_parts(w, x, w.ctas > 0 ? *w.per : 1, token, kvh);
+    const int n = n_own + parts.n;
+    auto place = [&](int j) { return j < n_own ? own0 + static_cast<uint32_t>(j) * p.R : parts.at(j - n_own); };
+    uint32_t mine = place(lane);
     for (int i = i_first; i < i_end; ++i) {
         float M = -INFINITY, den = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int j0 = 0; j0 < n; j0 += 8) {  // eight partials' loads in flight together
-            float y[8];
-            float4 v[8];
+        for (int j0 = 0; j0 < n; j0 += 32) {
+            const int m = min(n - j0, 32);
+            if (n > 32) mine = place(j0 + lane);
+            const bool in = lane < m && dbg_in(mine + i, 1, w.all, p.err);
+            const float y = in ? w.ws_lse[mine + i] : -INFINITY;
+            float keep = 0.f, u = 0.f;
+            for (int k0 = 0; k0 < m; k0 += 8) {  // eight partials' loads in flight together
+                float4 v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const bool own = j0 + j < n_own;
-                const int64_t row = (own ? own0 + static_cast<int64_t>(j0 + j) * p.R : parts.at(j0 + j - n_own)) + i;
-                const bool in = j0 + j < n && dbg_in(row, 1, own ? p.ws_rows : w.parts, p.err);
-                y[j] = in ? (own ? p.ws_lse : w.ws_lse)[row] : -INFINITY;
-                v[j] = in ? *reinterpret_cast<const float4 *>((own ? p.ws_o : w.ws_o) + row * 128 + lane * 4)
-                          : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            float now = M;
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t row = __shfl_sync(0xffffffffu, mine, k0 + k) + i;
+                    v[k] = k0 + k < m && dbg_in(row, 1, w.all, p.err)
+                               ? *reinterpret_cast<const float4 *>(w.ws_o + static_cast<size_t>(row) * 128 + lane * 4)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                if (k0 == 0) {  // the weights of all 32
+                    float now = y;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) now = fmaxf(now, y[j]);
-            const float base = now == -INFINITY ? 0.f : now, keep = fast_exp2(M - base);
-            M = now;
-            den *= keep;
-            acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+                    for (int o = 16; o; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
+                    now = fmaxf(now, M);
+                    const float base = now == -INFINITY ? 0.f : now;
+                    keep = fast_exp2(M - base);
+                    u = fast_exp2(y - base);  // (a part's NaN stays)
+                    M = now;
+                    float sum = u;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float u = fast_exp2(y[j] - base);  // (a part's NaN stays)
-                den += u;
-                acc.x += u * v[j].x;
-                acc.y += u * v[j].y;
-                acc.z += u * v[j].z;
-                acc.w += u * v[j].w;
+                    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    den = den * keep + sum;
+                    acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float f = __shfl_sync(0xffffffffu, u, k0 + k);
+                    acc.x += f * v[k].x;
+                    acc.y += f * v[k].y;
+                    acc.z += f * v[k].z;
+                    acc.w += f * v[k].w;
+                }
             }
         }
         const int h = kvh * w.group + i;
-        const int64_t row = static_cast<int64_t>(token) * w.Hqo + h;
+        const size_t row = static_cast<size_t>(token) * w.Hqo + h;
         float lse;
         const float mul = finish_row(p, h, M, den, lse);
         uint2 out;

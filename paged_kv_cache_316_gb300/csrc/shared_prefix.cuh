@@ -13,9 +13,10 @@
 // it out again.  A CTA's run through one item is a segment; only its first can
 // begin inside an item.
 //
-// Partials.  Row (token, head) of the segment that begins the item: index
-// token * Hqo + head; of a segment that continues it: rows + (cta * nb +
-// block) * 128 + row of the block.  One fp32 output row and one base-2 LSE each.
+// Partials: one array of fp32 output rows and one of base-2 LSEs.  Row (token,
+// head) of the segment that begins the item: index token * Hqo + head; of a
+// segment that continues it: rows + (cta * nb + block) * 128 + row of the
+// block; then, from `parts` on, those of the own keys (shared_own.cuh).
 #pragma once
 
 #include "pkv_common.cuh"
@@ -23,19 +24,23 @@
 namespace pkv {
 
 constexpr int kShTile = 128;  // keys per step
-constexpr int kShMinSteps = 8;
+constexpr float kShCtaSteps = 5.f;  // what a CTA of the prefix kernel costs beside its steps
 
 struct PrefixWork {
     const int32_t *group_indptr, *prefix_lens;
+    const uint32_t *seq_lens;  // own keys
+    int max_seq_len;
     int G, B, Q, Hqo, Hkv, group;
     int tok, nb;  // tokens of a block (128 / group), blocks of an item
     int max_prefix;
     int team, ctas;  // ctas: a multiple of team
-    int full;        // teams that all SMs hold
-    int64_t rows;   // B * Q * Hqo
-    int64_t parts;  // rows + ctas * nb * 128
-    float *ws_o;    // [parts][128]
-    float *ws_lse;  // [parts], base 2
+    int sms;
+    uint32_t rows;   // B * Q * Hqo
+    uint32_t parts;  // rows + ctas * nb * 128 (0 without a prefix)
+    uint32_t all;    // parts and the own keys' rows
+    float *ws_o;     // [all][128]
+    float *ws_lse;   // [all]
+    uint32_t *per;   // prefix_steps_per_team, for the kernel that joins
     int32_t *err;
 };
 
@@ -57,14 +62,13 @@ __device__ __forceinline__ void read_prefix_group(const PrefixWork &p, int g, Pr
     x.items = (x.tiles + p.team - 1) / p.team;
 }
 
-// All groups, by one warp: returns W and, in `found`, the group for which
-// match(W, a, b, first step, steps) holds (g = -1: none).  Where group_indptr
-// is not in order no group has work (*bad).  Up to 32 groups are read once,
-// more of them twice.
-template <typename F>
-__device__ __forceinline__ uint32_t scan_prefixes(const PrefixWork &p, F match, PrefixGroup &found, bool &bad) {
+// All groups, by one warp: calls total(W), then finds the group for which
+// match(a, b, first step, steps) holds (g = -1: none).  Where group_indptr is
+// not in order no group has work (*bad).  Up to 32 groups are read once, more
+// of them twice.
+template <typename G, typename F>
+__device__ __forceinline__ void scan_prefixes(const PrefixWork &p, G total, F match, PrefixGroup &found, bool &bad) {
     const int lane = threadIdx.x & 31;
-    uint32_t W = 0;
     found.g = -1;
     bad = false;
     PrefixGroup x = {};
@@ -87,9 +91,9 @@ __device__ __forceinline__ uint32_t scan_prefixes(const PrefixWork &p, F match, 
                 if (lane >= o) sum += y;
             }
             const uint32_t all = __shfl_sync(0xffffffffu, sum, 31);
-            if (p.G <= 32) W = all;
+            if (p.G <= 32) total(all);
             if (pass == 1) {
-                const unsigned m = __ballot_sync(0xffffffffu, g < p.G && match(W, x.a, x.b, carry + sum - n, n));
+                const unsigned m = __ballot_sync(0xffffffffu, g < p.G && match(x.a, x.b, carry + sum - n, n));
                 if (m && found.g < 0) {
                     const int j = __ffs(m) - 1;
                     found.g = g0 + j;
@@ -106,33 +110,48 @@ __device__ __forceinline__ uint32_t scan_prefixes(const PrefixWork &p, F match, 
         }
         if (bad) {
             found.g = -1;
-            return 0;
+            return;
         }
-        W = carry;
+        if (pass == 0) total(carry);
     }
-    return W;
 }
 
-// Steps of a team: all share the work evenly, but none takes fewer than
-// kShMinSteps while half of the SMs would do.
+// Steps of a team, by one warp.  N CTAs take C + W / N steps' time each (C =
+// kShCtaSteps), and the other SMs stream own keys meanwhile, which cost one SM A
+// steps: both are done at the same time T, and S SMs busy until then, if
+//   T = C + W / N,  S T = C N + W + A,  so  C N^2 + (W + A - C S) N - W S = 0
+// (W the CTAs' steps; N = S without own keys).  A: 128 own keys of a head are
+// streamed in about a step; of more than 256 requests, 256 stand for all.  So
+// few steps that half of the SMs have one each are not put together.  Every
+// CTA of the prefix kernel works it out alike; the kernel that joins reads it.
 __device__ __forceinline__ uint32_t prefix_steps_per_team(const PrefixWork &p, uint32_t W) {
-    const uint32_t n = p.ctas / p.team, even = (W + n - 1) / n, half = (2 * W + p.full - 1) / p.full;
-    return max(1u, max(even, min(static_cast<uint32_t>(kShMinSteps), half)));
+    const uint32_t w = W * p.team;
+    if (W == 0) return 1;
+    if (2 * w <= static_cast<uint32_t>(p.sms)) return 1;
+    const int lane = threadIdx.x & 31, n = min(p.B, 256), of = p.B / n;
+    float sum = 0.f;
+    for (int i = lane; i < n; i += 32)
+        sum += static_cast<float>(min(p.seq_lens[i * of], static_cast<uint32_t>(p.max_seq_len)));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float A = sum * static_cast<float>(of * p.Hkv) / kShTile, S = static_cast<float>(p.sms), steps = static_cast<float>(w);
+    const float half = 0.5f * (steps + A - kShCtaSteps * S);
+    const float N = (sqrtf(half * half + kShCtaSteps * steps * S) - half) / kShCtaSteps;
+    const uint32_t teams = max(1u, min(static_cast<uint32_t>(N), static_cast<uint32_t>(p.ctas)) / p.team);
+    return (W + teams - 1) / teams;
 }
 
 // The partials of a token's rows at one kv head: the first at `row` (of the
 // kv head's first query head), n in all, the others at extra + i * step.
 struct PrefixParts {
     int n;
-    int64_t row, extra;
-    int step;
-    __device__ __forceinline__ int64_t at(int i) const { return i == 0 ? row : extra + static_cast<int64_t>(i) * step; }
+    uint32_t row, extra, step;
+    __device__ __forceinline__ uint32_t at(int i) const { return i == 0 ? row : extra + static_cast<uint32_t>(i) * step; }
 };
-__device__ __forceinline__ PrefixParts prefix_parts(const PrefixWork &p, const PrefixGroup &x, uint32_t per, int token,
-                                                    int head, int kvh) {
+__device__ __forceinline__ PrefixParts prefix_parts(const PrefixWork &p, const PrefixGroup &x, uint32_t per, int token, int kvh) {
     PrefixParts r;
     r.n = 0;
-    r.row = static_cast<int64_t>(token) * p.Hqo + head;
+    r.row = static_cast<uint32_t>(token) * p.Hqo + kvh * p.group;
     r.extra = 0;
     r.step = p.team * p.nb * 128;
     if (x.g < 0 || x.nk == 0) return r;
@@ -140,8 +159,7 @@ __device__ __forceinline__ PrefixParts prefix_parts(const PrefixWork &p, const P
     const int item = tile / p.team, member = tile - item * p.team;
     const uint32_t s0 = x.base + (static_cast<uint32_t>(kvh) * x.items + item) * x.nk, c0 = s0 / per;
     r.n = static_cast<int>((s0 + x.nk - 1) / per - c0) + 1;
-    r.extra = p.rows + ((static_cast<int64_t>(c0) * p.team + member) * p.nb + block) * 128 + (in - block * p.tok) * p.group +
-              (head - kvh * p.group);
+    r.extra = p.rows + ((c0 * p.team + member) * p.nb + block) * 128 + (in - block * p.tok) * p.group;
     return r;
 }
 
