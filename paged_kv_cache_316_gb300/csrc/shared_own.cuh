@@ -8,7 +8,9 @@
 // looks their lengths and pages up and keeps a ring of K / V tiles filled by TMA
 // across item boundaries, while four warps compute.  Two CTAs per SM, 64 KB to
 // 96 KB in flight each.  A TMA box is both halves of the head of up to 64 slots:
-// two boxes of one half each took the copy engine almost twice as long.
+// two boxes of one half each took the copy engine almost twice as long.  The
+// issue of a box takes about 200 cycles (pages of 16 slots: 8 boxes a tile), so
+// that V's are another warp's.
 //
 // The four warps share an item.  Scores of a tile: 16 keys a warp, all R =
 // group * Q rows (padded to 16 MT) as the MMA's row side; the tile's row maxima
@@ -29,7 +31,7 @@
 namespace pkv {
 
 constexpr int kOwnTile = 64;      // keys per ring stage
-constexpr int kOwnThreads = 160;  // four warps and the producer
+constexpr int kOwnThreads = 192;  // four warps, the producer, its second for V
 constexpr uint32_t kOwnBytes = kOwnTile * 256;  // a tile's K or V
 
 template <int MT>
@@ -103,6 +105,7 @@ struct OwnStage {
     int b, kvh, s, L, key0;
     int first, last, end;  // of the item; end: nothing follows
     uint32_t valid[2];     // keys of the tile that exist
+    int pages[8];          // of its boxes; pages[0] < 0: no key, nothing to copy
 };
 
 // Takes over a CTA of the grid that has not begun: the answer, 16 bytes, comes
@@ -148,14 +151,15 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t ring = smem_u32(smem), q_s = ring + C::Q, p_s = ring + C::P;
     float *red_m = reinterpret_cast<float *>(smem + C::RED), *red_l = red_m + 4 * ROWS;  // [warp][row]
-    __shared__ __align__(8) uint64_t bars[2 * ST + 3];
+    __shared__ __align__(8) uint64_t bars[3 * ST + 3];
     __shared__ __align__(16) uint4 answer_s;
     __shared__ OwnStage stage_s[ST];
     __shared__ int abort_s;
     auto b_full = [&](int s) { return smem_u32(&bars[s]); };
     auto b_empty = [&](int s) { return smem_u32(&bars[ST + s]); };
-    const uint32_t b_qfull = smem_u32(&bars[2 * ST]), b_qempty = smem_u32(&bars[2 * ST + 1]),
-                   b_answer = smem_u32(&bars[2 * ST + 2]), answer = smem_u32(&answer_s);
+    auto b_known = [&](int s) { return smem_u32(&bars[2 * ST + s]); };  // stage_s of a tile is written
+    const uint32_t b_qfull = smem_u32(&bars[3 * ST]), b_qempty = smem_u32(&bars[3 * ST + 1]),
+                   b_answer = smem_u32(&bars[3 * ST + 2]), answer = smem_u32(&answer_s);
     const PrefixWork &w = p.prefix;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();  // (the merge waits for this grid's end)
@@ -164,7 +168,8 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
     if (tid == 0) {
         for (int s = 0; s < ST; ++s) {
             mbar_init(b_full(s), 1);
-            mbar_init(b_empty(s), 4);
+            mbar_init(b_empty(s), 5);
+            mbar_init(b_known(s), 1);
         }
         mbar_init(b_qfull, 1);
         mbar_init(b_qempty, 4);
@@ -275,7 +280,10 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
                     x.valid[1] = valid[1];
                     mbar_expect_tx(b_full(st), good ? STAGE : 0u);
                 }
+                const int box_page = __shfl_sync(0xffffffffu, pages, (j0 + lane) & 31);
+                if (lane < nbox) stage_s[st].pages[lane] = good ? (box_page < 0 ? oob : box_page) : -1;
                 __syncwarp();
+                if (lane == 0) mbar_arrive(b_known(st));
                 if (good) {
 #pragma unroll 1
                     for (int j = 0; j < nbox; ++j) {
@@ -290,10 +298,8 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
                         const uint32_t dst = ring + st * STAGE + j * RB * 256;
                         if (p.ratio) {  // (the prefix's maps: groups of 8 slots, (page, head))
                             tma_load_5d(dst, &tm_k, b_full(st), 0, 0, 0, slot >> 3, page * p.ratio + kvh);
-                            tma_load_5d(dst + kOwnBytes, &tm_v, b_full(st), 0, 0, 0, slot >> 3, page * p.ratio + kvh);
                         } else {
                             tma_load_5d(dst, &tm_k, b_full(st), 0, slot, 0, kvh, page);
-                            tma_load_5d(dst + kOwnBytes, &tm_v, b_full(st), 0, slot, 0, kvh, page);
                         }
                     }
                 }
@@ -325,6 +331,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
                 ok = false;
             } else if (lane == 0) {
                 stage_s[st].end = 1;
+                mbar_arrive(b_known(st));
                 mbar_arrive(b_full(st));
             }
         }
@@ -337,6 +344,28 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
             if (!mbar_wait_drain(b_full(t % ST), (t / ST) & 1) && lane == 0) set_err(p.err, PKV_DEV_ERR_TIMEOUT);
         if (items > 0 && !mbar_wait_drain(b_qfull, (items - 1) & 1) && lane == 0) set_err(p.err, PKV_DEV_ERR_TIMEOUT);
         if (heard < asked && !mbar_wait_drain(b_answer, heard & 1) && lane == 0) set_err(p.err, PKV_DEV_ERR_TIMEOUT);
+    } else if (warp == 5) {
+        // ---- V's copies, of the tiles that the producer announces
+        const int S = 1 << p.page_shift, RB = pf_box_rows(S, kOwnTile), nbox = kOwnTile / RB;
+        for (int i = 0;; ++i) {
+            const int st = i % ST;
+            const OwnStage &x = stage_s[st];
+            if (!__all_sync(0xffffffffu, mbar_wait(b_known(st), (i / ST) & 1, abort_flag, wlim))) {
+                if (lane == 0 && !*abort_flag) give_up();
+                break;
+            }
+            if (x.end) break;
+            if (lane != 0) continue;
+#pragma unroll 1
+            for (int j = 0; j < nbox && x.pages[0] >= 0; ++j) {
+                const int slot = (x.key0 + j * RB) & (S - 1), page = x.pages[j];
+                const uint32_t dst = ring + st * STAGE + kOwnBytes + j * RB * 256;
+                if (p.ratio) tma_load_5d(dst, &tm_v, b_full(st), 0, 0, 0, slot >> 3, page * p.ratio + x.kvh);
+                else tma_load_5d(dst, &tm_v, b_full(st), 0, slot, 0, x.kvh, page);
+            }
+            mbar_arrive(b_empty(st));  // (stage_s may be written again)
+        }
+        __syncwarp();
     } else {
         // ---- the four computing warps; lane (g, c): rows 16 mt + g and + 8
         const int g = lane >> 2, c = lane & 3;
