@@ -701,8 +701,8 @@ int paged_append_rotary(const void *query, const void *key, const void *value,
 
 /*
  * paged_decode_shared_workspace_size -- bytes of device workspace
- * paged_decode_shared needs (partial outputs of the prefixes' slices and of
- * the own keys' splits); 0 for sizes it refuses.
+ * paged_decode_shared needs (partial outputs over the prefixes and the own keys'
+ * splits, fp32); 0 for sizes it refuses.
  */
 size_t paged_decode_shared_workspace_size(int32_t batch_size,
                                           int32_t q_len_per_req,
@@ -732,7 +732,10 @@ size_t paged_decode_shared_workspace_size(int32_t batch_size,
  *   workspace: >= paged_decode_shared_workspace_size(...) bytes, 256-byte
  *   aligned, always needed; calls that overlap on the GPU need one each.
  * Host errors as paged_decode's (head_dim 128, page_size a power of two from
- * 8 to 256, at most 64 rows num_qo_heads / num_kv_heads * q_len_per_req).
+ * 8 to 256, at most 64 rows num_qo_heads / num_kv_heads * q_len_per_req);
+ * prefixes of more than 2^30 steps (tiles of about 128 or 256 rows of a group
+ * x kv heads x tiles of 128 keys, by max_prefix_len) or 2^31 partial rows ->
+ * PKV_ERR_UNSUPPORTED.
  * Device errors: bad page id -> PKV_DEV_ERR_PAGE (its keys count as zeros in a
  * prefix, as none among the own keys); group_indptr out of order or beyond the
  * batch -> PKV_DEV_ERR_BATCH and no request has a prefix; a length above its

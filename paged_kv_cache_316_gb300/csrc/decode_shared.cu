@@ -161,15 +161,13 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
             for (int g = lane; g < w.G && !bad; g += 32)
                 if (w.prefix_lens[g] < 0 || w.prefix_lens[g] > w.max_prefix) set_err(w.err, PKV_DEV_ERR_LEN);
         }
-        if (lane == 0) {
-            steps_s = w0 < W ? static_cast<int>(min(per, W - w0)) : 0;
-            if (w0 < W) {
-                const uint32_t item = (w0 - at.x.base) / at.x.nk;
-                at.k = static_cast<int>((w0 - at.x.base) - item * at.x.nk);
-                at.head = static_cast<int>(item / at.x.items);
-                at.item = static_cast<int>(item - at.head * at.x.items);
-                for (int i = 0; i < THREADS / 32; ++i) walk_s[i] = at;
-            }
+        if (lane == 0) steps_s = w0 < W ? static_cast<int>(min(per, W - w0)) : 0;
+        if (w0 < W) {
+            const uint32_t item = (w0 - at.x.base) / at.x.nk;
+            at.k = static_cast<int>((w0 - at.x.base) - item * at.x.nk);
+            at.head = static_cast<int>(item / at.x.items);
+            at.item = static_cast<int>(item - at.head * at.x.items);
+            if (lane < THREADS / 32) walk_s[lane] = at;
         }
     }
     __syncthreads();

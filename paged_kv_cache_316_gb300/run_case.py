@@ -7,11 +7,16 @@
     python -m paged_kv_cache_316_gb300.run_case --op append_scaled | decode_scaled | decode_window | prefill_window
                                                 [--batch N] [--iters 3] [--d-qk 128] [--q-len 1]
 
-The second line's operators on the same workloads: the append sweep into an
+    python -m paged_kv_cache_316_gb300.run_case --op append_rotary | decode_shared | merge_states
+                                                [--batch N] [--iters 3] [--q-len 1] [--prefix 8192]
+
+The third line's operators on the same workloads: the append sweep into an
 E4M3 cache with a scale for each 16 tokens and head; the Llama-shaped decode
 over such a cache (--q-len tokens a request); the long-context decode with 64
 first tokens that stay visible; the ragged prefill under a window of 1024 keys
-with 4 first tokens.
+with 4 first tokens.  The fourth's: the append sweep with 32 query heads,
+norms and rotations; a decode of requests with up to 1024 keys of their own
+behind one shared prefix; 8192 rows from two parts of their keys.
 
 Used to drive profilers (ncu) on one kernel at a size that keeps a capture
 short; it prints the mean CUDA-event time per call, which is informational
@@ -70,12 +75,49 @@ def long_session_op(a, dev):
                                    q_len_per_req=c.q_len_per_req, **kw)
 
 
+def prefix_op(a, dev):
+    """Rotated append, decode over a shared prefix, merged states."""
+    g = wl.generator(10, dev)
+
+    def rand(*shape):
+        return torch.randn(*shape, generator=g, device=dev, dtype=torch.bfloat16)
+
+    if a.op == "append_rotary":
+        c = wl.append_sweep(a.batch or 1024, seed=1, layout=wl.NHD, device=dev, fill="empty", dtype=wl.BF16)
+        kvi, kvp, last = (x.to(dev) for x in (c.kv_indices, c.kv_indptr, c.kv_last_page_len))
+        n = c.append_key.shape[0]
+        bi, pos = pk.paged_batch_indices_positions(c.append_indptr.to(dev), pk.paged_seq_lens(kvp, last, 16), n)
+        q, w = rand(n, 32, 128), rand(2, 128)
+        f, magnitude = pk.rotary_frequencies(128, 500000.0, device=dev)
+        return lambda: pk.paged_append_rotary(q, c.append_key, c.append_value, bi, pos, c.pool.storage[0], kvi, kvp, last,
+                                              f, kv_layout="NHD", magnitude=magnitude, query_weight=w[0], key_weight=w[1])
+    if a.op == "merge_states":
+        parts = [(rand(8192, 32, 128), torch.randn(8192, 32, generator=g, device=dev)) for _ in range(2)]
+        return lambda: pk.paged_merge_states(parts)
+    B, P, S, Q = a.batch or 64, a.prefix, 16, a.q_len
+    L = wl.uniform_lengths(wl.generator(0), B, 64, 1024)
+    need = [-(-n // S) for n in [P] + L]
+    ids = torch.randperm(sum(need), generator=g, device=dev).to(torch.int32)
+    table, at = torch.zeros(1 + B, max(need), dtype=torch.int32, device=dev), 0
+    for i, n in enumerate(need):
+        table[i, :n] = ids[at:at + n]
+        at += n
+    cache, q = rand(sum(need), 2, 8, S, 128), rand(B * Q, 32, 128)
+    i32 = dict(dtype=torch.int32, device=dev)
+    ws = torch.empty(pk.paged_decode_shared_workspace_size(B, Q, 32, 8, 128, 1, P, 1024, S), dtype=torch.uint8, device=dev)
+    plen, groups, lens = torch.tensor([P], **i32), torch.tensor([0, B], **i32), torch.tensor(L, **i32)
+    return lambda: pk.paged_decode_shared(q, cache, ws, table[:1], plen, groups, P, table[1:], lens, 1024,
+                                          bmm1_scale=128 ** -0.5, q_len_per_req=Q)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--op", required=True,
                     choices=["prefill", "decode_llama", "decode_long", "decode_varlen", "append", "append_scaled",
-                             "decode_scaled", "decode_window", "prefill_window"])
-    ap.add_argument("--q-len", type=int, default=1, help="decode_scaled: query tokens per request")
+                             "decode_scaled", "decode_window", "prefill_window", "append_rotary", "decode_shared",
+                             "merge_states"])
+    ap.add_argument("--q-len", type=int, default=1, help="decode_scaled, decode_shared: query tokens per request")
+    ap.add_argument("--prefix", type=int, default=8192, help="decode_shared: keys of the shared prefix")
     ap.add_argument("--d-qk", type=int, default=128)
     ap.add_argument("--batch", type=int, default=0, help="override the workload's batch")
     ap.add_argument("--iters", type=int, default=3)
@@ -90,6 +132,8 @@ def main():
 
     if a.op in ("append_scaled", "decode_scaled", "decode_window", "prefill_window"):
         run = long_session_op(a, dev)
+    elif a.op in ("append_rotary", "decode_shared", "merge_states"):
+        run = prefix_op(a, dev)
     elif a.op == "prefill":
         e4 = a.kv_dtype == "e4m3"  # E4M3 query and caches, unit device scales
         kw = dict(q_dtype=wl.E4M3, kv_dtype=wl.E4M3) if e4 else {}
