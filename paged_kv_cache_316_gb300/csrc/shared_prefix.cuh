@@ -125,9 +125,9 @@ __device__ __forceinline__ void scan_prefixes(const PrefixWork &p, G total, F ma
 // few steps that half of the SMs have one each are not put together.  Every
 // CTA of the prefix kernel works it out alike; the kernel that joins reads it.
 __device__ __forceinline__ uint32_t prefix_steps_per_team(const PrefixWork &p, uint32_t W) {
-    const uint32_t w = W * p.team;
-    if (W == 0) return 1;
-    if (2 * w <= static_cast<uint32_t>(p.sms)) return 1;
+    const uint32_t least = (W + p.ctas / p.team - 1) / (p.ctas / p.team);
+    const uint64_t w = static_cast<uint64_t>(W) * p.team;
+    if (2 * w <= static_cast<uint32_t>(p.sms)) return max(least, 1u);
     const int lane = threadIdx.x & 31, n = min(p.B, 256), of = p.B / n;
     float sum = 0.f;
     for (int i = lane; i < n; i += 32)
@@ -138,7 +138,7 @@ __device__ __forceinline__ uint32_t prefix_steps_per_team(const PrefixWork &p, u
     const float half = 0.5f * (steps + A - kShCtaSteps * S);
     const float N = (sqrtf(half * half + kShCtaSteps * steps * S) - half) / kShCtaSteps;
     const uint32_t teams = max(1u, min(static_cast<uint32_t>(N), static_cast<uint32_t>(p.ctas)) / p.team);
-    return (W + teams - 1) / teams;
+    return max(least, (W + teams - 1) / teams);
 }
 
 // The partials of a token's rows at one kv head: the first at `row` (of the
