@@ -11,19 +11,37 @@
 //           streaming; it does not wait for the first grid but runs beside it;
 //   shared_merge_kernel   joins the partials of both.
 //
-// The prefix kernel.  One CTA per SM takes an even share of the steps (see
+// The prefix kernel.  One CTA on each of the SMs that the prefixes' work is
+// worth (prefix_steps_per_team) takes an even share of the steps (see
 // shared_prefix.cuh), item by item: NB blocks of 128 rows (row = token * group
 // + head; a block holds as many whole tokens as fit) and one kv head, so that
 // a K / V tile in shared memory serves 128 NB rows.  Warps 0 .. 4 NB - 1 are
 // the softmax, one thread a row: scores read from TMEM once, running maximum
 // in base 2 that rises only where a tile's exceeds it by more than 2^8, P
 // written as 16-bit pairs over the consumed scores, the A operand of the PV
-// MMA, whose first half of the keys begins while the second's P is made.  Then a TMA warp for Q and K, the MMA warp, a TMA warp for V, and an
-// idle one.  With two blocks the MMAs alternate (QK_A QK_B, then PV_A(t)
+// MMA, whose first half of the keys begins while the second's P is made.  Then
+// a TMA warp for Q and K, the MMA warp, a TMA warp for V, and an idle one.
+// With two blocks the MMAs alternate (QK_A QK_B, then PV_A(t)
 // QK_A(t+1) PV_B(t) QK_B(t+1)), so that the tensor core works for one block
 // while the softmax of the other runs.  The K / V ring runs on from one item
 // into the next; the next Q comes as soon as the last QK has read this one.
 // Every wait is bounded.
+//
+// A step (2 x 128 rows, 128 keys) takes 2,800 cycles, its MMAs 2,048: scores -
+// maximum - exponentials - P of a row in one thread are 1,400, and two blocks
+// do not hide all of it.  Tried: two threads to a row, both finding its maximum
+// (290 us of the third case's prefix against 206: 96 registers a thread, and the
+// maximum's work twice); the first half's P from the last tile's maximum while
+// this one's is found (204, and short prefixes 2 to 5% slower); two stages of K
+// (2,930 cycles, waiting for L2); P in one piece (169 us against 166 on all
+// SMs); boxes of one half of the head (190 against 176).
+//
+// Times of the call replayed from a graph (floor of bytes at 6788 GB/s or
+// operations at 1912 TFLOP/s): 64 requests behind 8,192 keys, 64 to 1024 of
+// their own, 32 / 8 heads: 46 us (27); 45 requests of 4 tokens behind three
+// prefixes of up to 16,001, 28 / 4 heads, fp16: 42.5 (10); 256 behind 32,768,
+// 64 / 8 heads: 219 (145), 206 of them the prefix on 120 SMs, own keys beside
+// it on 32; 4 behind 512: 10.4.
 //
 // Roundings: P to the caches' 16-bit type for its product with V, the output
 // once at the end; scores, maxima, sums, O, the partials and the LSE are fp32.

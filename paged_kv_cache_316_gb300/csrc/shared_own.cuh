@@ -20,6 +20,11 @@
 // to partials, so that no item waits for the prefix, and shared_merge_kernel
 // joins them with the prefix's.
 //
+// Alone on all SMs: 290 MB of 256 requests' 264 keys in 55 us (5.3 TB/s, 78% of
+// the copy rate), 149 MB of 64 requests' 544 in 33: the first tile comes after
+// 4 us (length, page ids, data), the last items end unevenly, and an item's
+// claim takes 1 to 2 us.  Beside the prefix an SM streams 35 to 45 GB/s.
+//
 // Every wait is bounded; a warp whose wait ran out says so in the barrier that
 // all four meet at next, so that they leave together.
 #pragma once

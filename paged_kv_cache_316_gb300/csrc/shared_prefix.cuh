@@ -124,6 +124,9 @@ __device__ __forceinline__ void scan_prefixes(const PrefixWork &p, G total, F ma
 // streamed in about a step; of more than 256 requests, 256 stand for all.  So
 // few steps that half of the SMs have one each are not put together.  Every
 // CTA of the prefix kernel works it out alike; the kernel that joins reads it.
+// Against all SMs for the prefix first: 220 us for 226 (256 requests behind
+// 32,768 keys), 46 for 50 (64 behind 8,192), 42.5 for 45 (45 of 4 tokens in
+// three groups); A from 0.8 to 1 of this the same, from 0.7 or 1.5 slower.
 __device__ __forceinline__ uint32_t prefix_steps_per_team(const PrefixWork &p, uint32_t W) {
     const uint32_t least = (W + p.ctas / p.team - 1) / (p.ctas / p.team);
     const uint64_t w = static_cast<uint64_t>(W) * p.team;
