@@ -164,11 +164,12 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
         bool bad;
         const uint32_t team = blockIdx.x / w.team;
         uint32_t W = 0, per = 1, w0 = 0;
+        const OwnLengths own = own_lengths(w);
         scan_prefixes(
             w,
             [&](uint32_t all) {
                 W = all;
-                per = prefix_steps_per_team(w, all);
+                per = prefix_steps_per_team(w, all, own);
                 w0 = team * per;
             },
             [&](int, int, uint32_t first, uint32_t n) { return w0 >= first && w0 - first < n; }, at.x, bad);

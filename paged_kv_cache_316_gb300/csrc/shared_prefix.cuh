@@ -127,17 +127,29 @@ __device__ __forceinline__ void scan_prefixes(const PrefixWork &p, G total, F ma
 // Against all SMs for the prefix first: 220 us for 226 (256 requests behind
 // 32,768 keys), 46 for 50 (64 behind 8,192), 42.5 for 45 (45 of 4 tokens in
 // three groups); A from 0.8 to 1 of this the same, from 0.7 or 1.5 slower.
-__device__ __forceinline__ uint32_t prefix_steps_per_team(const PrefixWork &p, uint32_t W) {
+// The lengths are fetched first, beside the groups that W is found from.
+struct OwnLengths {
+    uint32_t x[8];  // of requests (lane + 32 i) * of
+    int of;
+};
+__device__ __forceinline__ OwnLengths own_lengths(const PrefixWork &p) {
+    const int lane = threadIdx.x & 31, n = min(p.B, 256);
+    OwnLengths r;
+    r.of = p.B / n;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.x[i] = lane + 32 * i < n ? p.seq_lens[(lane + 32 * i) * r.of] : 0u;
+    return r;
+}
+__device__ __forceinline__ uint32_t prefix_steps_per_team(const PrefixWork &p, uint32_t W, const OwnLengths &own) {
     const uint32_t least = (W + p.ctas / p.team - 1) / (p.ctas / p.team);
     const uint64_t w = static_cast<uint64_t>(W) * p.team;
     if (2 * w <= static_cast<uint32_t>(p.sms)) return max(least, 1u);
-    const int lane = threadIdx.x & 31, n = min(p.B, 256), of = p.B / n;
     float sum = 0.f;
-    for (int i = lane; i < n; i += 32)
-        sum += static_cast<float>(min(p.seq_lens[i * of], static_cast<uint32_t>(p.max_seq_len)));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += static_cast<float>(min(own.x[i], static_cast<uint32_t>(p.max_seq_len)));
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float A = sum * static_cast<float>(of * p.Hkv) / kShTile, S = static_cast<float>(p.sms), steps = static_cast<float>(w);
+    const float A = sum * static_cast<float>(own.of * p.Hkv) / kShTile, S = static_cast<float>(p.sms), steps = static_cast<float>(w);
     const float half = 0.5f * (steps + A - kShCtaSteps * S);
     const float N = (sqrtf(half * half + kShCtaSteps * steps * S) - half) / kShCtaSteps;
     const uint32_t teams = max(1u, min(static_cast<uint32_t>(N), static_cast<uint32_t>(p.ctas)) / p.team);
