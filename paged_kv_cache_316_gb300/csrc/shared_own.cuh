@@ -359,7 +359,9 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
                 if (lane == 0 && !*abort_flag) give_up();
                 break;
             }
-            if (x.end) break;
+            const bool end = x.end;
+            __syncwarp();  // (all lanes have read the record; from lane 0's arrival on it may be written again)
+            if (end) break;
             if (lane != 0) continue;
 #pragma unroll 1
             for (int j = 0; j < nbox && x.pages[0] >= 0; ++j) {
