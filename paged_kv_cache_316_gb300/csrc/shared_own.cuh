@@ -156,15 +156,16 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t ring = smem_u32(smem), q_s = ring + C::Q, p_s = ring + C::P;
     float *red_m = reinterpret_cast<float *>(smem + C::RED), *red_l = red_m + 4 * ROWS;  // [warp][row]
-    __shared__ __align__(8) uint64_t bars[3 * ST + 3];
+    __shared__ __align__(8) uint64_t bars[4 * ST + 3];
     __shared__ __align__(16) uint4 answer_s;
     __shared__ OwnStage stage_s[ST];
     __shared__ int abort_s;
-    auto b_full = [&](int s) { return smem_u32(&bars[s]); };
+    auto b_full = [&](int s) { return smem_u32(&bars[s]); };            // K has landed, or nothing follows
+    auto b_vfull = [&](int s) { return smem_u32(&bars[3 * ST + s]); };  // V has landed
     auto b_empty = [&](int s) { return smem_u32(&bars[ST + s]); };
     auto b_known = [&](int s) { return smem_u32(&bars[2 * ST + s]); };  // stage_s of a tile is written
-    const uint32_t b_qfull = smem_u32(&bars[3 * ST]), b_qempty = smem_u32(&bars[3 * ST + 1]),
-                   b_answer = smem_u32(&bars[3 * ST + 2]), answer = smem_u32(&answer_s);
+    const uint32_t b_qfull = smem_u32(&bars[4 * ST]), b_qempty = smem_u32(&bars[4 * ST + 1]),
+                   b_answer = smem_u32(&bars[4 * ST + 2]), answer = smem_u32(&answer_s);
     const PrefixWork &w = p.prefix;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();  // (the merge waits for this grid's end)
@@ -175,6 +176,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
             mbar_init(b_full(s), 1);
             mbar_init(b_empty(s), 5);
             mbar_init(b_known(s), 1);
+            mbar_init(b_vfull(s), 1);
         }
         mbar_init(b_qfull, 1);
         mbar_init(b_qempty, 4);
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
                     x.end = 0;
                     x.valid[0] = valid[0];
                     x.valid[1] = valid[1];
-                    mbar_expect_tx(b_full(st), good ? STAGE : 0u);
+                    mbar_expect_tx(b_full(st), good ? kOwnBytes : 0u);
                 }
                 const int box_page = __shfl_sync(0xffffffffu, pages, (j0 + lane) & 31);
                 if (lane < nbox) stage_s[st].pages[lane] = good ? (box_page < 0 ? oob : box_page) : -1;
@@ -342,8 +344,8 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
         }
         if (!ok && lane == 0) give_up();
         __syncwarp();
-        // every copy and answer lands before the CTA exits (the tile whose stage
-        // the end took was consumed before)
+        // every copy that this warp issued and the answer land before the CTA
+        // exits (the tile whose stage the end took was consumed before)
         const int open = ok ? ST - 1 : ST;
         for (int t = i > open ? i - open : 0; t < i; ++t)
             if (!mbar_wait_drain(b_full(t % ST), (t / ST) & 1) && lane == 0) set_err(p.err, PKV_DEV_ERR_TIMEOUT);
@@ -352,7 +354,8 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
     } else if (warp == 5) {
         // ---- V's copies, of the tiles that the producer announces
         const int S = 1 << p.page_shift, RB = pf_box_rows(S, kOwnTile), nbox = kOwnTile / RB;
-        for (int i = 0;; ++i) {
+        int i = 0;  // tiles whose V is on its way
+        for (;; ++i) {
             const int st = i % ST;
             const OwnStage &x = stage_s[st];
             if (!__all_sync(0xffffffffu, mbar_wait(b_known(st), (i / ST) & 1, abort_flag, wlim))) {
@@ -363,16 +366,21 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
             __syncwarp();  // (all lanes have read the record; from lane 0's arrival on it may be written again)
             if (end) break;
             if (lane != 0) continue;
+            mbar_expect_tx(b_vfull(st), x.pages[0] >= 0 ? kOwnBytes : 0u);
 #pragma unroll 1
             for (int j = 0; j < nbox && x.pages[0] >= 0; ++j) {
                 const int slot = (x.key0 + j * RB) & (S - 1), page = x.pages[j];
                 const uint32_t dst = ring + st * STAGE + kOwnBytes + j * RB * 256;
-                if (p.ratio) tma_load_5d(dst, &tm_v, b_full(st), 0, 0, 0, slot >> 3, page * p.ratio + x.kvh);
-                else tma_load_5d(dst, &tm_v, b_full(st), 0, slot, 0, x.kvh, page);
+                if (p.ratio) tma_load_5d(dst, &tm_v, b_vfull(st), 0, 0, 0, slot >> 3, page * p.ratio + x.kvh);
+                else tma_load_5d(dst, &tm_v, b_vfull(st), 0, slot, 0, x.kvh, page);
             }
             mbar_arrive(b_empty(st));  // (stage_s may be written again)
         }
         __syncwarp();
+        // V's copies land before the CTA exits: this warp waits for those that
+        // it issued, and for no tile that was announced after it gave up
+        for (int t = i > ST ? i - ST : 0; t < i; ++t)
+            if (!mbar_wait_drain(b_vfull(t % ST), (t / ST) & 1) && lane == 0) set_err(p.err, PKV_DEV_ERR_TIMEOUT);
     } else {
         // ---- the four computing warps; lane (g, c): rows 16 mt + g and + 8
         const int g = lane >> 2, c = lane & 3;
@@ -478,8 +486,9 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                         if (c == 0) red_m[warp * ROWS + 16 * mt + g + 8 * f] = top;
                     }
+                ok = wait_warp(b_vfull(st), (i / ST) & 1);
                 // values of rows without a key may be anything: zeroed, so that P = 0 cannot make 0 * NaN
-                if (!whole)
+                if (ok && !whole)
                     for (int q = tid; q < kOwnTile * 16; q += 128) {
                         const int row = q >> 4, ch = q & 15;
                         if (!(((row < 32 ? v0 : v1) >> (row & 31)) & 1u))
