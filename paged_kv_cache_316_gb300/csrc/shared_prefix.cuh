@@ -121,23 +121,27 @@ __device__ __forceinline__ void scan_prefixes(const PrefixWork &p, G total, F ma
 // steps: both are done at the same time T, and S SMs busy until then, if
 //   T = C + W / N,  S T = C N + W + A,  so  C N^2 + (W + A - C S) N - W S = 0
 // (W the CTAs' steps; N = S without own keys).  A: 128 own keys of a head are
-// streamed in about a step; of more than 256 requests, 256 stand for all.  So
-// few steps that half of the SMs have one each are not put together.  Every
-// CTA of the prefix kernel works it out alike; the kernel that joins reads it.
+// streamed in about a step; of more than 256 requests, 256 spread evenly over
+// the batch stand for all.  So few steps that half of the SMs have one each are
+// not put together.  Every CTA of the prefix kernel works it out alike; the
+// kernel that joins reads it.
 // Against all SMs for the prefix first: 220 us for 226 (256 requests behind
 // 32,768 keys), 46 for 50 (64 behind 8,192), 42.5 for 45 (45 of 4 tokens in
 // three groups); A from 0.8 to 1 of this the same, from 0.7 or 1.5 slower.
 // The lengths are fetched first, beside the groups that W is found from.
 struct OwnLengths {
-    uint32_t x[8];  // of requests (lane + 32 i) * of
-    int of;
+    uint32_t x[8];  // of n = min(B, 256) requests, the (lane + 32 i)-th of them
+    float each;     // requests that one stands for, B / n
 };
 __device__ __forceinline__ OwnLengths own_lengths(const PrefixWork &p) {
     const int lane = threadIdx.x & 31, n = min(p.B, 256);
     OwnLengths r;
-    r.of = p.B / n;
+    r.each = p.B > 256 ? static_cast<float>(p.B) / 256.f : 1.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r.x[i] = lane + 32 * i < n ? p.seq_lens[(lane + 32 * i) * r.of] : 0u;
+    for (int i = 0; i < 8; ++i) {
+        const int k = lane + 32 * i, b = p.B > 256 ? (k * p.B) >> 8 : k;  // (k B / n; B < 2^16)
+        r.x[i] = k < n ? p.seq_lens[b] : 0u;
+    }
     return r;
 }
 __device__ __forceinline__ uint32_t prefix_steps_per_team(const PrefixWork &p, uint32_t W, const OwnLengths &own) {
@@ -149,7 +153,7 @@ __device__ __forceinline__ uint32_t prefix_steps_per_team(const PrefixWork &p, u
     for (int i = 0; i < 8; ++i) sum += static_cast<float>(min(own.x[i], static_cast<uint32_t>(p.max_seq_len)));
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float A = sum * static_cast<float>(own.of * p.Hkv) / kShTile, S = static_cast<float>(p.sms), steps = static_cast<float>(w);
+    const float A = sum * own.each * static_cast<float>(p.Hkv) / kShTile, S = static_cast<float>(p.sms), steps = static_cast<float>(w);
     const float half = 0.5f * (steps + A - kShCtaSteps * S);
     const float N = (sqrtf(half * half + kShCtaSteps * steps * S) - half) / kShCtaSteps;
     const uint32_t teams = max(1u, min(static_cast<uint32_t>(N), static_cast<uint32_t>(p.ctas)) / p.team);
