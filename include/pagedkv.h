@@ -702,7 +702,9 @@ int paged_append_rotary(const void *query, const void *key, const void *value,
 /*
  * paged_decode_shared_workspace_size -- bytes of device workspace
  * paged_decode_shared needs (partial outputs over the prefixes and the own keys'
- * splits, fp32); 0 for sizes it refuses.
+ * splits, fp32); 0 for sizes it refuses.  A call with the same heads and no more
+ * requests, tokens, groups, prefix keys and own keys needs no more: a workspace
+ * reserved for the largest of each holds them all.
  */
 size_t paged_decode_shared_workspace_size(int32_t batch_size,
                                           int32_t q_len_per_req,

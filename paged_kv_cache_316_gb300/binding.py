@@ -689,6 +689,8 @@ def paged_decode_noalloc(query, kv_cache, block_tables, seq_lens, max_seq_len: i
 
 def paged_decode_shared_workspace_size(batch_size, q_len_per_req, num_qo_heads, num_kv_heads, head_dim, num_groups,
                                        max_prefix_len, max_seq_len, page_size) -> int:
+    """Bytes of paged_decode_shared's workspace.  One for the largest batch_size,
+    q_len_per_req, num_groups and lengths of a server holds every smaller call."""
     return int(load_library().paged_decode_shared_workspace_size(
         batch_size, q_len_per_req, num_qo_heads, num_kv_heads, head_dim, num_groups, max_prefix_len, max_seq_len,
         page_size))

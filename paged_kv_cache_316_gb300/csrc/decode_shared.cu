@@ -565,8 +565,35 @@ struct SharedPlan {
     int nb, tok, team, ctas;
     int64_t rows, parts;
     int64_t all;         // partial rows: the prefix's, then the own keys'
-    size_t lse, per, bytes;  // offsets in the workspace
+    size_t lse, per, bytes;  // offsets in the workspace, its size
 };
+
+// The workspace is as large as the largest call with no more of anything
+// (requests, tokens, groups, keys) needs, so that one reserved for a server's
+// maxima holds every smaller call; the calls themselves do not need more with
+// more keys always: splits of own keys get longer, a second block of rows
+// halves the tiles, teams leave CTAs out.  So the rows are counted by bounds
+// that grow with each size:
+//   own keys: (request, kv head) pairs times splits of c keys, c >= max(256,
+//     min(X / K, 4096)) (plan_shared) with X the keys of all pairs and K =
+//     10 SMs: at most a split more for each pair than X / c;
+//   prefix: a CTA holds up to nb blocks of 128 rows; blocks of full tiles,
+//     2 more for each group, and never more than 2 for each token or SM.
+static int64_t most_partials(const SharedPlan &pl, int64_t B, int64_t Hkv, int64_t tokens, int64_t G, int64_t max_seq_len,
+                             int64_t nk) {
+    const int64_t sms = num_sms(), K = kOwnItems * 2 * sms, X = B * Hkv * max_seq_len;
+    auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    // (X / floor(X / K) <= K + K / 256 + 1 where X / K >= 256)
+    int64_t splits = up(X, 256) < K + K / 256 + 1 ? up(X, 256) : K + K / 256 + 1;
+    if (splits < up(X, 4096)) splits = up(X, 4096);
+    splits += B * Hkv;
+    const int64_t short_splits = B * Hkv * own_splits(static_cast<int>(max_seq_len), 256);
+    if (splits > short_splits) splits = short_splits;
+    int64_t blocks = up(tokens, pl.tok) + 2 * G;
+    if (blocks > 2 * tokens) blocks = 2 * tokens;
+    blocks = G > 0 && nk > 0 ? (blocks * Hkv * nk < 2 * sms ? blocks * Hkv * nk : 2 * sms) : 0;
+    return (blocks > 0 ? pl.rows : 0) + blocks * 128 + splits * pl.R;
+}
 
 static int plan_shared(int B, int Q, int Hqo, int Hkv, int D, int G, int max_prefix, int max_seq_len, int page_size,
                        SharedPlan &pl) {
@@ -616,8 +643,9 @@ static int plan_shared(int B, int Q, int Hqo, int Hkv, int D, int G, int max_pre
     pl.all = pl.parts + static_cast<int64_t>(B) * Hkv * pl.n_split_max * pl.R;
     if (pl.all > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
     pl.lse = static_cast<size_t>(pl.all) * kShD * sizeof(float);
-    pl.per = pl.lse + round_up(static_cast<size_t>(pl.all) * sizeof(float), 256);
-    pl.bytes = pl.all > 0 ? pl.per + 256 : 0;
+    const size_t most_rows = static_cast<size_t>(most_partials(pl, B, Hkv, tokens, G, max_seq_len, nk));
+    pl.per = round_up(most_rows * (kShD + 1) * sizeof(float), 256);
+    pl.bytes = most_rows > 0 ? pl.per + 256 : 0;
     return PKV_OK;
 }
 
