@@ -738,6 +738,10 @@ size_t paged_decode_shared_workspace_size(int32_t batch_size,
  * prefixes of more than 2^30 steps (tiles of about 128 or 256 rows of a group
  * x kv heads x tiles of 128 keys, by max_prefix_len) or 2^31 partial rows ->
  * PKV_ERR_UNSUPPORTED.
+ * A NaN or infinity in a key or value has no effect on tokens that do not see
+ * it.  A NaN key, or a logit of plus infinity, makes the rows that see it NaN,
+ * out and lse; a NaN in a value that column of their out, an infinity infinite
+ * or NaN, lse not.
  * Device errors: bad page id -> PKV_DEV_ERR_PAGE (its keys count as zeros in a
  * prefix, as none among the own keys); group_indptr out of order or beyond the
  * batch -> PKV_DEV_ERR_BATCH and no request has a prefix; a length above its

@@ -687,9 +687,9 @@ static int launch_prefix(const SharedMaps &m, const SharedParams &p, dim3 grid, 
     return PKV_OK;
 }
 
-template <typename T, int MT>
+template <typename T, int MT, bool DRAFTS>
 static int launch_own(const SharedMaps &m, const OwnParams &p, dim3 grid, cudaStream_t st) {
-    auto kern = shared_own_kernel<T, MT>;
+    auto kern = shared_own_kernel<T, MT, DRAFTS>;
     constexpr int smem = static_cast<int>(OwnCfg<MT>::SMEM);
     static std::atomic<unsigned long long> set{0};
     if (!allow_smem(kern, smem, set)) return PKV_ERR_CUDA;
@@ -711,8 +711,12 @@ static int run_shared(const SharedMaps &m, const SharedParams &s, const OwnParam
         ++launches;
     }
     const dim3 grid(pl.n_split_max, p.prefix.Hkv, p.prefix.B);
-    rc = pl.MT == 1 ? launch_own<T, 1>(m, p, grid, st)
-                    : (pl.MT == 2 ? launch_own<T, 2>(m, p, grid, st) : launch_own<T, 4>(m, p, grid, st));
+    if (p.prefix.Q == 1)
+        rc = pl.MT == 1 ? launch_own<T, 1, false>(m, p, grid, st)
+                        : (pl.MT == 2 ? launch_own<T, 2, false>(m, p, grid, st) : launch_own<T, 4, false>(m, p, grid, st));
+    else
+        rc = pl.MT == 1 ? launch_own<T, 1, true>(m, p, grid, st)
+                        : (pl.MT == 2 ? launch_own<T, 2, true>(m, p, grid, st) : launch_own<T, 4, true>(m, p, grid, st));
     if (rc != PKV_OK) return rc;
     const int64_t warps = pl.rows / p.prefix.group * ((p.prefix.group + p.merge_rows - 1) / p.merge_rows);
     if (launch_dependent(shared_merge_kernel<T>, dim3(static_cast<unsigned>((warps + 3) / 4)), dim3(128), 0, st, p) !=

@@ -145,7 +145,61 @@ __device__ __forceinline__ bool own_sync(bool yes) {
     return all != 0;
 }
 
-template <typename T, int MT>
+// The newest keys of a tile, of which token t sees those up to pos + t, `left`
+// of the tile being the request's: the weights of hidden ones are 0, and 0 times
+// a NaN or an infinity is not 0.  Values that are neither are left to the MMA;
+// the others (drafts gone wrong; hardly ever one) are multiplied here for the
+// rows that see them and zeroed.  A warp does its own 32 dimensions, from which
+// no other reads; true if it wrote zeros.
+template <typename T, int MT, typename At>
+__device__ __forceinline__ bool hidden_values(uint8_t *v, const uint8_t *weights, At at, const int (&tq)[MT][2], int pos, int left,
+                                              float (&o)[MT][4][4]) {
+    constexpr uint32_t kExp = IsBf16<T>::value ? 0x7f80u : 0x7c00u;  // the exponent of one that is not finite
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+    const int j0 = max(pos + 1, 0), j1 = min(left, kOwnTile);
+    auto word = [&](int j, int n) { return reinterpret_cast<uint32_t *>(v + at(j, 4 * warp + n) + 4 * c); };
+    auto odd = [&](uint32_t x) { return (x & kExp) == kExp; };
+    bool any = false;
+    for (int j = j0 + g; j < j1; j += 8)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const uint32_t x = *word(j, n);
+            any |= odd(x) || odd(x >> 16);
+        }
+    if (!__any_sync(0xffffffffu, any)) return false;
+#pragma unroll 1
+    for (int j = j0; j < j1; ++j)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                if (j > pos + tq[mt][f]) continue;
+                const int row = 16 * mt + g + 8 * f;
+                const T w = *reinterpret_cast<const T *>(weights + row * 128 + (((j >> 3) ^ (row & 7)) << 4) + 2 * (j & 7));
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const uint32_t x = *word(j, n);
+                    const float2 y = unpack2<T>(x);
+                    if (odd(x)) o[mt][n][2 * f] += static_cast<float>(w) * y.x;
+                    if (odd(x >> 16)) o[mt][n][2 * f + 1] += static_cast<float>(w) * y.y;
+                }
+            }
+    __syncwarp();
+    for (int j = j0 + g; j < j1; j += 8)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const uint32_t x = *word(j, n);
+            if (odd(x) || odd(x >> 16)) *word(j, n) = (odd(x) ? 0u : x & 0xffffu) | (odd(x >> 16) ? 0u : x & 0xffff0000u);
+        }
+    __syncwarp();
+    return true;
+}
+
+// DRAFTS: several tokens to a request, some of whose keys the others do not see.
+// (A kernel of its own for one token: the code for several, which it never
+// reaches, cost the smallest call 0.4 us of 10.9.  With it, three groups of
+// requests of four tokens take the 43.3 us that they took without.)
+template <typename T, int MT, bool DRAFTS>
 __global__ void __launch_bounds__(kOwnThreads, 2)
     shared_own_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ OwnParams p) {
@@ -410,7 +464,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
             bool ok = wait_warp(b_full(st), (i / ST) & 1);
             const bool end = ok && x.end;
             float sv[MT][2][4];
-            bool whole = true;
+            bool whole = true, hides = false;
             if (ok && !end) {
                 if (x.first) {
                     ok = wait_warp(b_qfull, items & 1);
@@ -464,6 +518,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
                 }
                 const uint32_t v0 = x.valid[0], v1 = x.valid[1];
                 whole = (v0 & v1) == 0xffffffffu;
+                if constexpr (DRAFTS) hides = x.key0 + kOwnTile - 1 > x.L - w.Q;  // keys that some tokens do not see
                 const bool plain = whole && x.key0 + kOwnTile - 1 <= x.L - w.Q;
                 const uint32_t mine = (warp < 2 ? v0 : v1) >> (16 * (warp & 1));  // this warp's 16 keys
                 const int pos = x.L - w.Q - x.key0 - 16 * warp;                   // token 0's newest key among them
@@ -525,6 +580,11 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
                     }
                 }
             named_bar_sync(1, 128);
+            bool zeroed = false;
+            if constexpr (DRAFTS)
+                if (hides)
+                    zeroed = hidden_values<T, MT>(smem + st * STAGE + kOwnBytes, smem + C::P, at, tq, x.L - w.Q - x.key0,
+                                                  x.L - x.key0, o);
             // O += P V of this warp's 32 dimensions
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
@@ -545,7 +605,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
             }
             const bool last = x.last;
             const int b = x.b, kvh = x.kvh, s = x.s;
-            if (!whole) fence_proxy_async_smem();  // (zeros written before the next copy into the stage)
+            if (!whole || zeroed) fence_proxy_async_smem();  // (zeros written before the next copy into the stage)
             __syncwarp();
             if (lane == 0) mbar_arrive(b_empty(st));
             if (!last) continue;
