@@ -407,10 +407,11 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling=None, fac
       None      as they are;
       "linear"  f_i / factor (positions interpolated);
       "ntk"     base * factor^(rotary_dim / (rotary_dim - 2)) in place of base;
-      "yarn"    f_i of pairs that turn more than `fast` times over
-                trained_len kept, of those below `slow` turns divided by
-                factor, a linear ramp in the number of turns between them;
-                magnitude 0.1 ln(factor) + 1."""
+      "yarn"    pairs up to the one that turns `fast` times over trained_len
+                (its index rounded down) kept, from the one that turns `slow`
+                times (rounded up) on divided by factor, a linear ramp in the
+                pair's index between them, as the models trained with this
+                scaling have it; magnitude 0.1 ln(factor) + 1."""
     if rotary_dim <= 0 or rotary_dim % 2 or not base > 0 or not factor >= 1:
         raise PagedKVError("rotary_dim must be positive and even, base positive and factor at least 1")
     n = rotary_dim // 2
@@ -423,10 +424,13 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling=None, fac
     if scaling == "linear":
         f = f / factor
     elif scaling == "yarn":
-        if trained_len is None or trained_len <= 0 or not fast > slow:
-            raise PagedKVError("yarn scaling needs trained_len, and fast above slow")
-        keep = ((trained_len * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
-        f = f * (keep + (1 - keep) / factor)
+        if trained_len is None or trained_len <= 0 or not fast > slow > 0 or not base > 1:
+            raise PagedKVError("yarn scaling needs trained_len, fast above slow above 0, and a base above 1")
+        # the pair that turns r times: trained_len base^(-i / n) / (2 pi) = r
+        at = [n * math.log(trained_len / (2 * math.pi * turns)) / math.log(base) for turns in (fast, slow)]
+        first, last = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rotary_dim - 1)
+        share = ((torch.arange(n, dtype=torch.float64) - first) / max(last - first, 1e-3)).clamp(0, 1)
+        f = f * ((1 - share) + share / factor)
         magnitude = 0.1 * math.log(factor) + 1.0
     elif scaling not in (None, "ntk"):
         raise PagedKVError(f"unknown scaling {scaling!r}")
