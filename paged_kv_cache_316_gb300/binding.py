@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import threading
 
 import torch
 
@@ -23,6 +24,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libpagedkv.so"
 _lib = None
 _calls = None  # _calls.so, with the addresses of _lib's entry points
+_loading = threading.RLock()  # what is loaded is published when it can be called
 
 _c_p = ctypes.c_void_p
 _i32 = ctypes.c_int32
@@ -102,8 +104,12 @@ def load_library(path: str | None = None):
     With `path`, load that build of the library instead and route every later
     call to it (e.g. the range-checking libpagedkv_debug.so; passing
     library_path() switches back)."""
-    global _lib, _calls
-    if _lib is None or path is not None:
+    global _lib
+    if _lib is not None and path is None:
+        return _lib
+    with _loading:
+        if _lib is not None and path is None:
+            return _lib
         path = path or library_path()
         if not os.path.exists(path):
             raise PagedKVError(
@@ -114,17 +120,17 @@ def load_library(path: str | None = None):
             fn = getattr(lib, name)
             fn.argtypes = args
             fn.restype = res
-        try:
-            from . import _calls as calls
-        except ImportError as e:
-            raise PagedKVError("_calls.so is not built for this interpreter and torch: run "
-                               f"`python -m paged_kv_cache_316_gb300.build` first ({e})") from None
+        if _calls is not None:
+            _hand_over(_calls, lib)
         _lib = lib
-        calls.use(PagedKVError, _check, *(ctypes.cast(getattr(lib, f), _c_p).value for f in
-                                          ("paged_rotary", "paged_append_rotary", "paged_decode_shared",
-                                           "paged_merge_states")))
-        _calls = calls
-    return _lib
+        return lib
+
+
+def _hand_over(calls, lib):
+    """The C++ binding calls this build's entry points from now on."""
+    calls.use(PagedKVError, _check, *(ctypes.cast(getattr(lib, f), _c_p).value for f in
+                                      ("paged_rotary", "paged_append_rotary", "paged_decode_shared",
+                                       "paged_merge_states")))
 
 
 def debug_bounds() -> bool:
@@ -438,10 +444,20 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling=None, fac
 
 
 def _native():
-    """_calls.so, once the library is loaded."""
-    if _calls is None:
-        load_library()
-    return _calls
+    """_calls.so, which the calls below go through, with the library's entry
+    points.  (The other calls need the library alone.)"""
+    global _calls
+    with _loading:
+        lib = load_library()
+        if _calls is None:
+            try:
+                from . import _calls as calls
+            except ImportError as e:
+                raise PagedKVError("_calls.so is not built for this interpreter and torch: run "
+                                   f"`python -m paged_kv_cache_316_gb300.build` first ({e})") from None
+            _hand_over(calls, lib)
+            _calls = calls
+        return _calls
 
 
 def _stream_arg(stream):
