@@ -11,7 +11,10 @@ and no libcuda at link time).  The debug variant, libpagedkv_debug.so
 before use (the PKV_DEV_ERR_BOUNDS bit of the error word).
 
 _calls.so, the part of the Python binding that is C++ (csrc/calls.cpp), is
-compiled beside them with g++ against the installed torch's headers.
+compiled beside them with g++ against the installed torch's headers.  Its name
+carries the interpreter's ABI tag, it refuses to be imported under another
+torch, and it is compiled again when the command that made it (torch's version
+and paths, the flags) changes.
 """
 from __future__ import annotations
 
@@ -28,7 +31,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpagedkv.so")
 LIB_DEBUG = os.path.join(HERE, "libpagedkv_debug.so")
-LIB_CALLS = os.path.join(HERE, "_calls.so")
+LIB_CALLS = os.path.join(HERE, "_calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+CALLS_STAMP = os.path.join(BUILD, "calls.stamp")  # the command that made it
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -101,28 +105,41 @@ def _finish(objs, lib, procs, force: bool, ptxas_verbose: bool, quiet: bool) -> 
 
 def _start_calls(force: bool):
     """Start the compilation of _calls.so if it is stale; returns the jobs of
-    _finish."""
-    src = os.path.join(CSRC, "calls.cpp")
-    if not (force or _stale(LIB_CALLS, [src, os.path.join(INCLUDE, "pagedkv.h")])):
-        return []
+    _finish_calls."""
     import torch
+    src = os.path.join(CSRC, "calls.cpp")
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     lib = os.path.join(root, "lib")
-    tmp = LIB_CALLS + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DPKV_TORCH_VERSION="{torch.__version__}"',
            "-I", INCLUDE, "-I", os.path.join(root, "include"), "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
-           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), src, "-o", tmp, "-L", lib,
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), src, "-L", lib,
            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
-    return [(src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True), tmp)]
+    stamp = "\n".join(cmd)
+    if not (force or _stale(LIB_CALLS, [src, os.path.join(INCLUDE, "pagedkv.h")]) or _text(CALLS_STAMP) != stamp):
+        return []
+    tmp = LIB_CALLS + f".tmp{os.getpid()}"
+    pr = subprocess.Popen(cmd + ["-o", tmp], stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    return [(src, pr, tmp, stamp)]
+
+
+def _text(path: str) -> str | None:
+    if not os.path.exists(path):
+        return None
+    with open(path) as f:
+        return f.read()
 
 
 def _finish_calls(jobs):
-    for src, pr, tmp in jobs:
+    for src, pr, tmp, stamp in jobs:
         out, _ = pr.communicate()
         if pr.returncode != 0:
             raise RuntimeError(f"g++ failed:\n--- {src}\n{out}")
         os.replace(tmp, LIB_CALLS)
+        os.makedirs(BUILD, exist_ok=True)
+        with open(CALLS_STAMP, "w") as f:
+            f.write(stamp)
 
 
 def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True,

@@ -493,4 +493,18 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nul
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls(void) { return PyModule_Create(&module); }
+// Tensors are taken apart by torch's own headers, whose layouts another version
+// need not share: imported under the torch that it was compiled for, or not at all.
+PyMODINIT_FUNC PyInit__calls(void) {
+    PyObject *torch = PyImport_ImportModule("torch");
+    PyObject *version = torch ? PyObject_GetAttrString(torch, "__version__") : nullptr;
+    PyObject *text = version ? PyObject_Str(version) : nullptr;
+    const char *now = text ? PyUnicode_AsUTF8(text) : nullptr;
+    PyObject *made = nullptr;
+    if (now && std::string(now) == PKV_TORCH_VERSION) made = PyModule_Create(&module);
+    else if (now) PyErr_Format(PyExc_ImportError, "built for torch %s, this is %s", PKV_TORCH_VERSION, now);
+    Py_XDECREF(text);
+    Py_XDECREF(version);
+    Py_XDECREF(torch);
+    return made;
+}
