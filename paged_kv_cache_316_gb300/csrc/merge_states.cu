@@ -65,9 +65,11 @@ __global__ void __launch_bounds__(kMergeThreads) merge_states_kernel(const __gri
         for (int e = 0; e < 8; ++e) acc[e] *= keep;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const float w = fast_exp2((l[k] - base) * kLog2e);
-            total += w;
-            if (w != 0.f) {
+            // -1: nothing is seen.  (A weight that is 0 by underflow counts: a NaN
+            // in its part stays one in any order of the parts.)
+            const float w = l[k] == -INFINITY ? -1.f : fast_exp2((l[k] - base) * kLog2e);
+            if (!(w < 0.f)) {
+                total += w;
                 const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
