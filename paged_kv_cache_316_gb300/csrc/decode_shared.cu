@@ -175,10 +175,8 @@ __global__ void __launch_bounds__(ShCfg<NB>::THREADS, 1)
             [&](int, int, uint32_t first, uint32_t n) { return w0 >= first && w0 - first < n; }, at.x, bad);
         if (bad) W = 0;
         if (blockIdx.x == 0) {
-            if (bad && lane == 0) set_err(w.err, PKV_DEV_ERR_BATCH);
+            report_prefixes(w, bad);
             if (lane == 0) *w.per = per;
-            for (int g = lane; g < w.G && !bad; g += 32)
-                if (w.prefix_lens[g] < 0 || w.prefix_lens[g] > w.max_prefix) set_err(w.err, PKV_DEV_ERR_LEN);
         }
         if (lane == 0) steps_s = w0 < W ? static_cast<int>(min(per, W - w0)) : 0;
         if (w0 < W) {
@@ -775,7 +773,7 @@ extern "C" int paged_decode_shared(const void *query, const void *k_cache, const
     w.prefix_lens = prefix_lens;
     w.seq_lens = seq_lens;
     w.max_seq_len = max_seq_len;
-    w.G = pl.ctas > 0 ? num_groups : 0;
+    w.G = num_groups;
     w.B = batch_size;
     w.Q = q_len_per_req;
     w.Hqo = num_qo_heads;

@@ -661,6 +661,7 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const __grid_constant
     PrefixGroup x;
     bool bad;
     scan_prefixes(w, [](uint32_t) {}, [=](int lo, int hi, uint32_t, uint32_t) { return lo <= b && b < hi; }, x, bad);
+    if (w.ctas == 0 && at == 0) report_prefixes(w, bad);  // (max_prefix 0: no kernel over the prefixes does)
     const uint32_t own0 = own_part(p, b, kvh, 0, t * w.group);
     pdl_wait();
     const PrefixParts parts = prefix_parts(w, x, w.ctas > 0 ? *w.per : 1, token, kvh);

@@ -116,6 +116,14 @@ __device__ __forceinline__ void scan_prefixes(const PrefixWork &p, G total, F ma
     }
 }
 
+// What is wrong with the groups, into the error word, by one warp.
+__device__ __forceinline__ void report_prefixes(const PrefixWork &p, bool bad) {
+    const int lane = threadIdx.x & 31;
+    if (bad && lane == 0) set_err(p.err, PKV_DEV_ERR_BATCH);
+    for (int g = lane; g < p.G && !bad; g += 32)
+        if (p.prefix_lens[g] < 0 || p.prefix_lens[g] > p.max_prefix) set_err(p.err, PKV_DEV_ERR_LEN);
+}
+
 // Steps of a team, by one warp.  N CTAs take C + W / N steps' time each (C =
 // kShCtaSteps), and the other SMs stream own keys meanwhile, which cost one SM A
 // steps: both are done at the same time T, and S SMs busy until then, if
