@@ -12,8 +12,9 @@
 // F = round(2^64 frac(f / 2 pi)), and position * F mod 2^64 is the angle less
 // its whole turns without a rounding, so that an angle is as good at position
 // 10^9 as at 1 (with the double's 2^-53 of a turn a step: 2^-22 of a turn
-// there, where an fp32 product of position and frequency has lost all).  The
-// upper 32 bits feed sincospif.
+// there, where an fp32 product of position and frequency has lost all).  All 64
+// bits, rounded once to fp32, feed sincospif: the sine of a small angle is as
+// good in itself as that of a large one.
 //
 // Instruction issue bounds it before HBM does, so the work of an element is
 // brought down.  A lane holds both elements of its pairs, a and b (two pieces
@@ -100,7 +101,7 @@ __device__ __forceinline__ uint64_t turns_per_step(double f) {
 // (cos, sin) of position * step, times m.
 __device__ __forceinline__ float2 turned(int pos, uint64_t step, float m) {
     const uint64_t a = static_cast<uint64_t>(static_cast<int64_t>(pos)) * step;
-    const float half_turns = static_cast<float>(static_cast<int32_t>(a >> 32)) * 0x1p-31f;
+    const float half_turns = static_cast<float>(static_cast<int64_t>(a)) * 0x1p-63f;
     float s, c;
     sincospif(half_turns, &s, &c);
     return make_float2(c * m, s * m);
