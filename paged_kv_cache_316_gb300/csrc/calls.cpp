@@ -170,7 +170,7 @@ struct Rows {
         n = t.size(0);
         heads = t.size(1);
         dim = t.size(2);
-        stride = n > 1 ? t.stride(0) : std::max(t.stride(0), heads * dim);
+        stride = n > 1 ? t.stride(0) : heads * dim;  // (of one token any stride will do)
     }
 };
 
