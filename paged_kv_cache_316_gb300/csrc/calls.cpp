@@ -223,7 +223,6 @@ PyObject *guarded(F f) {
 struct Owned {
     PyObject *o;
     explicit Owned(PyObject *p) : o(p) {}
-    Owned(Owned &&x) noexcept : o(x.o) { x.o = nullptr; }
     Owned(const Owned &) = delete;
     Owned &operator=(const Owned &) = delete;
     ~Owned() { Py_XDECREF(o); }
@@ -414,20 +413,20 @@ PyObject *call_merge_states(PyObject *, PyObject *const *a, Py_ssize_t n) {
         arguments(n, 4);
         const Owned seq(PySequence_Fast(a[0], "states must be a sequence"));
         if (!seq.o) throw Raised();
-        const Py_ssize_t parts = PySequence_Fast_GET_SIZE(seq.o);
-        if (parts == 0) throw Refused("no states to merge");
-        std::vector<Owned> pairs;
-        pairs.reserve(parts);
-        std::vector<const Tensor *> outs, lses;
-        for (Py_ssize_t i = 0; i < parts; ++i) {
-            pairs.emplace_back(PySequence_Fast(PySequence_Fast_GET_ITEM(seq.o, i), "a state is an (out, lse) pair"));
-            PyObject *p = pairs.back().o;
+        // (references of this call's own: the lists are the caller's, and other
+        // threads run while the kernels are launched)
+        std::vector<Tensor> outs, lses;
+        for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(seq.o); ++i) {
+            const Owned pair(PySequence_Fast(PySequence_Fast_GET_ITEM(seq.o, i), "a state is an (out, lse) pair"));
+            PyObject *p = pair.o;
             if (!p) throw Raised();
             if (PySequence_Fast_GET_SIZE(p) != 2) throw Refused("a state is an (out, lse) pair");
-            outs.push_back(&tensor(PySequence_Fast_GET_ITEM(p, 0), "a state's output"));
-            lses.push_back(&tensor(PySequence_Fast_GET_ITEM(p, 1), "a state's log-sum-exp"));
+            outs.push_back(tensor(PySequence_Fast_GET_ITEM(p, 0), "a state's output"));
+            lses.push_back(tensor(PySequence_Fast_GET_ITEM(p, 1), "a state's log-sum-exp"));
         }
-        const Tensor &first = *outs[0];
+        const size_t parts = outs.size();
+        if (parts == 0) throw Refused("no states to merge");
+        const Tensor &first = outs[0];
         const int dtype = dtype_code(first);
         if (first.dim() != 3 || dtype < 0) throw Refused("a state's output is [rows, heads, head_dim] in fp16 or bf16");
         const auto rows = first.sizes().slice(0, 2);
@@ -438,19 +437,19 @@ PyObject *call_merge_states(PyObject *, PyObject *const *a, Py_ssize_t n) {
         dev.holds(lse);
         std::vector<const void *> o;
         std::vector<const float *> l;
-        for (Py_ssize_t i = 0; i < parts; ++i) {
-            if (outs[i]->sizes() != first.sizes() || outs[i]->scalar_type() != first.scalar_type() || !outs[i]->is_contiguous())
+        for (size_t i = 0; i < parts; ++i) {
+            if (outs[i].sizes() != first.sizes() || outs[i].scalar_type() != first.scalar_type() || !outs[i].is_contiguous())
                 throw Refused("outputs must be contiguous tensors of the same shape and type");
-            if (lses[i]->sizes() != rows || lses[i]->scalar_type() != at::kFloat || !lses[i]->is_contiguous())
+            if (lses[i].sizes() != rows || lses[i].scalar_type() != at::kFloat || !lses[i].is_contiguous())
                 throw Refused("log-sum-exps must be contiguous float32 [rows, heads]");
-            dev.holds(*outs[i]);
-            dev.holds(*lses[i]);
-            o.push_back(outs[i]->data_ptr());
-            l.push_back(static_cast<const float *>(lses[i]->data_ptr()));
+            dev.holds(outs[i]);
+            dev.holds(lses[i]);
+            o.push_back(outs[i].data_ptr());
+            l.push_back(static_cast<const float *>(lses[i].data_ptr()));
         }
         void *st = dev.stream(a[3]);
         check(unlocked([&] {
-            return g_merge_states(o.data(), l.data(), static_cast<int32_t>(std::min<Py_ssize_t>(parts, INT32_MAX)),
+            return g_merge_states(o.data(), l.data(), static_cast<int32_t>(std::min<size_t>(parts, INT32_MAX)),
                                   first.size(0) * first.size(1), static_cast<int32_t>(first.size(2)), dtype, address(out),
                                   static_cast<float *>(address(lse)), st);
         }));
