@@ -112,9 +112,9 @@ int pkv_debug_bounds(void);
 /*
  * pkv_set_wait_limit_ns -- time limit, in nanoseconds, of every bounded
  * pipeline wait (an mbarrier wait for copied data, for the tensor core or
- * for another warp of the CTA) in the kernels of paged_append and
- * paged_prefill launched after the call; 0 restores the default of one
- * second.  Returns the previous limit.  Process-wide (every thread and
+ * for another warp of the CTA) in the kernels of paged_append,
+ * paged_prefill and paged_decode_shared launched after the call; 0 restores
+ * the default of one second.  Returns the previous limit.  Process-wide (every thread and
  * device).  A wait that runs out sets PKV_DEV_ERR_TIMEOUT in the call's
  * error word; the CTA then stops its work, waits for the copies and MMAs
  * it had already issued, frees its tensor memory and exits, so the device

@@ -143,8 +143,9 @@ def kernel_launches() -> int:
 
 
 def set_wait_limit_ns(ns: int) -> int:
-    """Limit of the bounded pipeline waits of later append / prefill
-    launches (0: the default, one second); returns the previous limit."""
+    """Limit of the bounded pipeline waits of later append, prefill and
+    shared-decode launches (0: the default, one second); returns the previous
+    limit."""
     return int(load_library().pkv_set_wait_limit_ns(int(ns)))
 
 

@@ -6,7 +6,7 @@
 // These calls are made once per layer and step, on GPU work of a few
 // microseconds, so what a call costs on the host is what a small batch costs:
 // the same checks in Python and the conversion of 20 to 35 arguments by ctypes
-// took 16 to 31 us a call on a GB300's host, of which 8 to 14 remain.  binding.py holds
+// took 17 to 30 us a call on a GB300's host, of which 5 to 16 remain.  binding.py holds
 // the signatures and documentation and passes every argument by position.  The
 // C entry points are called through the addresses that it hands over when it
 // loads the library, so that a switch to another build of it is followed.

@@ -39,9 +39,9 @@
 // Times of the call replayed from a graph (floor of bytes at 6788 GB/s or
 // operations at 1912 TFLOP/s): 64 requests behind 8,192 keys, 64 to 1024 of
 // their own, 32 / 8 heads: 46 us (27); 45 requests of 4 tokens behind three
-// prefixes of up to 16,001, 28 / 4 heads, fp16: 42.5 (10); 256 behind 32,768,
+// prefixes of up to 14,309, 28 / 4 heads, fp16: 43 (10); 256 behind 32,768,
 // 64 / 8 heads: 219 (145), 206 of them the prefix on 120 SMs, own keys beside
-// it on 32; 4 behind 512: 10.4.
+// it on 32; 4 behind 512: 11.
 //
 // Roundings: P to the caches' 16-bit type for its product with V, the output
 // once at the end; scores, maxima, sums, O, the partials and the LSE are fp32.

@@ -33,10 +33,11 @@
 // shared memory (cp.async), on into the warp's next token.
 //
 // Times of the call replayed from a graph (a floor of bytes at 6788 GB/s):
-// 33k tokens of 1024 requests, 32 + 8 heads, norms: 256 us (floor 239); 26k
-// tokens, fp16, half of each head, neighbours: 70.5 (64); 8k rows of 32 + 32
-// heads of 192: 66 (58); 4096 tokens of a fused projection: 22.8 (14.8, and
-// 4 us of launch, first reads and tail); 64 tokens: 4.2, seven: 4.1.
+// 65,962 tokens of 1024 requests, 32 + 8 heads, norms: 255 us (floor 239);
+// 17,664 tokens, fp16, half of each head, neighbours: 70 (64); 8,039 rows of 32
+// + 32 heads of 192: 66.7 (58); 4096 tokens of a fused projection: 22 (14.8;
+// its 8,192 tasks on 2,432 warps are 3.4 rounds that take the time of 4, 2.8
+// us, and launch, first reads and tail are 4); 64 tokens: 4.6, seven: 3.7.
 // On the way: a row's partner by shuffles and loads of four rows, 490 us for
 // the first; rows through the ring one at a time, factors folded, 312; pairs in
 // one lane and sums of squares reduced four at a time, loads into registers,
@@ -377,8 +378,8 @@ static int run_rotary(RotaryParams &p, bool paired, cudaStream_t st) {
     p.batches[1] = (p.Hkv + heads - 1) / heads;
     p.batches[2] = p.src[2] ? p.batches[1] : 0;
     const int all = p.batches[0] + p.batches[1] + p.batches[2];
-    // A token's batches are divided among warps where there are fewer than two
-    // tokens to a warp that fits the machine.
+    // A token's batches are divided among warps where there are fewer than
+    // kRotRounds tokens to a warp that fits the machine.
     const int64_t warps = static_cast<int64_t>(num_sms()) * kRotCtas * kRotWarps;
     int64_t parts = (warps * kRotRounds + p.nnz - 1) / p.nnz;
     if (parts > all) parts = all;

@@ -20,13 +20,18 @@
 // to partials, so that no item waits for the prefix, and shared_merge_kernel
 // joins them with the prefix's.
 //
-// Alone on all SMs: 290 MB of 256 requests' 264 keys in 55 us (5.3 TB/s, 78% of
-// the copy rate), 149 MB of 64 requests' 544 in 33: the first tile comes after
+// Alone on all SMs: 278 MB of 256 requests' 265 keys in 55 us (5.1 TB/s, 74% of
+// the copy rate), 147 MB of 64 requests' 560 in 33: the first tile comes after
 // 4 us (length, page ids, data), the last items end unevenly, and an item's
-// claim takes 1 to 2 us.  Beside the prefix an SM streams 35 to 45 GB/s.
+// claim takes 1 to 2 us.  Beside the prefix an SM streams 35 to 45 GB/s.  Items
+// are cut for the caller's largest length: where it is far above the lengths,
+// splits are longer than they should be and empty items are claimed one by one
+// (64 requests' 560 keys beside a prefix of 8,192: 46 us for a largest of 1,019,
+// 55 for 32,768, 76 for 131,072).
 //
 // Every wait is bounded; a warp whose wait ran out says so in the barrier that
-// all four meet at next, so that they leave together.
+// all four meet at next, so that they leave together, and each of the two warps
+// that issue copies waits for its own to land.
 #pragma once
 
 #include "attn_tile.cuh"
